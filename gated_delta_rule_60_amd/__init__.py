@@ -10,6 +10,13 @@ kernels behind the C ABI of include/kda.h (libkda.so).
 ``import gated_delta_rule_60_amd`` does not load the library; the first call
 does, and raises if it has not been built.
 """
+from ._attn import (  # noqa: F401
+    attn_prefill,
+    attn_prefill_backward,
+    attn_prefill_backward_t,
+    attn_prefill_backward_workspace_size,
+    attn_prefill_t,
+)
 from ._lib import (  # noqa: F401
     KDA_DTYPE_BF16,
     KDA_DTYPE_F32,

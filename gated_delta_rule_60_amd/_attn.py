@@ -1,0 +1,131 @@
+"""Softmax attention over packed prompts and over a paged cache, and the
+cache's page operations: the binding of the ``attn_*`` and ``kv_*`` entry
+points of libkda.so (include/kda.h).
+
+As in ``_lib``: the functions named like the C symbols take raw device
+pointers and a stream handle; the ``*_t`` functions take torch tensors, check
+shapes, types and devices, allocate outputs, and call the C ABI on ``stream``
+(torch's current stream by default).  Every arithmetic step runs in the
+library's HIP kernels; there is no fallback of any kind.
+"""
+from __future__ import annotations
+
+import math
+
+from ._lib import _check, _dtype_code, _need, _stream_of, load
+
+
+# ---------------------------------------------------------------------------
+# C ABI, one to one
+# ---------------------------------------------------------------------------
+def attn_prefill(q, k, v, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_stride, k_stride, v_stride, scale, dtype,
+                 o, lse, stream) -> int:
+    return load().attn_prefill(q, k, v, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_stride, k_stride, v_stride,
+                               scale, dtype, o, lse, stream)
+
+
+def attn_prefill_backward(q, k, v, o, lse, d_o, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_stride, k_stride,
+                          v_stride, scale, dtype, d_q, d_k_out, d_v_out, workspace, workspace_bytes, stream) -> int:
+    return load().attn_prefill_backward(q, k, v, o, lse, d_o, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_stride,
+                                        k_stride, v_stride, scale, dtype, d_q, d_k_out, d_v_out, workspace,
+                                        workspace_bytes, stream)
+
+
+def attn_prefill_backward_workspace_size(T_tot, H_q) -> int:
+    return int(load().attn_prefill_backward_workspace_size(T_tot, H_q))
+
+
+# ---------------------------------------------------------------------------
+# torch conveniences (marshalling only)
+# ---------------------------------------------------------------------------
+def _tokens(t, name, shape, dtype, device) -> int:
+    """Check a [tokens, heads, size] tensor whose tokens are contiguous blocks;
+    returns the elements between tokens."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    n, h, d = shape
+    s = t.stride()
+    if n == 0:
+        return h * d
+    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous (strides {s})")
+    return int(s[0]) if n > 1 else max(h * d, 8)
+
+
+def attn_prefill_t(q, k, v, cu_seqlens=None, *, scale=None, o=None, lse=None, stream=None):
+    """Causal softmax attention over packed prompts; returns (o, lse).
+
+    q: [T, H_q, d_k]; k: [T, H_kv, d_k]; v: [T, H_kv, d_v] (bf16 or fp32, one
+    type; slices of a fused projection are taken as they are); cu_seqlens:
+    int32 [N + 1] on the device (None = one sequence); ``scale``: 1 / sqrt(d_k)
+    if None.  o: [T, H_q, d_v] in q's dtype; lse: [T, H_q] fp32."""
+    import torch
+    if not q.is_cuda:
+        raise ValueError("attention runs on a GPU device; q is on the CPU")
+    dev = q.device
+    st = _stream_of(stream, dev)
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        T, Hq, dk = (int(x) for x in q.shape)
+        Hkv, dv = int(k.shape[1]), int(v.shape[2])
+        code = _dtype_code(q)
+        if cu_seqlens is None:
+            cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
+        N = int(cu_seqlens.shape[0]) - 1
+        qs = _tokens(q, "q", (T, Hq, dk), q.dtype, dev)
+        ks = _tokens(k, "k", (T, Hkv, dk), q.dtype, dev)
+        vs = _tokens(v, "v", (T, Hkv, dv), q.dtype, dev)
+        _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
+        if o is None:
+            o = torch.empty((T, Hq, dv), dtype=q.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        _need(o, "o", (T, Hq, dv), q.dtype, dev)
+        _need(lse, "lse", (T, Hq), torch.float32, dev)
+        _check(attn_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), N, T, Hq, Hkv, dk, dv,
+                            qs, ks, vs, 1.0 / math.sqrt(dk) if scale is None else float(scale), code, o.data_ptr(),
+                            lse.data_ptr(), int(st.cuda_stream)))
+    return o, lse
+
+
+def attn_prefill_backward_t(q, k, v, o, lse, d_o, cu_seqlens=None, *, scale=None, workspace=None, stream=None):
+    """Backward of ``attn_prefill_t``: gradients (d_q, d_k, d_v), shaped and
+    typed like q, k and v, of a loss given d_o = dL/do and the forward's o and
+    lse.  ``workspace``: optional uint8 device tensor of at least
+    ``attn_prefill_backward_workspace_size(T, H_q)`` bytes."""
+    import torch
+    if not q.is_cuda:
+        raise ValueError("attention runs on a GPU device; q is on the CPU")
+    dev = q.device
+    st = _stream_of(stream, dev)
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        T, Hq, dk = (int(x) for x in q.shape)
+        Hkv, dv = int(k.shape[1]), int(v.shape[2])
+        code = _dtype_code(q)
+        if cu_seqlens is None:
+            cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
+        N = int(cu_seqlens.shape[0]) - 1
+        qs = _tokens(q, "q", (T, Hq, dk), q.dtype, dev)
+        ks = _tokens(k, "k", (T, Hkv, dk), q.dtype, dev)
+        vs = _tokens(v, "v", (T, Hkv, dv), q.dtype, dev)
+        _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
+        _need(o, "o", (T, Hq, dv), q.dtype, dev)
+        _need(lse, "lse", (T, Hq), torch.float32, dev)
+        _need(d_o, "d_o", (T, Hq, dv), q.dtype, dev)
+        d_q = torch.empty((T, Hq, dk), dtype=q.dtype, device=dev)
+        d_k = torch.empty((T, Hkv, dk), dtype=q.dtype, device=dev)
+        d_v = torch.empty((T, Hkv, dv), dtype=q.dtype, device=dev)
+        ws = attn_prefill_backward_workspace_size(T, Hq)
+        if workspace is None:
+            workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
+        elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+        _check(attn_prefill_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                     d_o.data_ptr(), cu_seqlens.data_ptr(), N, T, Hq, Hkv, dk, dv, qs, ks, vs,
+                                     1.0 / math.sqrt(dk) if scale is None else float(scale), code, d_q.data_ptr(),
+                                     d_k.data_ptr(), d_v.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                     int(st.cuda_stream)))
+    return d_q, d_k, d_v

@@ -64,6 +64,12 @@ SIGNATURES = {
                                             _vp, _sz, _vp]),
     "kda_prefill_noalloc": (ctypes.c_int, [_vp, _vp, _vp, _fp, _fp, _fp, _ip, _i32, _i64, _i32, _i32, _i32,
                                            ctypes.c_int, _vp, _fp, _vp]),
+    "attn_prefill": (ctypes.c_int, [_vp, _vp, _vp, _ip, _i32, _i64, _i32, _i32, _i32, _i32, _i64, _i64, _i64,
+                                    ctypes.c_float, ctypes.c_int, _vp, _fp, _vp]),
+    "attn_prefill_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _fp, _vp, _ip, _i32, _i64, _i32, _i32, _i32, _i32,
+                                             _i64, _i64, _i64, ctypes.c_float, ctypes.c_int, _vp, _vp, _vp, _vp, _sz,
+                                             _vp]),
+    "attn_prefill_backward_workspace_size": (_sz, [_i64, _i32]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_last_error": (ctypes.c_char_p, []),
     "kda_version": (_i32, []),

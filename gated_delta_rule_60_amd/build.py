@@ -15,7 +15,8 @@ _ROOT = os.path.dirname(_HERE)
 _CSRC = os.path.join(_HERE, "csrc")
 
 SOURCES = ["kda_api.cpp", "kda_prefill.hip", "kda_segment.hip", "kda_decode.hip", "kda_backward.hip",
-           "kda_bwd_chunk.hip", "kda_noalloc.hip", "kda_anymap.hip"]
+           "kda_bwd_chunk.hip", "kda_noalloc.hip", "kda_anymap.hip", "attn_api.cpp", "attn_prefill.hip",
+           "attn_backward.hip"]
 ARCH = "gfx950"
 
 

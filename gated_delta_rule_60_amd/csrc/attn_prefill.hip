@@ -1,0 +1,199 @@
+// attn_prefill.hip -- causal softmax attention over packed prompts, gfx950.
+//
+// For row i of a sequence and query head h (key head g = h / (Hq / Hkv)):
+//     s_ij = scale q_i . k_j (j <= i),  lse_i = ln sum_j exp(s_ij),
+//     o_i = sum_j exp(s_ij - lse_i) v_j.
+// One pass over the keys: with m the running maximum, l = sum exp(s - m) and
+// O = sum exp(s - m) v_j, a new tile adds to l and O, and both are rescaled
+// only when m rises.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "attn_device.hpp"
+#include "attn_launch.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kBM = 32 * kWaves;  // query rows of a workgroup
+// The running maximum is moved (and O, l rescaled) only when a row's scores
+// exceed it by more than this many powers of two: p then stays below 2^8,
+// where bf16 and fp32 hold it as exactly as below 1.
+constexpr float kLazyLog2 = 8.f;
+
+}  // namespace
+
+template <bool BF16, int DK, int DV>
+__global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a, float c /* scale log2(e) */) {
+    using Op = AttnOp<BF16>;
+    using KT = AttnTile<BF16, DK>;
+    using VT = AttnTile<BF16, DV>;
+    using G = typename Op::G;
+    constexpr int BN = Op::BN, NS = BN / 32;
+    constexpr int KB = BN * KT::ROWB, VB = BN * VT::ROWB;
+    __shared__ __attribute__((aligned(1024))) char lds[2][KB + VB];
+
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // consecutive workgroups take consecutive key heads: a key head's workgroups share an XCD's
+    // L2 when Hkv is a multiple of the 8 XCDs they are dealt to
+    const int hp = blockIdx.x % a.Hq;
+    const int group = a.Hq / a.Hkv;
+    const int g = hp % a.Hkv, h = g * group + hp / a.Hkv;
+    SeqTile st;
+    if (!find_tile<kBM>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hq, false, st)) return;
+
+    const int row0 = st.tile * kBM;
+    const int qi = row0 + 32 * wave + (lane & 31);  // the lane's query row in its sequence
+    const bool live = qi < st.len;
+    const size_t tok = static_cast<size_t>(st.beg) + (live ? qi : 0);
+
+    typename Op::Row q[KT::NF];
+    load_row_frags<BF16, DK>(q, static_cast<const G*>(a.q) + tok * a.q_stride + static_cast<size_t>(h) * DK, half, live);
+
+    const int ks = a.k_stride * Op::ES, vs = a.v_stride * Op::ES;
+    const char* kb = static_cast<const char*>(a.k) + (static_cast<size_t>(st.beg) * a.k_stride + static_cast<size_t>(g) * DK) * Op::ES;
+    const char* vb = static_cast<const char*>(a.v) + (static_cast<size_t>(st.beg) * a.v_stride + static_cast<size_t>(g) * DV) * Op::ES;
+    const auto ksrc = KT::template src<kWaves>(wave, lane, ks);
+    const auto vsrc = VT::template src<kWaves>(wave, lane, vs);
+    const int kat = KT::row_at(lane);
+    const auto vat = VT::col_at(lane);
+
+    const int last = st.len < row0 + kBM ? st.len : row0 + kBM;
+    const int tiles = (last + BN - 1) / BN;
+    const int wrow = row0 + 32 * wave;               // the wave's first row
+    const int wtiles = wrow < st.len ? (wrow + 31) / BN + 1 : 0;  // tiles it needs
+
+    auto stage_tile = [&](int t) __attribute__((always_inline)) {
+        char* b = lds[t & 1];
+        KT::template stage<kWaves, BN>(b, kb + static_cast<size_t>(t) * BN * ks, st.len - t * BN, ks, ksrc, wave);
+        VT::template stage<kWaves, BN>(b + KB, vb + static_cast<size_t>(t) * BN * vs, st.len - t * BN, vs, vsrc, wave);
+    };
+
+    f32x16_t o[VT::ND];
+#pragma unroll
+    for (int dt = 0; dt < VT::ND; ++dt) o[dt] = f32x16_t{};
+    float mc = -INFINITY;  // running maximum of c s
+    float l = 0.f;         // this half-wave's part of the row's sum
+
+    // One tile into the row's statistics and O.  LAST: the wave's last tile, which holds the
+    // diagonal; a step of its own keeps the masks out of the loop over the others.
+    auto step = [&](int t, auto LAST) __attribute__((always_inline)) {
+        const char* kt = lds[t & 1];
+        const char* vt = kt + KB;
+        f32x16_t s[NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) s[n] = KT::rows_times(f32x16_t{}, kt, kat, 32 * n, q);
+        if constexpr (LAST) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = t * BN + 32 * n + 8 * (i >> 2) + 4 * half + (i & 3);
+                    s[n][i] = key <= qi ? s[n][i] : -INFINITY;
+                }
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[n][i]);
+        mx = half_max(mx) * c;
+        if (__any(mx > mc + kLazyLog2)) {
+            // by row: what a row gives does not depend on the rows beside it
+            const float m1 = mx > mc + kLazyLog2 ? mx : mc;
+            const float r = exp2f(mc - m1);
+            mc = m1;
+            l *= r;
+#pragma unroll
+            for (int dt = 0; dt < VT::ND; ++dt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[dt][i] *= r;
+        }
+        ColOp<BF16> p[NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], c, -mc));
+                l += s[n][i];
+            }
+            p[n].set(s[n]);
+        }
+        // a weight of zero does not keep out an infinity or NaN behind the mask
+        if (LAST && VT::template any_nonfinite<BN>(vt, lane)) {
+#pragma unroll
+            for (int dt = 0; dt < VT::ND; ++dt)
+#pragma unroll
+                for (int n = 0; n < NS; ++n) o[dt] = VT::template cols_times<true>(o[dt], vt, vat, 32 * n, dt, p[n]);
+            for (int j = 0; j < BN; ++j) VT::add_nonfinite(o, vt, j, half, t * BN + j <= qi);
+        } else {
+#pragma unroll
+            for (int dt = 0; dt < VT::ND; ++dt)
+#pragma unroll
+                for (int n = 0; n < NS; ++n) o[dt] = VT::cols_times(o[dt], vt, vat, 32 * n, dt, p[n]);
+        }
+    };
+
+    // every wave passes every tile's barrier; each works on its own tiles
+    auto next = [&](int t) __attribute__((always_inline)) {
+        lds_ready();
+        if (t + 1 < tiles) stage_tile(t + 1);
+    };
+    stage_tile(0);
+    int t = 0;
+    for (; t < wtiles - 1; ++t) {
+        next(t);
+        step(t, std::false_type{});
+    }
+    if (t < wtiles) {
+        next(t);
+        step(t, std::true_type{});
+        ++t;
+    }
+    for (; t < tiles; ++t) next(t);
+
+    l = half_sum(l);
+    if (live && half == 0) a.lse[tok * a.Hq + h] = (mc + log2f(l)) * kLn2;
+    store_col_as_row<BF16, DV>(static_cast<G*>(a.o) + (tok * a.Hq + h) * DV, o, 1.f / l, half, live);
+}
+
+namespace {
+
+template <bool BF16, int DK, int DV>
+hipError_t launch(const AttnArgs& a) {
+    const int64_t units = (static_cast<int64_t>(a.T_tot) + kBM - 1) / kBM + a.N;
+    hipLaunchKernelGGL((attn_prefill_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hq)), dim3(64 * kWaves), 0,
+                       static_cast<hipStream_t>(a.stream), a, a.scale * kLog2e);
+    return hipGetLastError();
+}
+
+template <bool BF16, int DK>
+hipError_t launch_dv(const AttnArgs& a) {
+    switch (a.d_v) {
+        case 32: return launch<BF16, DK, 32>(a);
+        case 64: return launch<BF16, DK, 64>(a);
+        default: return launch<BF16, DK, 128>(a);
+    }
+}
+
+template <bool BF16>
+hipError_t launch_dk(const AttnArgs& a) {
+    switch (a.d_k) {
+        case 32: return launch_dv<BF16, 32>(a);
+        case 64: return launch_dv<BF16, 64>(a);
+        default: return launch_dv<BF16, 128>(a);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_attn_prefill(const AttnArgs& a) {
+    if (a.T_tot == 0) return hipSuccess;
+    return a.bf16 ? launch_dk<true>(a) : launch_dk<false>(a);
+}
+
+}  // namespace kda

@@ -398,6 +398,78 @@ kda_status kda_prefill_noalloc(const void* q, const void* k, const void* v,
                                int32_t d_k, int32_t d_v, kda_dtype dtype, void* o, float* S_T,
                                void* stream);
 
+/*
+ * Softmax attention.  The layers of a hybrid model that are not delta
+ * attention attend to every earlier token; like the rest of the library
+ * these entry points apply no position encoding.  Query heads come in groups
+ * that share a key/value head: query head h reads key head h / (H_q / H_kv).
+ *
+ * attn_prefill -- causal attention over a packed batch of whole prompts.
+ * For row i of a sequence and query head h with key head g:
+ *
+ *     s_ij = scale * q_i . k_j  (j <= i, same sequence)
+ *     lse_i = ln sum_j exp(s_ij),   o_i = sum_j exp(s_ij - lse_i) v_j
+ *
+ *   q          device [T_tot, H_q, d_k]   dtype   queries
+ *   k          device [T_tot, H_kv, d_k]  dtype   keys
+ *   v          device [T_tot, H_kv, d_v]  dtype   values
+ *   cu_seqlens device [N + 1]             int32   sequence offsets, as for
+ *              kda_prefill; cu[N] may be less than T_tot.  Offsets outside
+ *              [0, T_tot] are clamped to it.
+ *   N, T_tot   >= 1, in [0, 2^30]
+ *   H_q, H_kv  H_q a multiple of H_kv, at most 4096
+ *   d_k, d_v   each one of 32, 64, 128
+ *   q_stride, k_stride, v_stride   elements from one token to the next (the
+ *              heads of a token are contiguous): at least H * d, a multiple
+ *              of 16 bytes, at most 2^22.  Slices of one fused projection
+ *              need no copy.
+ *   scale      positive and finite
+ *   dtype      storage type of q, k, v and o.  Sums and softmax statistics
+ *              are fp32; for bf16 the weights exp(s - max) are rounded to
+ *              bf16 before they meet v.
+ *   o          device [T_tot, H_q, d_v]   dtype   outputs (written, contiguous)
+ *   lse        device [T_tot, H_q]        float32 row statistics (written);
+ *              NULL if not wanted.  The backward pass needs it.
+ * Rows of o and lse at or past cu[N] are not written.  A non-finite value in
+ * a token's k or v reaches the rows of that token and the later ones of its
+ * sequence only.
+ */
+kda_status attn_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
+                        int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k,
+                        int32_t d_v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                        float scale, kda_dtype dtype, void* o, float* lse, void* stream);
+
+/*
+ * attn_prefill_backward -- gradients of attn_prefill with respect to q, k
+ * and v, given d_o = dL/do ([T_tot, H_q, d_v], dtype, contiguous) and the
+ * forward's o and lse.  With p_ij = exp(s_ij - lse_i):
+ *
+ *     D_i = d_o_i . o_i,   ds_ij = p_ij (d_o_i . v_j - D_i)
+ *     d_q_i = scale sum_j ds_ij k_j
+ *     d_k_j = scale sum ds_ij q_i,  d_v_j = sum p_ij d_o_i   (over rows i >= j
+ *                                   of every query head of the key head)
+ *
+ *   d_q [T_tot, H_q, d_k], d_k_out [T_tot, H_kv, d_k], d_v_out [T_tot, H_kv,
+ *   d_v]: dtype, written, contiguous.  Sums are fp32; for bf16 p and ds are
+ *   rounded to bf16 before the products that sum them.
+ *   workspace  at least attn_prefill_backward_workspace_size bytes (two
+ *   floats per row and head), 256-byte aligned, used until the queued work
+ *   ends.
+ * Rows at or past cu[N] are not written.  Each gradient is summed in one
+ * order: the same inputs give the same bits.  A non-finite input may reach
+ * every gradient of its own sequence.
+ */
+kda_status attn_prefill_backward(const void* q, const void* k, const void* v, const void* o,
+                                 const float* lse, const void* d_o, const int32_t* cu_seqlens,
+                                 int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k,
+                                 int32_t d_v, int64_t q_stride, int64_t k_stride,
+                                 int64_t v_stride, float scale, kda_dtype dtype, void* d_q,
+                                 void* d_k_out, void* d_v_out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_prefill_backward needs (0 for unsupported sizes). */
+size_t attn_prefill_backward_workspace_size(int64_t T_tot, int32_t H_q);
+
 /* Static text for a status code. */
 const char* kda_status_string(kda_status status);
 

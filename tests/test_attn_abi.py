@@ -1,0 +1,126 @@
+"""The attention and cache entry points on the CPU: every symbol declared in
+include/kda.h is exported and bound, and every refusal comes before any HIP
+call (no kernel is launched here)."""
+import os
+import re
+
+import pytest
+
+import gated_delta_rule_60_amd as kda
+from gated_delta_rule_60_amd import _lib
+
+_ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 0x10000  # 256-byte aligned, never dereferenced: validation fails first
+BF16, F32 = kda.KDA_DTYPE_BF16, kda.KDA_DTYPE_F32
+BAD, NOT = kda.KDA_ERR_INVALID_ARG, kda.KDA_ERR_UNSUPPORTED
+
+
+def test_every_declared_symbol_is_exported_and_bound():
+    text = open(os.path.join(_ROOT, "include", "kda.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = sorted(set(re.findall(r"\b((?:attn|kv)_[a-z_]+)\s*\(", text)))
+    assert "attn_prefill" in names and "attn_prefill_backward" in names
+    lib = kda.load()
+    for name in names:
+        assert hasattr(lib, name), f"{name} declared in kda.h but not exported"
+        assert name in _lib.SIGNATURES, f"{name} has no signature in _lib.py"
+        assert hasattr(kda, name), f"{name} has no binding"
+
+
+def _prefill(**kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, cu_seqlens=FAKE, N=1, T_tot=64, H_q=4, H_kv=2, d_k=64, d_v=32, q_stride=256,
+             k_stride=128, v_stride=64, scale=0.125, dtype=BF16, o=FAKE, lse=FAKE, stream=None)
+    a.update(kw)
+    return kda.attn_prefill(**a)
+
+
+def _backward(**kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, o=FAKE, lse=FAKE, d_o=FAKE, cu_seqlens=FAKE, N=1, T_tot=64, H_q=4, H_kv=2,
+             d_k=64, d_v=32, q_stride=256, k_stride=128, v_stride=64, scale=0.125, dtype=BF16, d_q=FAKE,
+             d_k_out=FAKE, d_v_out=FAKE, workspace=FAKE, workspace_bytes=1 << 40, stream=None)
+    a.update(kw)
+    return kda.attn_prefill_backward(**a)
+
+
+COMMON = [
+    (dict(N=0), BAD, "N >= 1"),
+    (dict(T_tot=-1), BAD, "T_tot"),
+    (dict(T_tot=(1 << 30) + 1), BAD, "2^30"),
+    (dict(H_q=3), BAD, "multiple of H_kv"),
+    (dict(H_kv=0), BAD, "multiple of H_kv"),
+    (dict(H_q=0), BAD, "multiple of H_kv"),
+    (dict(H_q=4098, q_stride=4098 * 64), BAD, "4096"),
+    (dict(d_k=48), NOT, "d_k and d_v"),
+    (dict(d_v=256), NOT, "d_k and d_v"),
+    (dict(dtype=2), NOT, "dtype"),
+    (dict(q_stride=248), BAD, "q_stride"),
+    (dict(k_stride=132), BAD, "k_stride"),
+    (dict(v_stride=(1 << 22) + 8), BAD, "v_stride"),
+    (dict(scale=0.0), BAD, "scale"),
+    (dict(scale=-1.0), BAD, "scale"),
+    (dict(scale=float("inf")), BAD, "scale"),
+    (dict(scale=float("nan")), BAD, "scale"),
+    (dict(q=None), BAD, "must not be NULL"),
+    (dict(v=None), BAD, "must not be NULL"),
+    (dict(o=None), BAD, "must not be NULL"),
+    (dict(cu_seqlens=None), BAD, "cu_seqlens"),
+    (dict(k=FAKE + 8), BAD, "16-byte aligned"),
+    (dict(lse=FAKE + 2), BAD, "4-byte aligned"),
+    (dict(T_tot=1 << 30, H_q=2048, q_stride=2048 * 64), BAD, "too large"),
+]
+
+
+@pytest.mark.parametrize("kw,status,needle", COMMON)
+def test_prefill_refuses(kw, status, needle):
+    assert _prefill(**kw) == status
+    assert needle in kda.kda_last_error()
+
+
+@pytest.mark.parametrize("kw,status,needle", COMMON + [
+    (dict(lse=None), BAD, "lse"),
+    (dict(d_o=None), BAD, "d_o"),
+    (dict(d_k_out=None), BAD, "must not be NULL"),
+    (dict(d_v_out=FAKE + 8), BAD, "16-byte aligned"),
+    (dict(workspace=None), BAD, "workspace must not be NULL"),
+    (dict(workspace=FAKE + 16), BAD, "256-byte aligned"),
+    (dict(workspace_bytes=64 * 4 * 8 - 1), BAD, "workspace smaller"),
+])
+def test_backward_refuses(kw, status, needle):
+    assert _backward(**kw) == status
+    assert needle in kda.kda_last_error()
+
+
+def test_nothing_to_do_is_done():
+    assert _prefill(T_tot=0, q=None, k=None, v=None, o=None, lse=None) == kda.KDA_OK
+    assert kda.kda_last_error() == ""
+    assert _backward(T_tot=0, q=None, k=None, v=None, o=None, lse=None, d_o=None, d_q=None, d_k_out=None, d_v_out=None,
+                     workspace=None, workspace_bytes=0) == kda.KDA_OK
+
+
+def test_torch_helpers_refuse_cpu_tensors():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 2, 32)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.attn_prefill_t(x, x, x)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.attn_prefill_backward_t(x, x, x, x, x[..., 0], x)
+
+
+@pytest.mark.parametrize("shape,stride,want", [
+    ((5, 2, 32), (64, 32, 1), 64),
+    ((5, 2, 32), (200, 32, 1), 200),       # a slice of a wider projection
+    ((1, 2, 32), (7, 32, 1), 64),          # one token: its stride says nothing
+    ((5, 1, 32), (96, 5, 1), 96),          # one head: nor does the heads'
+    ((0, 2, 32), (1, 1, 1), 64),
+    ((5, 2, 32), (64, 1, 2), None),        # heads last
+    ((5, 2, 32), (32, 160, 1), None),      # heads first
+])
+def test_token_strides(shape, stride, want):
+    torch = pytest.importorskip("torch")
+    from gated_delta_rule_60_amd import _attn
+    t = torch.as_strided(torch.zeros(2000), shape, stride)
+    if want is None:
+        with pytest.raises(ValueError, match="contiguous"):
+            _attn._tokens(t, "q", shape, t.dtype, t.device)
+    else:
+        assert _attn._tokens(t, "q", shape, t.dtype, t.device) == want
