@@ -16,6 +16,10 @@ from ._attn import (  # noqa: F401
     attn_prefill_backward_t,
     attn_prefill_backward_workspace_size,
     attn_prefill_t,
+    attn_tree_decode,
+    attn_tree_decode_t,
+    attn_tree_decode_workspace_size,
+    attn_tree_masks,
 )
 from ._lib import (  # noqa: F401
     KDA_DTYPE_BF16,

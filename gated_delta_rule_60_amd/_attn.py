@@ -35,6 +35,17 @@ def attn_prefill_backward_workspace_size(T_tot, H_q) -> int:
     return int(load().attn_prefill_backward_workspace_size(T_tot, H_q))
 
 
+def attn_tree_decode(q, k_cache, v_cache, block_table, ctx_lens, cu_q, tree_mask, N, T_q, H_q, H_kv, d_k, d_v, n_pages,
+                     page_size, max_pages, q_stride, scale, dtype, o, lse, workspace, workspace_bytes, stream) -> int:
+    return load().attn_tree_decode(q, k_cache, v_cache, block_table, ctx_lens, cu_q, tree_mask, N, T_q, H_q, H_kv, d_k,
+                                   d_v, n_pages, page_size, max_pages, q_stride, scale, dtype, o, lse, workspace,
+                                   workspace_bytes, stream)
+
+
+def attn_tree_decode_workspace_size(N, T_q, H_q, H_kv, d_v, page_size, max_pages) -> int:
+    return int(load().attn_tree_decode_workspace_size(N, T_q, H_q, H_kv, d_v, page_size, max_pages))
+
+
 # ---------------------------------------------------------------------------
 # torch conveniences (marshalling only)
 # ---------------------------------------------------------------------------
@@ -129,3 +140,85 @@ def attn_prefill_backward_t(q, k, v, o, lse, d_o, cu_seqlens=None, *, scale=None
                                      d_k.data_ptr(), d_v.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                      int(st.cuda_stream)))
     return d_q, d_k, d_v
+
+
+def attn_tree_masks(parents):
+    """The masks of drafted trees: ``parents`` is one list per sequence with
+    every token's parent (an earlier token's number in the sequence, or -1 at
+    the root); a token sees its ancestors and itself.  Returns an int64 tensor
+    [tokens] on the host (bit j: drafted position j), for ``attn_tree_decode_t``."""
+    import torch
+    masks = []
+    for tree in parents:
+        if len(tree) > 64:
+            raise ValueError(f"a drafted tree holds at most 64 tokens, got {len(tree)}")
+        seen = []
+        for j, p in enumerate(tree):
+            if not -1 <= p < j:
+                raise ValueError(f"the parent of token {j} must be an earlier token or -1, got {p}")
+            seen.append((1 << j) | (seen[p] if p >= 0 else 0))
+        masks += [m - (1 << 64) if m >> 63 else m for m in seen]
+    return torch.tensor(masks, dtype=torch.int64)
+
+
+def _cache_shape(k_cache, v_cache, dtype, device):
+    if k_cache.dim() != 4 or v_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [n_pages, page_size, H_kv, d]")
+    P, ps, Hkv, dk = (int(x) for x in k_cache.shape)
+    dv = int(v_cache.shape[3])
+    _need(k_cache, "k_cache", (P, ps, Hkv, dk), dtype, device)
+    _need(v_cache, "v_cache", (P, ps, Hkv, dv), dtype, device)
+    return P, ps, Hkv, dk, dv
+
+
+def attn_tree_decode_t(q, k_cache, v_cache, block_table, ctx_lens, cu_q=None, tree_mask=None, *, scale=None, o=None,
+                       lse=None, workspace=None, stream=None):
+    """Attention of drafted tokens over a paged cache; returns (o, lse).
+
+    q: [T, H_q, d_k]; k_cache: [n_pages, page_size, H_kv, d_k] and v_cache:
+    [n_pages, page_size, H_kv, d_v] of q's dtype, which already hold the
+    drafted tokens' keys and values behind ctx_lens (``kv_append_t``);
+    block_table: int32 [N, max_pages]; ctx_lens: int32 [N]; cu_q: int32
+    [N + 1] (None: one token per sequence); tree_mask: int64 [T], bit j of a
+    token's mask set if it sees drafted position j (None: the ones up to
+    itself; ``attn_tree_masks`` builds it).  ``workspace``: optional uint8
+    device tensor of ``attn_tree_decode_workspace_size`` bytes."""
+    import torch
+    if not q.is_cuda:
+        raise ValueError("attention runs on a GPU device; q is on the CPU")
+    dev = q.device
+    st = _stream_of(stream, dev)
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        T, Hq, dk = (int(x) for x in q.shape)
+        code = _dtype_code(q)
+        P, ps, Hkv, _, dv = _cache_shape(k_cache, v_cache, q.dtype, dev)
+        _need(k_cache, "k_cache", (P, ps, Hkv, dk), q.dtype, dev)
+        N = int(ctx_lens.shape[0])
+        if cu_q is None:
+            if T != N:
+                raise ValueError(f"without cu_q there is one token per sequence: {T} tokens, {N} sequences")
+            cu_q = torch.arange(N + 1, dtype=torch.int32, device=dev)
+        MP = int(block_table.shape[1])
+        qs = _tokens(q, "q", (T, Hq, dk), q.dtype, dev)
+        _need(block_table, "block_table", (N, MP), torch.int32, dev)
+        _need(ctx_lens, "ctx_lens", (N,), torch.int32, dev)
+        _need(cu_q, "cu_q", (N + 1,), torch.int32, dev)
+        if tree_mask is not None:
+            _need(tree_mask, "tree_mask", (T,), torch.int64, dev)
+        if o is None:
+            o = torch.empty((T, Hq, dv), dtype=q.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        _need(o, "o", (T, Hq, dv), q.dtype, dev)
+        _need(lse, "lse", (T, Hq), torch.float32, dev)
+        if workspace is None:
+            ws = attn_tree_decode_workspace_size(N, T, Hq, Hkv, dv, ps, MP)
+            workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
+        elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+        _check(attn_tree_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                ctx_lens.data_ptr(), cu_q.data_ptr(),
+                                tree_mask.data_ptr() if tree_mask is not None else None, N, T, Hq, Hkv, dk, dv, P, ps,
+                                MP, qs, 1.0 / math.sqrt(dk) if scale is None else float(scale), code, o.data_ptr(),
+                                lse.data_ptr(), workspace.data_ptr(), workspace.numel(), int(st.cuda_stream)))
+    return o, lse

@@ -70,6 +70,9 @@ SIGNATURES = {
                                              _i64, _i64, _i64, ctypes.c_float, ctypes.c_int, _vp, _vp, _vp, _vp, _sz,
                                              _vp]),
     "attn_prefill_backward_workspace_size": (_sz, [_i64, _i32]),
+    "attn_tree_decode": (ctypes.c_int, [_vp, _vp, _vp, _ip, _ip, _ip, _vp, _i32, _i64, _i32, _i32, _i32, _i32, _i32,
+                                        _i32, _i32, _i64, ctypes.c_float, ctypes.c_int, _vp, _fp, _vp, _sz, _vp]),
+    "attn_tree_decode_workspace_size": (_sz, [_i32, _i64, _i32, _i32, _i32, _i32, _i32]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_last_error": (ctypes.c_char_p, []),
     "kda_version": (_i32, []),

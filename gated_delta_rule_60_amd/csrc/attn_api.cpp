@@ -127,3 +127,75 @@ kda_status attn_prefill_backward(const void* q, const void* k, const void* v, co
 }
 
 }  // extern "C"
+
+namespace {
+
+bool pow2(int32_t x) { return x > 0 && (x & (x - 1)) == 0; }
+
+// The cache's shape, common to every entry point that reads or writes it.
+kda_status check_cache(int32_t n_pages, int32_t page_size, int32_t max_pages) {
+    if (!pow2(page_size) || page_size > 4096)
+        return fail(KDA_ERR_INVALID_ARG, "page_size must be a power of two, at most 4096");
+    if (n_pages < 1 || static_cast<int64_t>(n_pages) * page_size > INT32_MAX)
+        return fail(KDA_ERR_INVALID_ARG, "need n_pages >= 1 and fewer than 2^31 positions in the cache");
+    if (max_pages < 1 || static_cast<int64_t>(max_pages) * page_size > (int64_t{1} << 30))
+        return fail(KDA_ERR_INVALID_ARG, "need max_pages >= 1 and at most 2^30 positions in a sequence");
+    return KDA_OK;
+}
+
+// Row tiles times key blocks must stay countable in 32 bits.
+bool tree_countable(const kda::TreePlan& p, int32_t max_pages, int32_t page_size, int32_t H_kv) {
+    const int64_t blocks = static_cast<int64_t>(max_pages) * page_size / 128 + 1;
+    return p.tiles <= INT32_MAX / blocks && (p.items + p.tiles) * H_kv <= INT32_MAX;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_tree_decode_workspace_size(int32_t N, int64_t T_q, int32_t H_q, int32_t H_kv, int32_t d_v, int32_t page_size,
+                                       int32_t max_pages) {
+    if (N < 1 || T_q < 0 || T_q > (int64_t{1} << 24) || H_kv < 1 || H_q < 1 || H_q > 4096 || H_q % H_kv != 0 ||
+        !supported_dim(d_v) || !pow2(page_size) || page_size > 4096 || max_pages < 1 ||
+        static_cast<int64_t>(max_pages) * page_size > (int64_t{1} << 30))
+        return 0;
+    return kda::tree_plan(N, T_q, H_q, H_kv, d_v, static_cast<int64_t>(max_pages) * page_size, kda::device_cus_or_default()).bytes;
+}
+
+kda_status attn_tree_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                            const int32_t* ctx_lens, const int32_t* cu_q, const uint64_t* tree_mask, int32_t N, int64_t T_q,
+                            int32_t H_q, int32_t H_kv, int32_t d_k, int32_t d_v, int32_t n_pages, int32_t page_size,
+                            int32_t max_pages, int64_t q_stride, float scale, kda_dtype dtype, void* o, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    kda::set_last_error("");
+    if (N < 1 || T_q < 0 || T_q > (int64_t{1} << 24)) return fail(KDA_ERR_INVALID_ARG, "need N >= 1 and T_q in [0, 2^24]");
+    kda_status s = check_heads(H_q, H_kv, d_k, d_v, dtype);
+    if (s != KDA_OK) return s;
+    if ((s = check_cache(n_pages, page_size, max_pages)) != KDA_OK) return s;
+    if ((s = check_scale(scale)) != KDA_OK) return s;
+    if ((s = check_stride(q_stride, static_cast<int64_t>(H_q) * d_k, dtype, "q_stride")) != KDA_OK) return s;
+    if (!block_table || !ctx_lens || !cu_q) return fail(KDA_ERR_INVALID_ARG, "block_table, ctx_lens and cu_q must not be NULL");
+    if (T_q > 0 && (!q || !k_cache || !v_cache || !o))
+        return fail(KDA_ERR_INVALID_ARG, "q, k_cache, v_cache and o must not be NULL when T_q > 0");
+    for (const void* p : {q, k_cache, v_cache, static_cast<const void*>(o)})
+        if (!aligned(p, 16)) return fail(KDA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+    if (!aligned(tree_mask, 8)) return fail(KDA_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
+    if (!aligned(lse, 4) || !aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(cu_q, 4))
+        return fail(KDA_ERR_INVALID_ARG, "lse, block_table, ctx_lens and cu_q must be 4-byte aligned");
+    const kda::TreePlan plan = kda::tree_plan(N, T_q, H_q, H_kv, d_v, static_cast<int64_t>(max_pages) * page_size,
+                                              kda::device_cus_or_default());
+    if (!tree_countable(plan, max_pages, page_size, H_kv))
+        return fail(KDA_ERR_INVALID_ARG, "too many drafted tokens for sequences this long");
+    if (workspace_bytes < plan.bytes) return fail(KDA_ERR_INVALID_ARG, "workspace smaller than attn_tree_decode_workspace_size");
+    if (plan.bytes > 0 && !workspace) return fail(KDA_ERR_INVALID_ARG, "workspace must not be NULL");
+    if (!aligned(workspace, 256)) return fail(KDA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (T_q == 0) return KDA_OK;
+    kda::TreeArgs a{q, k_cache, v_cache, block_table, ctx_lens, cu_q, reinterpret_cast<const unsigned long long*>(tree_mask),
+                    N, static_cast<int32_t>(T_q), H_q, H_kv, d_k, d_v, n_pages, page_size, __builtin_ctz(page_size), max_pages,
+                    static_cast<int32_t>(q_stride), scale, dtype == KDA_DTYPE_BF16, o, lse, workspace, stream};
+    (void)hipGetLastError();  // report only this launch's status
+    const hipError_t e = kda::launch_attn_tree(a, plan);
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "tree attention kernel launch");
+}
+
+}  // extern "C"

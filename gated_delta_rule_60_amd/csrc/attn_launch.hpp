@@ -35,6 +35,43 @@ struct AttnBwdArgs {
     void* workspace;   // attn_bwd_workspace_bytes
 };
 
+// Attention of drafted tokens over a paged cache.
+struct TreeArgs {
+    const void* q;        // [T_q, Hq, d_k], q_stride elements between tokens
+    const void* k_cache;  // [n_pages, page_size, Hkv, d_k]
+    const void* v_cache;  // [n_pages, page_size, Hkv, d_v]
+    const int32_t* block_table;  // [N, max_pages]
+    const int32_t* ctx_lens;     // [N]
+    const int32_t* cu_q;         // [N + 1]
+    const unsigned long long* tree_mask;  // [T_q] or null
+    int32_t N, T_q, Hq, Hkv, d_k, d_v;
+    int32_t n_pages, page_size, page_shift, max_pages;
+    int32_t q_stride;
+    float scale;
+    bool bf16;
+    void* o;
+    float* lse;  // may be null
+    void* workspace;
+    void* stream;
+    // set by the launcher
+    int32_t chunks_target = 0;
+    int32_t items = 0;
+    float* part_o = nullptr;
+    float* part_ml = nullptr;
+};
+
+// Launch shape: query rows a pass, row tiles and chunk items at most, and the
+// partial results' rows and bytes.
+struct TreePlan {
+    int32_t rows, target;
+    int64_t tiles, items, part_rows;
+    size_t bytes;
+    bool split;
+};
+
+TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus);
+hipError_t launch_attn_tree(TreeArgs a, const TreePlan& p);
+
 hipError_t launch_attn_prefill(const AttnArgs& a);
 hipError_t launch_attn_bwd(const AttnBwdArgs& a);
 size_t attn_bwd_workspace_bytes(int64_t T_tot, int32_t Hq);

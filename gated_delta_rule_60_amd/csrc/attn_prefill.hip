@@ -129,6 +129,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a, float 
             for (int dt = 0; dt < VT::ND; ++dt)
 #pragma unroll
                 for (int n = 0; n < NS; ++n) o[dt] = VT::template cols_times<true>(o[dt], vt, vat, 32 * n, dt, p[n]);
+#pragma unroll 1
             for (int j = 0; j < BN; ++j) VT::add_nonfinite(o, vt, j, half, t * BN + j <= qi);
         } else {
 #pragma unroll

@@ -1,0 +1,649 @@
+// attn_tree.hip -- softmax attention of drafted tokens over a paged cache,
+// gfx950.  One drafted token per sequence is the plain decode step.
+//
+// Sequence n holds ctx_n committed positions and, behind them, the keys and
+// values of its drafted tokens; position p lies in page
+// block_table[n][p / page_size] at row p % page_size.  A drafted token sees
+// every committed position and the drafted ones its mask names.
+//
+// The step reads every visible key and value once per key head and does
+// little with them (2 H_q / H_kv products a value), so it is bound by HBM.
+// The query rows of a key head (drafted tokens x grouped heads) are the
+// columns of 16x16 MFMAs, 16 to 128 of them per pass over the keys.  The keys
+// of a sequence are cut into chunks of equal work over the whole batch, a
+// workgroup each.  A wave holds up to 32 rows.  With no more rows than that
+// its waves take 32-key tiles in turn, each with its own running maximum, sum
+// and output and its own two tiles in LDS, which the loads fill directly: a
+// wave always has a tile in flight and never waits for another.  With more
+// rows, two or four waves share a tile, and all of them load it.  (One wave
+// with 64 rows spilled: 0.69 ms for 329 drafted tokens of 12 trees over up to
+// 32k positions, 32/8 heads of 128, against 0.29 ms with 32 rows a pass.)
+// The waves' results are joined in LDS, the chunks' by a second launch, in a
+// fixed order.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "attn_device.hpp"
+#include "attn_launch.hpp"
+#include "kda_launch.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int kTK = 32;      // keys of a wave's tile
+constexpr int kBlock = 128;  // chunks are multiples of this many keys
+constexpr float kLazyLog2 = 8.f;  // as in attn_prefill.hip
+
+// what the loads of rows outside the cache read instead
+__device__ const float kZeroRow[128] = {};
+
+// NQ 16-row groups a wave, RW waves to a tile (KW tiles at a time, TT in a slot of LDS).
+template <bool BF16, int DK, int DV, int NQ, int RW>
+struct TreeShape {
+    static constexpr int ES = BF16 ? 2 : 4;
+    static constexpr int KB = kTK * DK * ES, VB = kTK * DV * ES;  // tile bytes
+    static constexpr int NW = RW > 1 || 8 * (KB + VB) <= 128 * 1024 ? 4 : 2;
+    static constexpr int KW = NW / RW;
+    static constexpr int R = 16 * NQ * RW;  // query rows
+    // slots: of one wave's tile (RW = 1), or of two tiles that all waves load
+    static constexpr int TT = RW == 1 ? 1 : 2;
+    static constexpr int SLOT = TT * (KB + VB);
+    static constexpr int NS = RW == 1 ? 2 : 4 * SLOT <= 128 * 1024 ? 4 : 2;
+    static constexpr int JOIN = KW / 2 * R * (DV + 2) * 4 + NW * 4;
+    static constexpr int TILES = (RW == 1 ? NW : 1) * NS * SLOT;
+    static constexpr int LDS = TILES > JOIN ? TILES : JOIN;
+};
+
+}  // namespace
+
+// One workgroup's share: query rows [rt R, ...) of sequence n against keys
+// [k0, k1); part `item` of the partial results if the sequence has several
+// chunks.
+struct TreeItem {
+    int n, tok0, lq, ctx, rt, chunks, item, k0, k1;
+};
+
+struct SeqWork {
+    int tok0, lq, ctx, tiles, blocks;
+};
+
+__device__ __forceinline__ SeqWork seq_work(const TreeArgs& a, int n, int rows) {
+    SeqWork s = {0, 0, 0, 0, 0};
+    if (n < a.N) {
+        const int2 bl = seq_bounds(a.cu_q, n, a.T_q);
+        const int room = a.max_pages * a.page_size;
+        int ctx = a.ctx_lens[n];
+        ctx = ctx < 0 ? 0 : (ctx > room ? room : ctx);
+        const int total = ctx + (bl.y < room - ctx ? bl.y : room - ctx);
+        s.tok0 = bl.x;
+        s.lq = bl.y;
+        s.ctx = ctx;
+        s.tiles = (bl.y * (a.Hq / a.Hkv) + rows - 1) / rows;
+        s.blocks = (total + kBlock - 1) / kBlock;
+    }
+    return s;
+}
+
+// Keys a chunk: the whole batch's (row tile, key block) pairs over a.chunks_target chunks.
+__device__ __forceinline__ int chunk_blocks(const TreeArgs& a, int lane, int rows) {
+    int sum = 0;
+    for (int n0 = 0; n0 < a.N; n0 += 64) {
+        const SeqWork s = seq_work(a, n0 + lane, rows);
+        sum += s.tiles * s.blocks;
+    }
+    sum = wave_sum(sum);
+    const int per = (sum + a.chunks_target - 1) / a.chunks_target;
+    return per < 1 ? 1 : per;
+}
+
+// Row tile `p` of the batch (by_chunk: chunk p, counting every row tile's chunks).
+__device__ __forceinline__ bool find_item(const TreeArgs& a, int p, int rows, bool by_chunk, TreeItem& t) {
+    const int lane = threadIdx.x & 63;
+    const int per = chunk_blocks(a, lane, rows);
+    int base = 0;  // chunks before
+    for (int n0 = 0; n0 < a.N; n0 += 64) {
+        const SeqWork s = seq_work(a, n0 + lane, rows);
+        const int chunks = s.blocks > per ? (s.blocks + per - 1) / per : 1;
+        const int all = s.tiles * chunks, mine = by_chunk ? all : s.tiles;
+        const int upto = wave_scan(mine), upto_chunks = wave_scan(all);
+        const int total = __builtin_amdgcn_readlane(upto, 63);
+        if (p < total) {
+            const int l = __builtin_ctzll(__ballot(upto > p));
+            const int r = p - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l));
+            t.chunks = __builtin_amdgcn_readlane(chunks, l);
+            t.n = n0 + l;
+            t.tok0 = __builtin_amdgcn_readlane(s.tok0, l);
+            t.lq = __builtin_amdgcn_readlane(s.lq, l);
+            t.ctx = __builtin_amdgcn_readlane(s.ctx, l);
+            t.rt = by_chunk ? r / t.chunks : r;
+            const int c = by_chunk ? r % t.chunks : 0;
+            t.item = base + __builtin_amdgcn_readlane(upto_chunks, l) - __builtin_amdgcn_readlane(all, l) + t.rt * t.chunks + c;
+            const int blocks = __builtin_amdgcn_readlane(s.blocks, l);
+            // even chunks, in blocks
+            t.k0 = static_cast<int>(static_cast<int64_t>(blocks) * c / t.chunks) * kBlock;
+            t.k1 = static_cast<int>(static_cast<int64_t>(blocks) * (c + 1) / t.chunks) * kBlock;
+            return true;
+        }
+        p -= total;
+        base += __builtin_amdgcn_readlane(upto_chunks, 63);
+    }
+    return false;
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+    const unsigned u = __float_as_uint(x);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+    const unsigned u = __float_as_uint(x);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// 16 bytes a lane from its own address to LDS at `lds` + 16 lane.
+__device__ __forceinline__ void load_lds16_from(const char* p, char* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p, (KDA_LDS void*)lds, 16, 0, 0);
+#endif
+}
+
+template <bool BF16, int DK, int DV, int NQ, int RW>
+__global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW)) void attn_tree_kernel(TreeArgs a, float c) {
+    using Sh = TreeShape<BF16, DK, DV, NQ, RW>;
+    using T = Elem<BF16>;
+    using KT = AttnTile<BF16, DK>;
+    using VT = AttnTile<BF16, DV>;
+    constexpr int NW = Sh::NW, KW = Sh::KW, R = Sh::R, ES = Sh::ES, KB = Sh::KB, VB = Sh::VB, SLOT = Sh::SLOT, NS = Sh::NS, TT = Sh::TT;
+    constexpr int NK = DK / 32, ND = DV / 16;
+    constexpr int LW = RW == 1 ? 1 : NW;            // waves that load a slot
+    constexpr int TK = TT * kTK;                    // its keys
+    constexpr int KI = TT * KB / 1024 / LW, VI = TT * VB / 1024 / LW;  // wave-wide loads of each wave
+    static_assert(KI >= 1 && VI >= 1, "every wave loads");
+    __shared__ __attribute__((aligned(1024))) char lds[Sh::LDS];
+
+    const int lane = threadIdx.x & 63, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kw = wave / RW, rw = wave % RW;  // the wave's tile among KW, its rows among RW
+    const int g = blockIdx.x % a.Hkv;
+    const int group = a.Hq / a.Hkv;
+    TreeItem it;
+    if (!find_item(a, blockIdx.x / a.Hkv, R, true, it)) return;
+    const int wrow = it.rt * R + rw * 16 * NQ;  // the wave's first row
+    const bool working = wrow < it.lq * group;
+
+    // the lane's query rows: column lane & 15 of each 16-row tile
+    typename T::F8 q[NQ][NK];
+    unsigned long long sees[NQ];  // drafted positions the row sees
+    int own[NQ];                  // its token
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+        const int r = wrow + 16 * x + (lane & 15);
+        const int t = r / group, h = g * group + r % group;
+        const bool live = t < it.lq;
+        const typename T::G* p = static_cast<const typename T::G*>(a.q) + static_cast<size_t>(it.tok0 + (live ? t : 0)) * a.q_stride +
+                                 static_cast<size_t>(live ? h : 0) * DK;
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+            typename T::F8 f = {};
+            if (live) f = *reinterpret_cast<const typename T::F8*>(p + 32 * kk + 8 * g4);
+            q[x][kk] = f;
+        }
+        unsigned long long m = 0;
+        if (live) {
+            if (a.tree_mask) {
+                m = a.tree_mask[it.tok0 + t];
+                if (it.lq < 64) m &= (1ull << it.lq) - 1;
+            }
+        }
+        sees[x] = m;
+        own[x] = t;
+    }
+
+    // Which of the 32 keys from key0 on the row sees, a bit each.  Without a mask a token sees the
+    // drafted ones up to itself, however many.
+    auto visible = [&](int x, int key0) __attribute__((always_inline)) {
+        const int past = key0 - it.ctx;  // committed keys come first: -past of them, or none
+        const int upto = a.tree_mask ? -past : own[x] + 1 - past;  // leading keys seen for sure
+        unsigned v = upto >= 32 ? ~0u : upto > 0 ? (1u << upto) - 1 : 0u;
+        const unsigned long long up = past <= -32 ? 0ull : sees[x] << (past < 0 ? -past : 0);
+        const unsigned long long down = past >= 64 ? 0ull : sees[x] >> (past > 0 ? past : 0);
+        const unsigned drafted = static_cast<unsigned>(past < 0 ? up : down);
+        return a.tree_mask ? v | drafted : v;
+    };
+
+    const int room = a.max_pages * a.page_size;
+    const int total = it.ctx + (it.lq < room - it.ctx ? it.lq : room - it.ctx);
+    const int k1 = it.k1 < total ? it.k1 : total;
+    // slots of keys this wave sees go by: its own tiles, every NW-th, or all
+    const int all = k1 > it.k0 ? (k1 - it.k0 + TK - 1) / TK : 0;
+    const int slots = RW > 1 ? all : all > wave ? (all - wave + NW - 1) / NW : 0;
+    char* const mine = lds + (RW == 1 ? wave * NS * SLOT : 0);
+    const int32_t* table = a.block_table + static_cast<size_t>(it.n) * a.max_pages;
+
+    auto slot_key = [&](int i) __attribute__((always_inline)) { return it.k0 + (RW == 1 ? wave + i * NW : i) * TK; };
+    // token row in the cache of key `lane % TK` of slot i; negative if there is none
+    auto lookup = [&](int i) __attribute__((always_inline)) {
+        const int pos = slot_key(i) + lane % TK;
+        int tok = -1;
+        if (i < slots && pos < k1) {
+            const int page = table[pos >> a.page_shift];
+            if (page >= 0 && page < a.n_pages) tok = (page << a.page_shift) + (pos & (a.page_size - 1));
+        }
+        return tok;
+    };
+    const char* const kc = static_cast<const char*>(a.k_cache) + static_cast<size_t>(g) * DK * ES;
+    const char* const vc = static_cast<const char*>(a.v_cache) + static_cast<size_t>(g) * DV * ES;
+    const size_t krow = static_cast<size_t>(a.Hkv) * DK * ES, vrow = static_cast<size_t>(a.Hkv) * DV * ES;
+    const char* const zeros = reinterpret_cast<const char*>(kZeroRow);
+    // slot: TT tiles' keys, then their values
+    auto stage = [&](int slot, int tok) __attribute__((always_inline)) {
+        char* b = mine + slot * SLOT;
+        const int w = RW == 1 ? 0 : wave;
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+            const int r = (i * LW + w) * KT::RPI + lane / KT::U, u = (lane % KT::U) ^ KT::swz(r);
+            const int t = __shfl(tok, r);
+            load_lds16_from(t >= 0 ? kc + t * krow + u * 16 : zeros, b + (i * LW + w) * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < VI; ++i) {
+            const int r = (i * LW + w) * VT::RPI + lane / VT::U, u = (lane % VT::U) ^ VT::swz(r);
+            const int t = __shfl(tok, r);
+            load_lds16_from(t >= 0 ? vc + t * vrow + u * 16 : zeros, b + TT * KB + (i * LW + w) * 1024);
+        }
+    };
+
+    f32x4_t o[NQ][ND];
+    float mc[NQ], l[NQ];
+    int poisoned = 0;  // a drafted value of a tile was not finite
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+        mc[x] = -INFINITY;
+        l[x] = 0.f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[x][d] = f32x4_t{};
+    }
+
+    // element [row][unit of the lane's fragment] of a tile
+    auto kfrag = [&](const char* kt, int r, int kk) __attribute__((always_inline)) {
+        if constexpr (BF16) {
+            return *reinterpret_cast<const typename T::F8*>(kt + r * KT::ROWB + (((4 * kk + g4) ^ KT::swz(r)) << 4));
+        } else {
+            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(kt + r * KT::ROWB + (((8 * kk + 2 * g4) ^ KT::swz(r)) << 4));
+            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(kt + r * KT::ROWB + (((8 * kk + 2 * g4 + 1) ^ KT::swz(r)) << 4));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
+    // columns 16 d .. 16 d + 15 of the tile's rows, as the A operand over its 32 rows
+    auto vfrag = [&](const char* vt, int d) __attribute__((always_inline)) {
+        typename T::F8 f;
+        if constexpr (BF16) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int i = lane & 15, r = 16 * hh + 4 * g4 + (i >> 2), u = 2 * d + ((i & 3) >> 1);
+                const char* p = vt + r * VT::ROWB + ((u ^ VT::swz(r)) << 4) + (i & 1) * 8;
+                const auto x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((KDA_LDS bf16x4_t*)p);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[4 * hh + e] = x[e];
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int r = 16 * (s >> 2) + 4 * g4 + (s & 3), u = 4 * d + ((lane & 15) >> 2);
+                f[s] = *reinterpret_cast<const float*>(vt + r * VT::ROWB + ((u ^ VT::swz(r)) << 4) + (lane & 3) * 4);
+            }
+        }
+        return f;
+    };
+
+    // One tile into the rows' statistics and outputs.  MASKED: the tile holds drafted positions or
+    // rows that are not in the cache.
+    auto step = [&](auto MASKED, const char* kt, char* vt, int key0, unsigned there) __attribute__((always_inline)) {
+        f32x4_t s[NQ][2];
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) s[x][y] = f32x4_t{};
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk) {
+                const typename T::F8 k = kfrag(kt, 16 * y + (lane & 15), kk);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) s[x][y] = mma8<BF16>(s[x][y], k, q[x][kk]);
+            }
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+                const unsigned w = (visible(x, key0) & there) >> (4 * g4);
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[x][y][e] = (w >> (16 * y + e)) & 1 ? s[x][y][e] : -INFINITY;
+            }
+        }
+        typename T::F8 p[NQ];
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            float mx = s[x][0][0];
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[x][y][e]);
+            mx = quad_max(mx) * c;
+            if (__any(mx > mc[x] + kLazyLog2)) {
+                const float m1 = mx > mc[x] + kLazyLog2 ? mx : mc[x];
+                const float r = m1 > mc[x] ? exp2f(mc[x] - m1) : 1.f;
+                mc[x] = m1;
+                l[x] *= r;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[x][d][e] *= r;
+            }
+            const float m = mc[x] == -INFINITY ? 0.f : mc[x];  // nothing seen yet: weights are 2^-inf
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[x][y][e] = __builtin_amdgcn_exp2f(fmaf(s[x][y][e], c, -m));
+                    l[x] += s[x][y][e];
+                }
+            p[x] = acc_frag8<BF16>(s[x][0], s[x][1]);
+        }
+        // A weight of zero does not keep out an infinity or NaN behind the mask: where the tile has
+        // any, drafted positions' are cleared, and added at the end to the rows that see them.
+        // (Committed positions are seen by all rows.)
+        if (MASKED && VT::template any_nonfinite<kTK>(vt, lane)) {
+            poisoned = 1;
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            for (int r = 0; r < kTK; ++r)
+                if (key0 + r >= it.ctx)
+                    for (int e = lane; e < DV; e += 64) {  // in any order of the row's units
+                        typename T::E* y = reinterpret_cast<typename T::E*>(vt + r * VT::ROWB) + e;
+                        if (!VT::finite(*y)) *y = static_cast<typename T::E>(0.f);
+                    }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            const typename T::F8 v = vfrag(vt, d);
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) o[x][d] = mma8<BF16>(o[x][d], v, p[x]);
+        }
+    };
+
+    // tokens of slots i .. i + NS: one more than are loaded or in flight
+    int tok[NS + 1];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) tok[n] = lookup(n);
+#pragma unroll
+    for (int n = 0; n < NS - 1; ++n)
+        if (n < slots) stage(n, tok[n]);
+    for (int i = 0, slot = 0; i < slots; ++i, slot = slot + 1 == NS ? 0 : slot + 1) {
+        tok[NS] = lookup(i + NS);
+        // slot i has landed: at most the loads of the NS - 2 after it are still on the way
+        const int after = slots - 1 - i;
+        if (NS > 2 && after >= NS - 2)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(NS > 2 ? (NS - 2) * (KI + VI) : 0) : "memory");
+        else if (RW > 1 || NS > 2)
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        else
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if constexpr (RW > 1) {  // and every wave's part; all are done with the slot before
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        }
+        if (i + NS - 1 < slots) {
+            stage(slot == 0 ? NS - 1 : slot - 1, tok[NS - 1]);
+            if constexpr (RW == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(KI + VI) : "memory");
+        } else if constexpr (RW == 1) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        for (int tt = RW == 1 ? 0 : kw; tt < TT; tt += KW) {
+            const char* kt = mine + slot * SLOT + tt * KB;
+            char* vt = mine + slot * SLOT + TT * KB + tt * VB;
+            const int key0 = slot_key(i) + tt * kTK;
+            if (!working || key0 >= k1) break;
+            // keys of the tile that exist; drafted ones need a look at the masks
+            const unsigned there = static_cast<unsigned>(__ballot(tok[0] >= 0) >> (tt * kTK));
+            const bool masked = there != 0xFFFFFFFFu || key0 + kTK > it.ctx;
+            if (masked) step(std::true_type{}, kt, vt, key0, there); else step(std::false_type{}, kt, vt, key0, there);
+        }
+#pragma unroll
+        for (int n = 0; n < NS; ++n) tok[n] = tok[n + 1];
+    }
+
+    // join the waves, the upper half into the lower until one is left
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) l[x] = quad_sum(l[x]);
+    float* const so = reinterpret_cast<float*>(lds);                  // [KW / 2][RW][NQ][ND][64 lanes][4]
+    float* const sm = so + KW / 2 * R * DV;                           // [KW / 2][RW][NQ][16][2]
+    int* const sp = reinterpret_cast<int*>(sm + KW / 2 * R * 2);      // [NW]
+    __syncthreads();
+    if (lane == 0) sp[wave] = poisoned;
+    if constexpr (KW > 1) {
+#pragma unroll
+        for (int w = KW >> 1; w > 0; w >>= 1) {
+            if (w < KW / 2) __syncthreads();
+            if (kw >= w && kw < 2 * w) {
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    const int y = ((kw - w) * RW + rw) * NQ + x;
+                    if (g4 == 0) {
+                        sm[2 * (y * 16 + lane)] = mc[x];
+                        sm[2 * (y * 16 + lane) + 1] = l[x];
+                    }
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4_t*>(so + ((y * ND + d) * 64 + lane) * 4) = o[x][d];
+                }
+            }
+            __syncthreads();
+            if (kw < w) {
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    const int z = (kw * RW + rw) * NQ + x, b = z * 16 + (lane & 15);
+                    const float m2 = sm[2 * b], l2 = sm[2 * b + 1];
+                    const float m1 = fmaxf(mc[x], m2);
+                    const float r1 = mc[x] == m1 ? 1.f : exp2f(mc[x] - m1), r2 = m2 == m1 ? 1.f : exp2f(m2 - m1);
+                    mc[x] = m1;
+                    l[x] = l[x] * r1 + l2 * r2;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) {
+                        const f32x4_t y = *reinterpret_cast<const f32x4_t*>(so + ((z * ND + d) * 64 + lane) * 4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[x][d][e] = o[x][d][e] * r1 + y[e] * r2;
+                    }
+                }
+            }
+        }
+    } else {
+        __syncthreads();
+    }
+    if (kw != 0 || !working) return;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) poisoned |= sp[w];
+    if (poisoned) {
+        for (int pos = it.k0 > it.ctx ? it.k0 : it.ctx; pos < k1; ++pos) {
+            const int page = table[pos >> a.page_shift];
+            if (page < 0 || page >= a.n_pages) continue;
+            const size_t t = (static_cast<size_t>(page) << a.page_shift) + (pos & (a.page_size - 1));
+            unsigned v1[NQ];
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) v1[x] = visible(x, pos) & 1;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                float v[4];
+                T::load4(reinterpret_cast<const typename T::G*>(vc + t * vrow) + 16 * d + 4 * g4, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int x = 0; x < NQ; ++x)
+                        if (!VT::finite(v[e]) && v1[x]) o[x][d][e] += v[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+        const int rr = (rw * NQ + x) * 16 + (lane & 15), r = it.rt * R + rr;
+        const int t = r / group, h = g * group + r % group;
+        if (t >= it.lq) continue;
+        if (it.chunks == 1) {
+            const size_t row = static_cast<size_t>(it.tok0 + t) * a.Hq + h;
+            const float inv = l[x] > 0.f ? 1.f / l[x] : (l[x] == 0.f ? 0.f : l[x]);
+            typename T::G* p = static_cast<typename T::G*>(a.o) + row * DV + 4 * g4;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const float y[4] = {o[x][d][0] * inv, o[x][d][1] * inv, o[x][d][2] * inv, o[x][d][3] * inv};
+                T::store4(p + 16 * d, y);
+            }
+            if (a.lse && g4 == 0) a.lse[row] = (mc[x] + log2f(l[x])) * kLn2;
+        } else {
+            const size_t row = (static_cast<size_t>(it.item) * a.Hkv + g) * R + rr;
+            float* p = a.part_o + row * DV + 4 * g4;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4_t*>(p + 16 * d) = o[x][d];
+            if (g4 == 0) {
+                a.part_ml[2 * row] = mc[x];
+                a.part_ml[2 * row + 1] = l[x];
+            }
+        }
+    }
+}
+
+// Joins the chunks of a row tile: o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c, in the chunks'
+// order; a few rows a workgroup.
+template <bool BF16, int DV>
+__global__ __launch_bounds__(256) void attn_tree_join_kernel(TreeArgs a, int R) {
+    using T = Elem<BF16>;
+    constexpr int TPR = DV / 4;  // threads a row
+    const int g = blockIdx.x % a.Hkv;
+    const int group = a.Hq / a.Hkv;
+    TreeItem it;
+    if (!find_item(a, blockIdx.x / a.Hkv, R, false, it) || it.chunks == 1) return;
+    if (it.item + it.chunks > a.items) return;  // offsets that overlap: no such partial results
+    const int rr = blockIdx.y * (256 / TPR) + threadIdx.x / TPR;
+    const int r = it.rt * R + rr, t = r / group, h = g * group + r % group;
+    if (rr >= R || t >= it.lq) return;
+    const int d = 4 * (threadIdx.x % TPR);
+    const size_t step = static_cast<size_t>(a.Hkv) * R;
+    const size_t row0 = (static_cast<size_t>(it.item) * a.Hkv + g) * R + rr;
+    // four chunks' loads at a time; past the last, the last again with weight zero
+    constexpr int B = 4;
+    float m = -INFINITY;
+    for (int c = 0; c < it.chunks; c += B) {
+        float m2[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) m2[b] = a.part_ml[2 * (row0 + (c + b < it.chunks ? c + b : it.chunks - 1) * step)];
+#pragma unroll
+        for (int b = 0; b < B; ++b) m = fmaxf(m, m2[b]);
+    }
+    float l = 0.f;
+    f32x4_t o = {};
+    for (int c = 0; c < it.chunks; c += B) {
+        float m2[B], l2[B];
+        f32x4_t y[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const size_t row = row0 + (c + b < it.chunks ? c + b : it.chunks - 1) * step;
+            m2[b] = a.part_ml[2 * row];
+            l2[b] = a.part_ml[2 * row + 1];
+            y[b] = *reinterpret_cast<const f32x4_t*>(a.part_o + row * DV + d);
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (c + b >= it.chunks) break;
+            const float w = m2[b] == m ? 1.f : exp2f(m2[b] - m);
+            l = fmaf(l2[b], w, l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(y[b][e], w, o[e]);
+        }
+    }
+    const size_t row = static_cast<size_t>(it.tok0 + t) * a.Hq + h;
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const float y[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+    T::store4(static_cast<typename T::G*>(a.o) + row * DV + d, y);
+    if (a.lse && d == 0) a.lse[row] = (m + log2f(l)) * kLn2;
+}
+
+namespace {
+
+template <bool BF16, int DK, int DV, int NQ, int RW>
+hipError_t launch(const TreeArgs& a, const TreePlan& p) {
+    using Sh = TreeShape<BF16, DK, DV, NQ, RW>;
+    const hipStream_t st = static_cast<hipStream_t>(a.stream);
+    hipLaunchKernelGGL((attn_tree_kernel<BF16, DK, DV, NQ, RW>), dim3(static_cast<unsigned>(p.items * a.Hkv)), dim3(64 * Sh::NW), 0,
+                       st, a, a.scale * kLog2e);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !p.split) return e;
+    constexpr int rows = 256 / (DV / 4);  // of a workgroup of the join
+    hipLaunchKernelGGL((attn_tree_join_kernel<BF16, DV>), dim3(static_cast<unsigned>(p.tiles * a.Hkv), (Sh::R + rows - 1) / rows),
+                       dim3(256), 0, st, a, Sh::R);
+    return hipGetLastError();
+}
+
+template <bool BF16, int DK, int DV>
+hipError_t launch_rows(const TreeArgs& a, const TreePlan& p) {
+    switch (p.rows) {
+        case 16: return launch<BF16, DK, DV, 1, 1>(a, p);
+        case 32: return launch<BF16, DK, DV, 2, 1>(a, p);
+        case 64: return launch<BF16, DK, DV, 2, 2>(a, p);
+        default: return launch<BF16, DK, DV, 2, 4>(a, p);
+    }
+}
+
+template <bool BF16, int DK>
+hipError_t launch_dv(const TreeArgs& a, const TreePlan& p) {
+    switch (a.d_v) {
+        case 32: return launch_rows<BF16, DK, 32>(a, p);
+        case 64: return launch_rows<BF16, DK, 64>(a, p);
+        default: return launch_rows<BF16, DK, 128>(a, p);
+    }
+}
+
+template <bool BF16>
+hipError_t launch_dk(const TreeArgs& a, const TreePlan& p) {
+    switch (a.d_k) {
+        case 32: return launch_dv<BF16, 32>(a, p);
+        case 64: return launch_dv<BF16, 64>(a, p);
+        default: return launch_dv<BF16, 128>(a, p);
+    }
+}
+
+}  // namespace
+
+// Query rows a pass: the smallest of 16, 32, 64 and 128 that holds an average
+// sequence's rows.  Chunks: eight workgroups a compute unit, so that uneven
+// sequences end together; never more than the cache's blocks.
+TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus) {
+    TreePlan p;
+    const int64_t rows = T_q * (Hq / Hkv);
+    const int64_t avg = (rows + N - 1) / N;
+    p.rows = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
+    p.tiles = rows / p.rows + N;
+    if (p.tiles > rows) p.tiles = rows;
+    const int64_t blocks = (room + kBlock - 1) / kBlock;
+    int64_t target = 8 * static_cast<int64_t>(cus) / Hkv;
+    if (target < 1) target = 1;
+    p.target = static_cast<int32_t>(target);
+    p.split = blocks > 1 && T_q > 0;
+    p.items = p.split ? p.tiles + p.target : p.tiles;
+    if (p.items > p.tiles * blocks) p.items = p.tiles * (blocks > 0 ? blocks : 1);
+    p.part_rows = p.split ? p.items * Hkv * p.rows : 0;
+    p.bytes = p.split ? static_cast<size_t>(p.part_rows) * (d_v + 2) * sizeof(float) : 0;
+    return p;
+}
+
+hipError_t launch_attn_tree(TreeArgs a, const TreePlan& p) {
+    if (a.T_q == 0) return hipSuccess;
+    a.chunks_target = p.target;
+    a.items = static_cast<int32_t>(p.items);
+    a.part_o = static_cast<float*>(a.workspace);
+    a.part_ml = a.part_o + static_cast<size_t>(p.part_rows) * a.d_v;
+    return a.bf16 ? launch_dk<true>(a, p) : launch_dk<false>(a, p);
+}
+
+}  // namespace kda

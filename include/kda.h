@@ -470,6 +470,55 @@ kda_status attn_prefill_backward(const void* q, const void* k, const void* v, co
 /* Workspace bytes attn_prefill_backward needs (0 for unsupported sizes). */
 size_t attn_prefill_backward_workspace_size(int64_t T_tot, int32_t H_q);
 
+/*
+ * A paged cache holds the keys and values of many sequences of growing
+ * length in pages of page_size positions:
+ *
+ *   k_cache      device [n_pages, page_size, H_kv, d_k]  dtype
+ *   v_cache      device [n_pages, page_size, H_kv, d_v]  dtype
+ *   block_table  device [N, max_pages]  int32   position p of sequence n lies
+ *                in page block_table[n][p / page_size], row p % page_size
+ *   page_size a power of two, at most 4096; n_pages * page_size < 2^31;
+ *   max_pages * page_size <= 2^30.
+ * An entry outside [0, n_pages) is no page: its positions are seen by no row
+ * and written by no call.
+ *
+ * attn_tree_decode -- attention of drafted tokens over such a cache.  The
+ * T_q tokens are packed by sequence (cu_q).  Sequence n has ctx_lens[n]
+ * committed positions; its drafted token j (counted within the sequence) has
+ * its key and value at position ctx_lens[n] + j (kv_append puts them there).
+ * Token t sees every committed position of its sequence and drafted position
+ * j if bit j of tree_mask[t] is set (bits at or past the sequence's number
+ * of drafted tokens count as clear; without a mask, j <= its own number, any
+ * number of them).  One token per sequence and no mask: the decode step.
+ * A row that sees nothing: o = 0, lse = -infinity.
+ *
+ *   q          device [T_q, H_q, d_k] dtype, q_stride elements between tokens
+ *   cu_q       device [N + 1] int32, as cu_seqlens of attn_prefill
+ *   ctx_lens   device [N] int32, clamped to [0, max_pages * page_size]
+ *   tree_mask  device [T_q] uint64, or NULL
+ *   T_q        in [0, 2^24]
+ *   o, lse     as for attn_prefill ([T_q, H_q, d_v], [T_q, H_q] or NULL);
+ *              rows at or past cu_q[N] are not written
+ *   workspace  at least attn_tree_decode_workspace_size bytes (NULL if 0),
+ *              256-byte aligned, used until the queued work ends
+ * No size on the host depends on ctx_lens: a captured call can be replayed
+ * while the sequences grow.  Non-finite keys and values that a row does not
+ * see do not reach it.
+ */
+kda_status attn_tree_decode(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* ctx_lens,
+                            const int32_t* cu_q, const uint64_t* tree_mask, int32_t N,
+                            int64_t T_q, int32_t H_q, int32_t H_kv, int32_t d_k, int32_t d_v,
+                            int32_t n_pages, int32_t page_size, int32_t max_pages,
+                            int64_t q_stride, float scale, kda_dtype dtype, void* o, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_tree_decode needs on the current device (0 for
+ * unsupported sizes): the partial results of sequences cut into chunks. */
+size_t attn_tree_decode_workspace_size(int32_t N, int64_t T_q, int32_t H_q, int32_t H_kv,
+                                       int32_t d_v, int32_t page_size, int32_t max_pages);
+
 /* Static text for a status code. */
 const char* kda_status_string(kda_status status);
 

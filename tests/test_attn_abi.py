@@ -90,9 +90,79 @@ def test_backward_refuses(kw, status, needle):
     assert needle in kda.kda_last_error()
 
 
+def _tree(**kw):
+    a = dict(q=FAKE, k_cache=FAKE, v_cache=FAKE, block_table=FAKE, ctx_lens=FAKE, cu_q=FAKE, tree_mask=FAKE, N=4, T_q=16,
+             H_q=8, H_kv=2, d_k=64, d_v=128, n_pages=100, page_size=16, max_pages=32, q_stride=512, scale=0.1,
+             dtype=BF16, o=FAKE, lse=FAKE, workspace=FAKE, workspace_bytes=1 << 40, stream=None)
+    a.update(kw)
+    return kda.attn_tree_decode(**a)
+
+
+CACHE = [
+    (dict(page_size=12), BAD, "page_size"),
+    (dict(page_size=0), BAD, "page_size"),
+    (dict(page_size=-16), BAD, "page_size"),
+    (dict(page_size=8192), BAD, "page_size"),
+    (dict(n_pages=0), BAD, "n_pages"),
+    (dict(n_pages=1 << 27), BAD, "2^31"),
+    (dict(max_pages=0), BAD, "max_pages"),
+    (dict(max_pages=(1 << 26) + 1), BAD, "2^30"),
+]
+
+
+@pytest.mark.parametrize("kw,status,needle", CACHE + [
+    (dict(N=0), BAD, "N >= 1"),
+    (dict(T_q=-1), BAD, "T_q"),
+    (dict(T_q=(1 << 24) + 1), BAD, "T_q"),
+    (dict(H_q=7), BAD, "multiple of H_kv"),
+    (dict(d_k=16), NOT, "d_k and d_v"),
+    (dict(dtype=3), NOT, "dtype"),
+    (dict(q_stride=504), BAD, "q_stride"),
+    (dict(scale=0.0), BAD, "scale"),
+    (dict(block_table=None), BAD, "must not be NULL"),
+    (dict(ctx_lens=None), BAD, "must not be NULL"),
+    (dict(q=None), BAD, "must not be NULL"),
+    (dict(o=None), BAD, "must not be NULL"),
+    (dict(k_cache=FAKE + 8), BAD, "16-byte aligned"),
+    (dict(tree_mask=FAKE + 4), BAD, "8-byte aligned"),
+    (dict(cu_q=FAKE + 1), BAD, "4-byte aligned"),
+    (dict(workspace_bytes=64), BAD, "workspace smaller"),
+    (dict(workspace=None), BAD, "workspace must not be NULL"),
+    (dict(workspace=FAKE + 128), BAD, "256-byte aligned"),
+    (dict(T_q=1 << 24, max_pages=1 << 26), BAD, "too many drafted tokens"),
+])
+def test_tree_refuses(kw, status, needle):
+    assert _tree(**kw) == status
+    assert needle in kda.kda_last_error()
+
+
+def test_tree_workspace():
+    size = kda.attn_tree_decode_workspace_size
+    assert size(4, 16, 8, 2, 128, 16, 8) == 0        # one block of keys: nothing to join
+    assert size(4, 16, 8, 2, 128, 16, 32) > 0
+    assert size(4, 0, 8, 2, 128, 16, 32) == 0
+    assert size(4, 16, 8, 2, 128, 16, 64) >= size(4, 16, 8, 2, 128, 16, 32)
+    for bad in ((0, 16, 8, 2, 128, 16, 32), (4, -1, 8, 2, 128, 16, 32), (4, 16, 8, 3, 128, 16, 32),
+                (4, 16, 8, 2, 48, 16, 32), (4, 16, 8, 2, 128, 12, 32), (4, 16, 8, 2, 128, 16, 0)):
+        assert size(*bad) == 0
+
+
+def test_tree_masks():
+    torch = pytest.importorskip("torch")
+    m = kda.attn_tree_masks([[-1, 0, 0, 1, -1], [], [-1] + list(range(63))])
+    assert m.dtype == torch.int64 and m.tolist()[:5] == [1, 3, 5, 11, 16]
+    assert m[5 + 63] == -1 and m[5 + 62] == (1 << 63) - 1
+    with pytest.raises(ValueError, match="64"):
+        kda.attn_tree_masks([[-1] * 65])
+    for bad in ([0], [-1, 1], [-1, -2]):
+        with pytest.raises(ValueError, match="parent"):
+            kda.attn_tree_masks([bad])
+
+
 def test_nothing_to_do_is_done():
     assert _prefill(T_tot=0, q=None, k=None, v=None, o=None, lse=None) == kda.KDA_OK
     assert kda.kda_last_error() == ""
+    assert _tree(T_q=0, q=None, k_cache=None, v_cache=None, o=None, workspace=None, workspace_bytes=0) == kda.KDA_OK
     assert _backward(T_tot=0, q=None, k=None, v=None, o=None, lse=None, d_o=None, d_q=None, d_k_out=None, d_v_out=None,
                      workspace=None, workspace_bytes=0) == kda.KDA_OK
 
