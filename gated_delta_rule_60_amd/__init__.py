@@ -11,6 +11,7 @@ kernels behind the C ABI of include/kda.h (libkda.so).
 does, and raises if it has not been built.
 """
 from ._attn import (  # noqa: F401
+    KVPages,
     attn_prefill,
     attn_prefill_backward,
     attn_prefill_backward_t,
@@ -20,6 +21,17 @@ from ._attn import (  # noqa: F401
     attn_tree_decode_t,
     attn_tree_decode_workspace_size,
     attn_tree_masks,
+    kv_append,
+    kv_append_t,
+    kv_compact,
+    kv_compact_t,
+    kv_fork,
+    kv_fork_t,
+    kv_free,
+    kv_free_t,
+    kv_pages,
+    kv_reserve,
+    kv_reserve_t,
 )
 from ._lib import (  # noqa: F401
     KDA_DTYPE_BF16,

@@ -10,7 +10,9 @@ library's HIP kernels; there is no fallback of any kind.
 """
 from __future__ import annotations
 
+import dataclasses
 import math
+from typing import Any
 
 from ._lib import _check, _dtype_code, _need, _stream_of, load
 
@@ -44,6 +46,36 @@ def attn_tree_decode(q, k_cache, v_cache, block_table, ctx_lens, cu_q, tree_mask
 
 def attn_tree_decode_workspace_size(N, T_q, H_q, H_kv, d_v, page_size, max_pages) -> int:
     return int(load().attn_tree_decode_workspace_size(N, T_q, H_q, H_kv, d_v, page_size, max_pages))
+
+
+def kv_reserve(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages, rows, n_tokens,
+               n, status, stream) -> int:
+    return load().kv_reserve(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages,
+                             rows, n_tokens, n, status, stream)
+
+
+def kv_free(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages, rows, n,
+            stream) -> int:
+    return load().kv_free(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages, rows,
+                          n, stream)
+
+
+def kv_fork(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages, src, dst, n,
+            k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, status, stream) -> int:
+    return load().kv_fork(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages, src,
+                          dst, n, k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, status, stream)
+
+
+def kv_append(k, v, k_cache, v_cache, block_table, lens, cu_new, N, T_new, n_layers, H_kv, d_k, d_v, n_pages, page_size,
+              max_pages, dtype, stream) -> int:
+    return load().kv_append(k, v, k_cache, v_cache, block_table, lens, cu_new, N, T_new, n_layers, H_kv, d_k, d_v,
+                            n_pages, page_size, max_pages, dtype, stream)
+
+
+def kv_compact(k_cache, v_cache, block_table, lens, accepted, cu_accepted, N, A_tot, n_layers, H_kv, d_k, d_v, n_pages,
+               page_size, max_pages, dtype, new_lens, stream) -> int:
+    return load().kv_compact(k_cache, v_cache, block_table, lens, accepted, cu_accepted, N, A_tot, n_layers, H_kv, d_k,
+                             d_v, n_pages, page_size, max_pages, dtype, new_lens, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -222,3 +254,162 @@ def attn_tree_decode_t(q, k_cache, v_cache, block_table, ctx_lens, cu_q=None, tr
                                 MP, qs, 1.0 / math.sqrt(dk) if scale is None else float(scale), code, o.data_ptr(),
                                 lse.data_ptr(), workspace.data_ptr(), workspace.numel(), int(st.cuda_stream)))
     return o, lse
+
+
+# ---------------------------------------------------------------------------
+# pages of the cache
+# ---------------------------------------------------------------------------
+@dataclasses.dataclass
+class KVPages:
+    """The bookkeeping of a paged cache: int32 device tensors, shared by all
+    layers (``kv_pages`` makes an empty one).
+
+    table [rows, max_pages]: a row's pages, -1 behind them; lens [rows]: its
+    committed positions; held [rows]: its pages; refs [n_pages]: rows that
+    hold a page; free [n_pages]: free pages, the first n_free [1] of them."""
+    table: Any
+    lens: Any
+    held: Any
+    refs: Any
+    free: Any
+    n_free: Any
+    page_size: int
+
+
+def kv_pages(n_rows: int, max_pages: int, n_pages: int, page_size: int, device="cuda") -> KVPages:
+    """The bookkeeping of an empty cache: every page free, every row unused."""
+    import torch
+    z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+    return KVPages(table=z(n_rows, max_pages) - 1, lens=z(n_rows), held=z(n_rows), refs=z(n_pages),
+                   free=torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   n_free=z(1) + n_pages, page_size=page_size)
+
+
+def _pages_args(p: KVPages):
+    """Check the six tensors; returns (device, the C calls' leading arguments)."""
+    import torch
+    t = p.table
+    if not t.is_cuda:
+        raise ValueError("the cache's pages are kept on a GPU device; table is on the CPU")
+    if t.dim() != 2 or p.refs.dim() != 1:
+        raise ValueError("table must be [rows, max_pages] and refs [n_pages]")
+    R, MP, P = int(t.shape[0]), int(t.shape[1]), int(p.refs.shape[0])
+    for x, name, shape in ((t, "table", (R, MP)), (p.lens, "lens", (R,)), (p.held, "held", (R,)),
+                           (p.refs, "refs", (P,)), (p.free, "free", (P,)), (p.n_free, "n_free", (1,))):
+        _need(x, name, shape, torch.int32, t.device)
+    return t.device, (t.data_ptr(), p.lens.data_ptr(), p.held.data_ptr(), p.refs.data_ptr(), p.free.data_ptr(),
+                      p.n_free.data_ptr(), R, P, int(p.page_size), MP)
+
+
+def _layers(k_cache, v_cache, device):
+    """(dtype code, n_layers, n_pages, page_size, H_kv, d_k, d_v) of [n_layers, n_pages, page_size,
+    H_kv, d] caches ([n_pages, page_size, H_kv, d]: one layer)."""
+    if k_cache.dim() not in (4, 5) or v_cache.dim() != k_cache.dim():
+        raise ValueError("k_cache and v_cache must both be [n_layers, n_pages, page_size, H_kv, d] or one layer of it")
+    shape = tuple(int(x) for x in k_cache.shape)
+    _need(k_cache, "k_cache", shape, k_cache.dtype, device)
+    _need(v_cache, "v_cache", shape[:-1] + (int(v_cache.shape[-1]),), k_cache.dtype, device)
+    L = shape[0] if len(shape) == 5 else 1
+    return (_dtype_code(k_cache), L) + shape[-4:] + (int(v_cache.shape[-1]),)
+
+
+def kv_reserve_t(pages: KVPages, rows, n_tokens, *, stream=None):
+    """Pages for ``n_tokens[i]`` more positions of row ``rows[i]`` (int32 [n]).
+    Returns status int32 [n]: 0 done, 1 no pages left, 2 refused."""
+    import torch
+    dev, args = _pages_args(pages)
+    n = int(rows.shape[0])
+    _need(rows, "rows", (n,), torch.int32, dev)
+    _need(n_tokens, "n_tokens", (n,), torch.int32, dev)
+    st = _stream_of(stream, dev)
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        status = torch.empty(n, dtype=torch.int32, device=dev)
+        _check(kv_reserve(*args, rows.data_ptr(), n_tokens.data_ptr(), n, status.data_ptr(), int(st.cuda_stream)))
+    return status
+
+
+def kv_free_t(pages: KVPages, rows, *, stream=None) -> None:
+    """Rows ``rows`` (int32 [n]) give up their pages and become unused."""
+    import torch
+    dev, args = _pages_args(pages)
+    n = int(rows.shape[0])
+    _need(rows, "rows", (n,), torch.int32, dev)
+    st = _stream_of(stream, dev)
+    with torch.cuda.device(dev):
+        _check(kv_free(*args, rows.data_ptr(), n, int(st.cuda_stream)))
+
+
+def kv_fork_t(pages: KVPages, src, dst, k_cache, v_cache, *, stream=None):
+    """Row ``dst[i]`` (unused) becomes a continuation of row ``src[i]`` (int32
+    [n]): full pages shared, the last one copied in every layer of the caches.
+    Returns status as ``kv_reserve_t`` does."""
+    import torch
+    dev, args = _pages_args(pages)
+    n = int(src.shape[0])
+    _need(src, "src", (n,), torch.int32, dev)
+    _need(dst, "dst", (n,), torch.int32, dev)
+    code, L, P, ps, Hkv, dk, dv = _layers(k_cache, v_cache, dev)
+    if (P, ps) != (args[7], args[8]):
+        raise ValueError(f"the caches have {P} pages of {ps} positions, the bookkeeping {args[7]} of {args[8]}")
+    st = _stream_of(stream, dev)
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        status = torch.empty(n, dtype=torch.int32, device=dev)
+        _check(kv_fork(*args, src.data_ptr(), dst.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(), L, Hkv, dk, dv,
+                       code, status.data_ptr(), int(st.cuda_stream)))
+    return status
+
+
+def kv_append_t(k, v, k_cache, v_cache, block_table, lens, cu_new=None, *, stream=None) -> None:
+    """Keys and values of new tokens into the cache: k [n_layers, T, H_kv, d_k]
+    and v [n_layers, T, H_kv, d_v] (one layer: [T, H_kv, d] with the caches of
+    that layer), token j of sequence n to position lens[n] + j through row n of
+    block_table; cu_new int32 [N + 1] (None: one token per sequence).  lens is
+    left as it is."""
+    import torch
+    if not k.is_cuda:
+        raise ValueError("the cache is on a GPU device; k is on the CPU")
+    dev = k.device
+    st = _stream_of(stream, dev)
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        code, L, P, ps, Hkv, dk, dv = _layers(k_cache, v_cache, dev)
+        lead = (L,) if k_cache.dim() == 5 else ()
+        T = int(k.shape[len(lead)])
+        N, MP = int(lens.shape[0]), int(block_table.shape[1])
+        if cu_new is None:
+            if T != N:
+                raise ValueError(f"without cu_new there is one token per sequence: {T} tokens, {N} sequences")
+            cu_new = torch.arange(N + 1, dtype=torch.int32, device=dev)
+        _need(k, "k", lead + (T, Hkv, dk), k_cache.dtype, dev)
+        _need(v, "v", lead + (T, Hkv, dv), k_cache.dtype, dev)
+        _need(block_table, "block_table", (N, MP), torch.int32, dev)
+        _need(lens, "lens", (N,), torch.int32, dev)
+        _need(cu_new, "cu_new", (N + 1,), torch.int32, dev)
+        _check(kv_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                         lens.data_ptr(), cu_new.data_ptr(), N, T, L, Hkv, dk, dv, P, ps, MP, code,
+                         int(st.cuda_stream)))
+
+
+def kv_compact_t(k_cache, v_cache, block_table, lens, accepted, cu_accepted, *, new_lens=None, stream=None):
+    """The accepted drafted tokens of every sequence move together behind its
+    committed positions (all layers): ``accepted`` int32 [A], their numbers in
+    the draft, rising, packed by ``cu_accepted`` int32 [N + 1].  Returns the
+    new lengths, int32 [N]."""
+    import torch
+    if not k_cache.is_cuda:
+        raise ValueError("the cache is on a GPU device; k_cache is on the CPU")
+    dev = k_cache.device
+    st = _stream_of(stream, dev)
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        code, L, P, ps, Hkv, dk, dv = _layers(k_cache, v_cache, dev)
+        N, MP, A = int(lens.shape[0]), int(block_table.shape[1]), int(accepted.shape[0])
+        _need(block_table, "block_table", (N, MP), torch.int32, dev)
+        _need(lens, "lens", (N,), torch.int32, dev)
+        _need(accepted, "accepted", (A,), torch.int32, dev)
+        _need(cu_accepted, "cu_accepted", (N + 1,), torch.int32, dev)
+        if new_lens is None:
+            new_lens = torch.empty(N, dtype=torch.int32, device=dev)
+        _need(new_lens, "new_lens", (N,), torch.int32, dev)
+        _check(kv_compact(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+                          accepted.data_ptr(), cu_accepted.data_ptr(), N, A, L, Hkv, dk, dv, P, ps, MP, code,
+                          new_lens.data_ptr(), int(st.cuda_stream)))
+    return new_lens

@@ -73,6 +73,12 @@ SIGNATURES = {
     "attn_tree_decode": (ctypes.c_int, [_vp, _vp, _vp, _ip, _ip, _ip, _vp, _i32, _i64, _i32, _i32, _i32, _i32, _i32,
                                         _i32, _i32, _i64, ctypes.c_float, ctypes.c_int, _vp, _fp, _vp, _sz, _vp]),
     "attn_tree_decode_workspace_size": (_sz, [_i32, _i64, _i32, _i32, _i32, _i32, _i32]),
+    "kv_reserve": (ctypes.c_int, [_ip] * 6 + [_i32] * 4 + [_ip, _ip, _i32, _ip, _vp]),
+    "kv_free": (ctypes.c_int, [_ip] * 6 + [_i32] * 4 + [_ip, _i32, _vp]),
+    "kv_fork": (ctypes.c_int, [_ip] * 6 + [_i32] * 4 + [_ip, _ip, _i32, _vp, _vp, _i32, _i32, _i32, _i32, ctypes.c_int,
+                                                        _ip, _vp]),
+    "kv_append": (ctypes.c_int, [_vp, _vp, _vp, _vp, _ip, _ip, _ip, _i32, _i64] + [_i32] * 7 + [ctypes.c_int, _vp]),
+    "kv_compact": (ctypes.c_int, [_vp, _vp, _ip, _ip, _ip, _ip, _i32, _i64] + [_i32] * 7 + [ctypes.c_int, _ip, _vp]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_last_error": (ctypes.c_char_p, []),
     "kda_version": (_i32, []),

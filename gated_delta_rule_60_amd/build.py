@@ -16,7 +16,7 @@ _CSRC = os.path.join(_HERE, "csrc")
 
 SOURCES = ["kda_api.cpp", "kda_prefill.hip", "kda_segment.hip", "kda_decode.hip", "kda_backward.hip",
            "kda_bwd_chunk.hip", "kda_noalloc.hip", "kda_anymap.hip", "attn_api.cpp", "attn_prefill.hip",
-           "attn_backward.hip", "attn_tree.hip"]
+           "attn_backward.hip", "attn_tree.hip", "kv_pages.hip"]
 ARCH = "gfx950"
 
 

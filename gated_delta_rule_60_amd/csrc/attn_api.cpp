@@ -199,3 +199,125 @@ kda_status attn_tree_decode(const void* q, const void* k_cache, const void* v_ca
 }
 
 }  // extern "C"
+
+namespace {
+
+constexpr int32_t kMaxRequests = 1024;  // of one bookkeeping call
+
+kda_status check_pages(const void* const* ptrs, int count, int32_t n_rows, int32_t n_pages, int32_t page_size, int32_t max_pages) {
+    kda::set_last_error("");
+    if (n_rows < 1) return fail(KDA_ERR_INVALID_ARG, "need n_rows >= 1");
+    const kda_status s = check_cache(n_pages, page_size, max_pages);
+    if (s != KDA_OK) return s;
+    for (int i = 0; i < count; ++i) {
+        if (!ptrs[i]) return fail(KDA_ERR_INVALID_ARG, "block_table, lens, held, refs, free_list, n_free and the requests must not be NULL");
+        if (!aligned(ptrs[i], 4)) return fail(KDA_ERR_INVALID_ARG, "int32 pointers must be 4-byte aligned");
+    }
+    return KDA_OK;
+}
+
+kda_status check_requests(int32_t n) {
+    if (n < 0 || n > kMaxRequests) return fail(KDA_ERR_INVALID_ARG, "n must lie in [0, 1024]");
+    return KDA_OK;
+}
+
+// The cache of all layers, its rows in 16-byte units.
+kda_status check_layers(const void* k_cache, const void* v_cache, int32_t n_layers, int32_t H_kv, int32_t d_k, int32_t d_v,
+                        kda_dtype dtype, kda::CacheArgs& c) {
+    const kda_status s = check_heads(H_kv, H_kv, d_k, d_v, dtype);
+    if (s != KDA_OK) return s;
+    if (n_layers < 1 || n_layers > 65535) return fail(KDA_ERR_INVALID_ARG, "n_layers must lie in [1, 65535]");
+    if (!k_cache || !v_cache) return fail(KDA_ERR_INVALID_ARG, "k_cache and v_cache must not be NULL");
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(KDA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+    const int64_t es = dtype == KDA_DTYPE_BF16 ? 2 : 4;
+    c.k_cache = const_cast<void*>(k_cache);
+    c.v_cache = const_cast<void*>(v_cache);
+    c.n_layers = n_layers;
+    c.k_row = H_kv * d_k * es / 16;
+    c.v_row = H_kv * d_v * es / 16;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kv_reserve(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* refs, int32_t* free_list, int32_t* n_free,
+                      int32_t n_rows, int32_t n_pages, int32_t page_size, int32_t max_pages, const int32_t* rows,
+                      const int32_t* n_tokens, int32_t n, int32_t* status, void* stream) {
+    const void* ptrs[] = {block_table, lens, held, refs, free_list, n_free, rows, n_tokens, status};
+    kda_status s = check_pages(ptrs, n > 0 ? 9 : 6, n_rows, n_pages, page_size, max_pages);
+    if (s != KDA_OK || (s = check_requests(n)) != KDA_OK) return s;
+    (void)hipGetLastError();
+    const hipError_t e = kda::launch_kv_reserve({block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size,
+                                                 __builtin_ctz(page_size), max_pages, stream}, rows, n_tokens, n, status);
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "page kernel launch");
+}
+
+kda_status kv_free(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* refs, int32_t* free_list, int32_t* n_free,
+                   int32_t n_rows, int32_t n_pages, int32_t page_size, int32_t max_pages, const int32_t* rows, int32_t n,
+                   void* stream) {
+    const void* ptrs[] = {block_table, lens, held, refs, free_list, n_free, rows};
+    kda_status s = check_pages(ptrs, n > 0 ? 7 : 6, n_rows, n_pages, page_size, max_pages);
+    if (s != KDA_OK || (s = check_requests(n)) != KDA_OK) return s;
+    if (static_cast<int64_t>(n) * max_pages > (int64_t{1} << 29))
+        return fail(KDA_ERR_INVALID_ARG, "n * max_pages must not exceed 2^29");
+    (void)hipGetLastError();
+    const hipError_t e = kda::launch_kv_free({block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size,
+                                              __builtin_ctz(page_size), max_pages, stream}, rows, n);
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "page kernel launch");
+}
+
+kda_status kv_fork(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* refs, int32_t* free_list, int32_t* n_free,
+                   int32_t n_rows, int32_t n_pages, int32_t page_size, int32_t max_pages, const int32_t* src, const int32_t* dst,
+                   int32_t n, void* k_cache, void* v_cache, int32_t n_layers, int32_t H_kv, int32_t d_k, int32_t d_v,
+                   kda_dtype dtype, int32_t* status, void* stream) {
+    const void* ptrs[] = {block_table, lens, held, refs, free_list, n_free, src, dst, status};
+    kda_status s = check_pages(ptrs, n > 0 ? 9 : 6, n_rows, n_pages, page_size, max_pages);
+    if (s != KDA_OK || (s = check_requests(n)) != KDA_OK) return s;
+    kda::CacheArgs c{};
+    if ((s = check_layers(k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, c)) != KDA_OK) return s;
+    (void)hipGetLastError();
+    const hipError_t e = kda::launch_kv_fork({block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size,
+                                              __builtin_ctz(page_size), max_pages, stream}, c, src, dst, n, status);
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "page kernel launch");
+}
+
+kda_status kv_append(const void* k, const void* v, void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* lens,
+                     const int32_t* cu_new, int32_t N, int64_t T_new, int32_t n_layers, int32_t H_kv, int32_t d_k, int32_t d_v,
+                     int32_t n_pages, int32_t page_size, int32_t max_pages, kda_dtype dtype, void* stream) {
+    const void* ptrs[] = {block_table, lens, cu_new};
+    kda_status s = check_pages(ptrs, 3, N, n_pages, page_size, max_pages);
+    if (s != KDA_OK) return s;
+    if (T_new < 0 || T_new > (int64_t{1} << 24)) return fail(KDA_ERR_INVALID_ARG, "T_new must lie in [0, 2^24]");
+    kda::CacheArgs c{};
+    if ((s = check_layers(k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, c)) != KDA_OK) return s;
+    if (T_new > 0 && (!k || !v)) return fail(KDA_ERR_INVALID_ARG, "k and v must not be NULL when T_new > 0");
+    if (!aligned(k, 16) || !aligned(v, 16)) return fail(KDA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+    c.k_new = k;
+    c.v_new = v;
+    (void)hipGetLastError();
+    const hipError_t e = kda::launch_kv_append({const_cast<int32_t*>(block_table), const_cast<int32_t*>(lens), nullptr, nullptr, nullptr,
+                                                nullptr, N, n_pages, page_size, __builtin_ctz(page_size), max_pages, stream},
+                                               c, cu_new, N, static_cast<int32_t>(T_new));
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "page kernel launch");
+}
+
+kda_status kv_compact(void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* lens, const int32_t* accepted,
+                      const int32_t* cu_accepted, int32_t N, int64_t A_tot, int32_t n_layers, int32_t H_kv, int32_t d_k, int32_t d_v,
+                      int32_t n_pages, int32_t page_size, int32_t max_pages, kda_dtype dtype, int32_t* new_lens, void* stream) {
+    const void* ptrs[] = {block_table, lens, cu_accepted, new_lens, accepted};
+    kda_status s = check_pages(ptrs, A_tot > 0 ? 5 : 4, N, n_pages, page_size, max_pages);
+    if (s != KDA_OK) return s;
+    if (A_tot < 0 || A_tot > (int64_t{1} << 24)) return fail(KDA_ERR_INVALID_ARG, "A_tot must lie in [0, 2^24]");
+    if (new_lens == lens) return fail(KDA_ERR_INVALID_ARG, "new_lens must not be lens: every layer's work reads it");
+    kda::CacheArgs c{};
+    if ((s = check_layers(k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, c)) != KDA_OK) return s;
+    (void)hipGetLastError();
+    const hipError_t e = kda::launch_kv_compact({const_cast<int32_t*>(block_table), const_cast<int32_t*>(lens), nullptr, nullptr, nullptr,
+                                                 nullptr, N, n_pages, page_size, __builtin_ctz(page_size), max_pages, stream},
+                                                c, accepted, cu_accepted, N, static_cast<int32_t>(A_tot), new_lens);
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "page kernel launch");
+}
+
+}  // extern "C"

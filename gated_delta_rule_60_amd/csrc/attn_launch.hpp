@@ -72,6 +72,37 @@ struct TreePlan {
 TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus);
 hipError_t launch_attn_tree(TreeArgs a, const TreePlan& p);
 
+// The pages of a cache: block table rows and what is kept about them.  Calls
+// that only read the table and the lengths leave the rest null.
+struct PageArgs {
+    int32_t* table;   // [n_rows, max_pages]
+    int32_t* lens;    // [n_rows]
+    int32_t* held;    // [n_rows] pages of a row
+    int32_t* refs;    // [n_pages] rows that hold a page
+    int32_t* free;    // [n_pages] free pages, n_free of them
+    int32_t* n_free;  // [1]
+    int32_t n_rows, n_pages, page_size, page_shift, max_pages;
+    void* stream;
+};
+
+// The cache [n_layers, n_pages, page_size, row] and new tokens [n_layers, tokens, row]; rows in
+// 16-byte units.
+struct CacheArgs {
+    void* k_cache;
+    void* v_cache;
+    const void* k_new;
+    const void* v_new;
+    int32_t n_layers;
+    int64_t k_row, v_row;
+};
+
+hipError_t launch_kv_reserve(const PageArgs& a, const int32_t* rows, const int32_t* n_tokens, int n, int32_t* status);
+hipError_t launch_kv_free(const PageArgs& a, const int32_t* rows, int n);
+hipError_t launch_kv_fork(const PageArgs& a, const CacheArgs& c, const int32_t* src, const int32_t* dst, int n, int32_t* status);
+hipError_t launch_kv_append(const PageArgs& a, const CacheArgs& c, const int32_t* cu_new, int N, int T_new);
+hipError_t launch_kv_compact(const PageArgs& a, const CacheArgs& c, const int32_t* accepted, const int32_t* cu_accepted, int N,
+                             int A_tot, int32_t* new_lens);
+
 hipError_t launch_attn_prefill(const AttnArgs& a);
 hipError_t launch_attn_bwd(const AttnBwdArgs& a);
 size_t attn_bwd_workspace_bytes(int64_t T_tot, int32_t Hq);

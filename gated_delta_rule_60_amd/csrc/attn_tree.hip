@@ -427,7 +427,7 @@ __global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW)) void at
     if (lane == 0) sp[wave] = poisoned;
     if constexpr (KW > 1) {
 #pragma unroll
-        for (int w = KW >> 1; w > 0; w >>= 1) {
+        for (int w = KW / 2; w >= 1; w /= 2) {
             if (w < KW / 2) __syncthreads();
             if (kw >= w && kw < 2 * w) {
 #pragma unroll

@@ -519,6 +519,91 @@ kda_status attn_tree_decode(const void* q, const void* k_cache, const void* v_ca
 size_t attn_tree_decode_workspace_size(int32_t N, int64_t T_q, int32_t H_q, int32_t H_kv,
                                        int32_t d_v, int32_t page_size, int32_t max_pages);
 
+/*
+ * The pages of such a cache are kept in six int32 arrays on the device, owned
+ * by the caller and shared by every layer:
+ *
+ *   block_table [n_rows, max_pages]  a row is a sequence (or an unused slot);
+ *               entries from held[row] on are -1
+ *   lens        [n_rows]   its committed positions
+ *   held        [n_rows]   its pages
+ *   refs        [n_pages]  how many rows hold a page
+ *   free_list   [n_pages]  the pages nobody holds come first, n_free of them;
+ *               they are taken from the end and given back to it
+ *   n_free      [1]
+ *
+ * and the caches of all layers are [n_layers, n_pages, page_size, H_kv, d].
+ * Calls of one cache must be ordered on the device (one stream, or events).
+ * A bookkeeping call takes up to 1024 requests, and its outcome is that of
+ * the requests one after another, pages taken in their order; of several
+ * requests for one row the first counts.  status[i]: 0 done; 1 not enough
+ * free pages were left (nothing changed for this request, nor for any later
+ * one that needs pages); 2 refused (a row outside the table, a repeated one,
+ * a negative number, more than max_pages).
+ *
+ * kv_reserve -- row rows[i] gets the pages that lens + n_tokens[i] positions
+ * need beyond the ones it holds.
+ */
+kda_status kv_reserve(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* refs,
+                      int32_t* free_list, int32_t* n_free, int32_t n_rows, int32_t n_pages,
+                      int32_t page_size, int32_t max_pages, const int32_t* rows,
+                      const int32_t* n_tokens, int32_t n, int32_t* status, void* stream);
+
+/*
+ * kv_free -- row rows[i] gives up its pages and becomes unused (lens and held
+ * 0).  Pages that no row holds any more are added to the free list, in the
+ * order of the requests and of the row's pages.  Rows outside the table and
+ * repeated ones are passed over.  n * max_pages <= 2^29.
+ */
+kda_status kv_free(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* refs,
+                   int32_t* free_list, int32_t* n_free, int32_t n_rows, int32_t n_pages,
+                   int32_t page_size, int32_t max_pages, const int32_t* rows, int32_t n,
+                   void* stream);
+
+/*
+ * kv_fork -- row dst[i], which holds nothing, becomes a continuation of row
+ * src[i]: it shares the pages that src's committed positions fill, and gets a
+ * page of its own with a copy of the positions of the last, partly filled one
+ * (in every layer; the rest of that page stays as it was).  Also refused
+ * (status 2): a dst that holds pages, a src that is the dst of any request of
+ * the call, a src that holds fewer pages than its positions need.
+ */
+kda_status kv_fork(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* refs,
+                   int32_t* free_list, int32_t* n_free, int32_t n_rows, int32_t n_pages,
+                   int32_t page_size, int32_t max_pages, const int32_t* src, const int32_t* dst,
+                   int32_t n, void* k_cache, void* v_cache, int32_t n_layers, int32_t H_kv,
+                   int32_t d_k, int32_t d_v, kda_dtype dtype, int32_t* status, void* stream);
+
+/*
+ * kv_append -- the keys and values of new tokens into the cache: k [n_layers,
+ * T_new, H_kv, d_k] and v [n_layers, T_new, H_kv, d_v] (16-byte aligned),
+ * packed by sequence (cu_new [N + 1]); token j of sequence n (row n of the
+ * table) goes to position lens[n] + j.  lens stays as it is: drafted tokens
+ * lie behind it until they are accepted.  Tokens at or past cu_new[N], and
+ * positions without a page, are passed over.  A page that several rows share
+ * is written all the same: kv_fork gives every row a last page of its own.
+ */
+kda_status kv_append(const void* k, const void* v, void* k_cache, void* v_cache,
+                     const int32_t* block_table, const int32_t* lens, const int32_t* cu_new,
+                     int32_t N, int64_t T_new, int32_t n_layers, int32_t H_kv, int32_t d_k,
+                     int32_t d_v, int32_t n_pages, int32_t page_size, int32_t max_pages,
+                     kda_dtype dtype, void* stream);
+
+/*
+ * kv_compact -- the accepted ones of a sequence's drafted tokens move together
+ * behind its committed positions: drafted token accepted[cu_accepted[n] + i]
+ * (counted within the sequence, rising) goes from position lens[n] +
+ * accepted to lens[n] + i, in every layer, and new_lens[n] = lens[n] + their
+ * number.  The list of a sequence ends early at an entry that does not rise
+ * or has no page.  new_lens [N] must not be lens itself.  Sequences may not
+ * share the pages of their drafted positions.
+ */
+kda_status kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
+                      const int32_t* lens, const int32_t* accepted, const int32_t* cu_accepted,
+                      int32_t N, int64_t A_tot, int32_t n_layers, int32_t H_kv, int32_t d_k,
+                      int32_t d_v, int32_t n_pages, int32_t page_size, int32_t max_pages,
+                      kda_dtype dtype, int32_t* new_lens, void* stream);
+
 /* Static text for a status code. */
 const char* kda_status_string(kda_status status);
 

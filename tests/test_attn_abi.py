@@ -159,6 +159,47 @@ def test_tree_masks():
             kda.attn_tree_masks([bad])
 
 
+_BOOK = dict(block_table=FAKE, lens=FAKE, held=FAKE, refs=FAKE, free_list=FAKE, n_free=FAKE, n_rows=8, n_pages=100,
+             page_size=16, max_pages=32)
+_LAYERS = dict(k_cache=FAKE, v_cache=FAKE, n_layers=2, H_kv=2, d_k=64, d_v=128, dtype=BF16)
+_CALLS = {
+    "kv_reserve": dict(_BOOK, rows=FAKE, n_tokens=FAKE, n=4, status=FAKE, stream=None),
+    "kv_free": dict(_BOOK, rows=FAKE, n=4, stream=None),
+    "kv_fork": dict(_BOOK, **_LAYERS, src=FAKE, dst=FAKE, n=4, status=FAKE, stream=None),
+    "kv_append": dict(_LAYERS, k=FAKE, v=FAKE, block_table=FAKE, lens=FAKE, cu_new=FAKE, N=4, T_new=9, n_pages=100,
+                      page_size=16, max_pages=32, stream=None),
+    "kv_compact": dict(_LAYERS, block_table=FAKE, lens=FAKE, accepted=FAKE, cu_accepted=FAKE, N=4, A_tot=9, n_pages=100,
+                       page_size=16, max_pages=32, new_lens=FAKE + 64, stream=None),
+}
+_SOME_ROWS = [(dict(n=-1), BAD, "1024"), (dict(n=1025), BAD, "1024"), (dict(n_rows=0), BAD, "n_rows"),
+              (dict(held=None), BAD, "must not be NULL"), (dict(n_free=FAKE + 2), BAD, "4-byte aligned")]
+_SOME_LAYERS = [(dict(n_layers=0), BAD, "n_layers"), (dict(n_layers=65536), BAD, "n_layers"), (dict(d_k=40), NOT, "d_k and d_v"),
+                (dict(dtype=9), NOT, "dtype"), (dict(H_kv=0), BAD, "H_kv"), (dict(k_cache=None), BAD, "must not be NULL"),
+                (dict(v_cache=FAKE + 8), BAD, "16-byte aligned")]
+
+
+@pytest.mark.parametrize("call,kw,status,needle", [
+    (call, *rest) for call in _CALLS for rest in
+    CACHE + (_SOME_ROWS if "n" in _CALLS[call] else []) + (_SOME_LAYERS if "n_layers" in _CALLS[call] else [])] + [
+    ("kv_reserve", dict(n_tokens=None), BAD, "must not be NULL"),
+    ("kv_reserve", dict(status=None), BAD, "must not be NULL"),
+    ("kv_free", dict(rows=None), BAD, "must not be NULL"),
+    ("kv_free", dict(n=1024, max_pages=(1 << 19) + 1), BAD, "2^29"),
+    ("kv_fork", dict(dst=None), BAD, "must not be NULL"),
+    ("kv_append", dict(T_new=-1), BAD, "T_new"),
+    ("kv_append", dict(T_new=(1 << 24) + 1), BAD, "T_new"),
+    ("kv_append", dict(N=0), BAD, "n_rows"),
+    ("kv_append", dict(k=None), BAD, "must not be NULL"),
+    ("kv_append", dict(v=FAKE + 8), BAD, "16-byte aligned"),
+    ("kv_compact", dict(A_tot=-1), BAD, "A_tot"),
+    ("kv_compact", dict(accepted=None), BAD, "must not be NULL"),
+    ("kv_compact", dict(new_lens=FAKE), BAD, "must not be lens"),
+])
+def test_page_calls_refuse(call, kw, status, needle):
+    assert getattr(kda, call)(**dict(_CALLS[call], **kw)) == status
+    assert needle in kda.kda_last_error()
+
+
 def test_nothing_to_do_is_done():
     assert _prefill(T_tot=0, q=None, k=None, v=None, o=None, lse=None) == kda.KDA_OK
     assert kda.kda_last_error() == ""
