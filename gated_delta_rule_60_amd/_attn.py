@@ -14,7 +14,7 @@ import dataclasses
 import math
 from typing import Any
 
-from ._lib import _check, _dtype_code, _need, _stream_of, load
+from ._lib import _check, _dtype_code, _stream_of, load
 
 
 # ---------------------------------------------------------------------------
@@ -81,12 +81,43 @@ def kv_compact(k_cache, v_cache, block_table, lens, accepted, cu_accepted, N, A_
 # ---------------------------------------------------------------------------
 # torch conveniences (marshalling only)
 # ---------------------------------------------------------------------------
+# A call's own cost counts where its kernels take microseconds: on the current
+# device and stream it enters no context, and a dense tensor is checked by one
+# comparison of each property.
+def _on_stream(stream, dev, body, *args):
+    """body(*args, stream handle) with outputs and temporaries allocated under that stream."""
+    import torch
+    if stream is None and dev.index == torch.cuda.current_device():
+        return body(*args, torch._C._cuda_getCurrentRawStream(dev.index))  # 0.1 us; current_stream() is 1.8
+    st = _stream_of(stream, dev)
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        return body(*args, st.cuda_stream)
+
+
+def _need(t, name, shape, dtype, device):
+    """A dense tensor of this shape, type and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _gpu(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"the attention and cache calls run on a GPU device; {name} is on the CPU")
+    return t.device
+
+
 def _tokens(t, name, shape, dtype, device) -> int:
     """Check a [tokens, heads, size] tensor whose tokens are contiguous blocks;
     returns the elements between tokens."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -96,7 +127,30 @@ def _tokens(t, name, shape, dtype, device) -> int:
         return h * d
     if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
         raise ValueError(f"the heads of a token of {name} must be contiguous (strides {s})")
-    return int(s[0]) if n > 1 else max(h * d, 8)
+    return s[0] if n > 1 else h * d
+
+
+def _scale(scale, d_k) -> float:
+    return 1.0 / math.sqrt(d_k) if scale is None else float(scale)
+
+
+def _prompt_args(q, k, v, cu_seqlens):
+    """Checks shared by the forward and backward; returns (cu_seqlens, N, T, H_q, H_kv, d_k, d_v, strides, dtype code)."""
+    import torch
+    dev = q.device
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, size]")
+    T, Hq, dk = q.shape
+    Hkv, dv = k.shape[1], v.shape[2]
+    code = _dtype_code(q)
+    if cu_seqlens is None:
+        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
+    N = cu_seqlens.shape[0] - 1
+    dt = q.dtype
+    strides = (_tokens(q, "q", (T, Hq, dk), dt, dev), _tokens(k, "k", (T, Hkv, dk), dt, dev),
+               _tokens(v, "v", (T, Hkv, dv), dt, dev))
+    _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
+    return cu_seqlens, N, T, Hq, Hkv, dk, dv, strides, code
 
 
 def attn_prefill_t(q, k, v, cu_seqlens=None, *, scale=None, o=None, lse=None, stream=None):
@@ -106,71 +160,57 @@ def attn_prefill_t(q, k, v, cu_seqlens=None, *, scale=None, o=None, lse=None, st
     type; slices of a fused projection are taken as they are); cu_seqlens:
     int32 [N + 1] on the device (None = one sequence); ``scale``: 1 / sqrt(d_k)
     if None.  o: [T, H_q, d_v] in q's dtype; lse: [T, H_q] fp32."""
+    return _on_stream(stream, _gpu(q, "q"), _attn_prefill_on, q, k, v, cu_seqlens, scale, o, lse)
+
+
+def _attn_prefill_on(q, k, v, cu_seqlens, scale, o, lse, stream):
     import torch
-    if not q.is_cuda:
-        raise ValueError("attention runs on a GPU device; q is on the CPU")
     dev = q.device
-    st = _stream_of(stream, dev)
-    with torch.cuda.device(dev), torch.cuda.stream(st):
-        T, Hq, dk = (int(x) for x in q.shape)
-        Hkv, dv = int(k.shape[1]), int(v.shape[2])
-        code = _dtype_code(q)
-        if cu_seqlens is None:
-            cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
-        N = int(cu_seqlens.shape[0]) - 1
-        qs = _tokens(q, "q", (T, Hq, dk), q.dtype, dev)
-        ks = _tokens(k, "k", (T, Hkv, dk), q.dtype, dev)
-        vs = _tokens(v, "v", (T, Hkv, dv), q.dtype, dev)
-        _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
-        if o is None:
-            o = torch.empty((T, Hq, dv), dtype=q.dtype, device=dev)
-        if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    cu_seqlens, N, T, Hq, Hkv, dk, dv, strides, code = _prompt_args(q, k, v, cu_seqlens)
+    if o is None:
+        o = torch.empty((T, Hq, dv), dtype=q.dtype, device=dev)
+    else:
         _need(o, "o", (T, Hq, dv), q.dtype, dev)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
         _need(lse, "lse", (T, Hq), torch.float32, dev)
-        _check(attn_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), N, T, Hq, Hkv, dk, dv,
-                            qs, ks, vs, 1.0 / math.sqrt(dk) if scale is None else float(scale), code, o.data_ptr(),
-                            lse.data_ptr(), int(st.cuda_stream)))
+    _check(attn_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), N, T, Hq, Hkv, dk, dv,
+                        *strides, _scale(scale, dk), code, o.data_ptr(), lse.data_ptr(), stream))
     return o, lse
+
+
+def _workspace(workspace, need, dev):
+    import torch
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    return workspace
 
 
 def attn_prefill_backward_t(q, k, v, o, lse, d_o, cu_seqlens=None, *, scale=None, workspace=None, stream=None):
     """Backward of ``attn_prefill_t``: gradients (d_q, d_k, d_v), shaped and
     typed like q, k and v, of a loss given d_o = dL/do and the forward's o and
     lse.  ``workspace``: optional uint8 device tensor of at least
-    ``attn_prefill_backward_workspace_size(T, H_q)`` bytes."""
+    ``attn_prefill_backward_workspace_size(...)`` bytes."""
+    return _on_stream(stream, _gpu(q, "q"), _attn_backward_on, q, k, v, o, lse, d_o, cu_seqlens, scale, workspace)
+
+
+def _attn_backward_on(q, k, v, o, lse, d_o, cu_seqlens, scale, workspace, stream):
     import torch
-    if not q.is_cuda:
-        raise ValueError("attention runs on a GPU device; q is on the CPU")
     dev = q.device
-    st = _stream_of(stream, dev)
-    with torch.cuda.device(dev), torch.cuda.stream(st):
-        T, Hq, dk = (int(x) for x in q.shape)
-        Hkv, dv = int(k.shape[1]), int(v.shape[2])
-        code = _dtype_code(q)
-        if cu_seqlens is None:
-            cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
-        N = int(cu_seqlens.shape[0]) - 1
-        qs = _tokens(q, "q", (T, Hq, dk), q.dtype, dev)
-        ks = _tokens(k, "k", (T, Hkv, dk), q.dtype, dev)
-        vs = _tokens(v, "v", (T, Hkv, dv), q.dtype, dev)
-        _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
-        _need(o, "o", (T, Hq, dv), q.dtype, dev)
-        _need(lse, "lse", (T, Hq), torch.float32, dev)
-        _need(d_o, "d_o", (T, Hq, dv), q.dtype, dev)
-        d_q = torch.empty((T, Hq, dk), dtype=q.dtype, device=dev)
-        d_k = torch.empty((T, Hkv, dk), dtype=q.dtype, device=dev)
-        d_v = torch.empty((T, Hkv, dv), dtype=q.dtype, device=dev)
-        ws = attn_prefill_backward_workspace_size(T, Hq)
-        if workspace is None:
-            workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
-        elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-        _check(attn_prefill_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                     d_o.data_ptr(), cu_seqlens.data_ptr(), N, T, Hq, Hkv, dk, dv, qs, ks, vs,
-                                     1.0 / math.sqrt(dk) if scale is None else float(scale), code, d_q.data_ptr(),
-                                     d_k.data_ptr(), d_v.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                     int(st.cuda_stream)))
+    cu_seqlens, N, T, Hq, Hkv, dk, dv, strides, code = _prompt_args(q, k, v, cu_seqlens)
+    _need(o, "o", (T, Hq, dv), q.dtype, dev)
+    _need(lse, "lse", (T, Hq), torch.float32, dev)
+    _need(d_o, "d_o", (T, Hq, dv), q.dtype, dev)
+    d_q = torch.empty((T, Hq, dk), dtype=q.dtype, device=dev)
+    d_k = torch.empty((T, Hkv, dk), dtype=q.dtype, device=dev)
+    d_v = torch.empty((T, Hkv, dv), dtype=q.dtype, device=dev)
+    ws = _workspace(workspace, attn_prefill_backward_workspace_size(T, Hq), dev)
+    _check(attn_prefill_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), d_o.data_ptr(),
+                                 cu_seqlens.data_ptr(), N, T, Hq, Hkv, dk, dv, *strides, _scale(scale, dk), code,
+                                 d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(), ws.data_ptr(), ws.numel(), stream))
     return d_q, d_k, d_v
 
 
@@ -196,8 +236,8 @@ def attn_tree_masks(parents):
 def _cache_shape(k_cache, v_cache, dtype, device):
     if k_cache.dim() != 4 or v_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [n_pages, page_size, H_kv, d]")
-    P, ps, Hkv, dk = (int(x) for x in k_cache.shape)
-    dv = int(v_cache.shape[3])
+    P, ps, Hkv, dk = k_cache.shape
+    dv = v_cache.shape[3]
     _need(k_cache, "k_cache", (P, ps, Hkv, dk), dtype, device)
     _need(v_cache, "v_cache", (P, ps, Hkv, dv), dtype, device)
     return P, ps, Hkv, dk, dv
@@ -215,44 +255,44 @@ def attn_tree_decode_t(q, k_cache, v_cache, block_table, ctx_lens, cu_q=None, tr
     token's mask set if it sees drafted position j (None: the ones up to
     itself; ``attn_tree_masks`` builds it).  ``workspace``: optional uint8
     device tensor of ``attn_tree_decode_workspace_size`` bytes."""
+    return _on_stream(stream, _gpu(q, "q"), _attn_tree_on, q, k_cache, v_cache, block_table, ctx_lens, cu_q, tree_mask,
+                      scale, o, lse, workspace)
+
+
+def _attn_tree_on(q, k_cache, v_cache, block_table, ctx_lens, cu_q, tree_mask, scale, o, lse, workspace, stream):
     import torch
-    if not q.is_cuda:
-        raise ValueError("attention runs on a GPU device; q is on the CPU")
     dev = q.device
-    st = _stream_of(stream, dev)
-    with torch.cuda.device(dev), torch.cuda.stream(st):
-        T, Hq, dk = (int(x) for x in q.shape)
-        code = _dtype_code(q)
-        P, ps, Hkv, _, dv = _cache_shape(k_cache, v_cache, q.dtype, dev)
-        _need(k_cache, "k_cache", (P, ps, Hkv, dk), q.dtype, dev)
-        N = int(ctx_lens.shape[0])
-        if cu_q is None:
-            if T != N:
-                raise ValueError(f"without cu_q there is one token per sequence: {T} tokens, {N} sequences")
-            cu_q = torch.arange(N + 1, dtype=torch.int32, device=dev)
-        MP = int(block_table.shape[1])
-        qs = _tokens(q, "q", (T, Hq, dk), q.dtype, dev)
-        _need(block_table, "block_table", (N, MP), torch.int32, dev)
-        _need(ctx_lens, "ctx_lens", (N,), torch.int32, dev)
-        _need(cu_q, "cu_q", (N + 1,), torch.int32, dev)
-        if tree_mask is not None:
-            _need(tree_mask, "tree_mask", (T,), torch.int64, dev)
-        if o is None:
-            o = torch.empty((T, Hq, dv), dtype=q.dtype, device=dev)
-        if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [tokens, heads, size] and block_table [N, max_pages]")
+    T, Hq, dk = q.shape
+    code = _dtype_code(q)
+    P, ps, Hkv, dk_cache, dv = _cache_shape(k_cache, v_cache, q.dtype, dev)
+    if dk_cache != dk:
+        raise ValueError(f"k_cache holds keys of {dk_cache}, q has {dk}")
+    N, MP = ctx_lens.shape[0], block_table.shape[1]
+    if cu_q is None:
+        if T != N:
+            raise ValueError(f"without cu_q there is one token per sequence: {T} tokens, {N} sequences")
+        cu_q = torch.arange(N + 1, dtype=torch.int32, device=dev)
+    qs = _tokens(q, "q", (T, Hq, dk), q.dtype, dev)
+    _need(block_table, "block_table", (N, MP), torch.int32, dev)
+    _need(ctx_lens, "ctx_lens", (N,), torch.int32, dev)
+    _need(cu_q, "cu_q", (N + 1,), torch.int32, dev)
+    if tree_mask is not None:
+        _need(tree_mask, "tree_mask", (T,), torch.int64, dev)
+    if o is None:
+        o = torch.empty((T, Hq, dv), dtype=q.dtype, device=dev)
+    else:
         _need(o, "o", (T, Hq, dv), q.dtype, dev)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
         _need(lse, "lse", (T, Hq), torch.float32, dev)
-        if workspace is None:
-            ws = attn_tree_decode_workspace_size(N, T, Hq, Hkv, dv, ps, MP)
-            workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
-        elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-        _check(attn_tree_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                ctx_lens.data_ptr(), cu_q.data_ptr(),
-                                tree_mask.data_ptr() if tree_mask is not None else None, N, T, Hq, Hkv, dk, dv, P, ps,
-                                MP, qs, 1.0 / math.sqrt(dk) if scale is None else float(scale), code, o.data_ptr(),
-                                lse.data_ptr(), workspace.data_ptr(), workspace.numel(), int(st.cuda_stream)))
+    ws = _workspace(workspace, attn_tree_decode_workspace_size(N, T, Hq, Hkv, dv, ps, MP), dev)
+    _check(attn_tree_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                            ctx_lens.data_ptr(), cu_q.data_ptr(), tree_mask.data_ptr() if tree_mask is not None else None,
+                            N, T, Hq, Hkv, dk, dv, P, ps, MP, qs, _scale(scale, dk), code, o.data_ptr(), lse.data_ptr(),
+                            ws.data_ptr(), ws.numel(), stream))
     return o, lse
 
 
@@ -289,16 +329,24 @@ def _pages_args(p: KVPages):
     """Check the six tensors; returns (device, the C calls' leading arguments)."""
     import torch
     t = p.table
-    if not t.is_cuda:
-        raise ValueError("the cache's pages are kept on a GPU device; table is on the CPU")
+    dev = _gpu(t, "table")
     if t.dim() != 2 or p.refs.dim() != 1:
         raise ValueError("table must be [rows, max_pages] and refs [n_pages]")
-    R, MP, P = int(t.shape[0]), int(t.shape[1]), int(p.refs.shape[0])
+    (R, MP), P = t.shape, p.refs.shape[0]
     for x, name, shape in ((t, "table", (R, MP)), (p.lens, "lens", (R,)), (p.held, "held", (R,)),
                            (p.refs, "refs", (P,)), (p.free, "free", (P,)), (p.n_free, "n_free", (1,))):
-        _need(x, name, shape, torch.int32, t.device)
-    return t.device, (t.data_ptr(), p.lens.data_ptr(), p.held.data_ptr(), p.refs.data_ptr(), p.free.data_ptr(),
-                      p.n_free.data_ptr(), R, P, int(p.page_size), MP)
+        _need(x, name, shape, torch.int32, dev)
+    return dev, (t.data_ptr(), p.lens.data_ptr(), p.held.data_ptr(), p.refs.data_ptr(), p.free.data_ptr(),
+                 p.n_free.data_ptr(), R, P, int(p.page_size), MP)
+
+
+def _requests(dev, **lists):
+    import torch
+    n = None
+    for name, t in lists.items():
+        n = t.shape[0] if n is None else n
+        _need(t, name, (n,), torch.int32, dev)
+    return n
 
 
 def _layers(k_cache, v_cache, device):
@@ -306,56 +354,55 @@ def _layers(k_cache, v_cache, device):
     H_kv, d] caches ([n_pages, page_size, H_kv, d]: one layer)."""
     if k_cache.dim() not in (4, 5) or v_cache.dim() != k_cache.dim():
         raise ValueError("k_cache and v_cache must both be [n_layers, n_pages, page_size, H_kv, d] or one layer of it")
-    shape = tuple(int(x) for x in k_cache.shape)
+    shape, dv = k_cache.shape, v_cache.shape[-1]
     _need(k_cache, "k_cache", shape, k_cache.dtype, device)
-    _need(v_cache, "v_cache", shape[:-1] + (int(v_cache.shape[-1]),), k_cache.dtype, device)
-    L = shape[0] if len(shape) == 5 else 1
-    return (_dtype_code(k_cache), L) + shape[-4:] + (int(v_cache.shape[-1]),)
+    _need(v_cache, "v_cache", (*shape[:-1], dv), k_cache.dtype, device)
+    return (_dtype_code(k_cache), shape[0] if len(shape) == 5 else 1, *shape[-4:], dv)
 
 
 def kv_reserve_t(pages: KVPages, rows, n_tokens, *, stream=None):
     """Pages for ``n_tokens[i]`` more positions of row ``rows[i]`` (int32 [n]).
     Returns status int32 [n]: 0 done, 1 no pages left, 2 refused."""
+    return _on_stream(stream, _gpu(pages.table, "table"), _kv_reserve_on, pages, rows, n_tokens)
+
+
+def _kv_reserve_on(pages, rows, n_tokens, stream):
     import torch
     dev, args = _pages_args(pages)
-    n = int(rows.shape[0])
-    _need(rows, "rows", (n,), torch.int32, dev)
-    _need(n_tokens, "n_tokens", (n,), torch.int32, dev)
-    st = _stream_of(stream, dev)
-    with torch.cuda.device(dev), torch.cuda.stream(st):
-        status = torch.empty(n, dtype=torch.int32, device=dev)
-        _check(kv_reserve(*args, rows.data_ptr(), n_tokens.data_ptr(), n, status.data_ptr(), int(st.cuda_stream)))
+    n = _requests(dev, rows=rows, n_tokens=n_tokens)
+    status = torch.empty(n, dtype=torch.int32, device=dev)
+    _check(kv_reserve(*args, rows.data_ptr(), n_tokens.data_ptr(), n, status.data_ptr(), stream))
     return status
 
 
 def kv_free_t(pages: KVPages, rows, *, stream=None) -> None:
     """Rows ``rows`` (int32 [n]) give up their pages and become unused."""
-    import torch
+    return _on_stream(stream, _gpu(pages.table, "table"), _kv_free_on, pages, rows)
+
+
+def _kv_free_on(pages, rows, stream):
     dev, args = _pages_args(pages)
-    n = int(rows.shape[0])
-    _need(rows, "rows", (n,), torch.int32, dev)
-    st = _stream_of(stream, dev)
-    with torch.cuda.device(dev):
-        _check(kv_free(*args, rows.data_ptr(), n, int(st.cuda_stream)))
+    n = _requests(dev, rows=rows)
+    _check(kv_free(*args, rows.data_ptr(), n, stream))
 
 
 def kv_fork_t(pages: KVPages, src, dst, k_cache, v_cache, *, stream=None):
     """Row ``dst[i]`` (unused) becomes a continuation of row ``src[i]`` (int32
     [n]): full pages shared, the last one copied in every layer of the caches.
     Returns status as ``kv_reserve_t`` does."""
+    return _on_stream(stream, _gpu(pages.table, "table"), _kv_fork_on, pages, src, dst, k_cache, v_cache)
+
+
+def _kv_fork_on(pages, src, dst, k_cache, v_cache, stream):
     import torch
     dev, args = _pages_args(pages)
-    n = int(src.shape[0])
-    _need(src, "src", (n,), torch.int32, dev)
-    _need(dst, "dst", (n,), torch.int32, dev)
+    n = _requests(dev, src=src, dst=dst)
     code, L, P, ps, Hkv, dk, dv = _layers(k_cache, v_cache, dev)
     if (P, ps) != (args[7], args[8]):
         raise ValueError(f"the caches have {P} pages of {ps} positions, the bookkeeping {args[7]} of {args[8]}")
-    st = _stream_of(stream, dev)
-    with torch.cuda.device(dev), torch.cuda.stream(st):
-        status = torch.empty(n, dtype=torch.int32, device=dev)
-        _check(kv_fork(*args, src.data_ptr(), dst.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(), L, Hkv, dk, dv,
-                       code, status.data_ptr(), int(st.cuda_stream)))
+    status = torch.empty(n, dtype=torch.int32, device=dev)
+    _check(kv_fork(*args, src.data_ptr(), dst.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(), L, Hkv, dk, dv, code,
+                   status.data_ptr(), stream))
     return status
 
 
@@ -365,28 +412,28 @@ def kv_append_t(k, v, k_cache, v_cache, block_table, lens, cu_new=None, *, strea
     that layer), token j of sequence n to position lens[n] + j through row n of
     block_table; cu_new int32 [N + 1] (None: one token per sequence).  lens is
     left as it is."""
+    return _on_stream(stream, _gpu(k, "k"), _kv_append_on, k, v, k_cache, v_cache, block_table, lens, cu_new)
+
+
+def _kv_append_on(k, v, k_cache, v_cache, block_table, lens, cu_new, stream):
     import torch
-    if not k.is_cuda:
-        raise ValueError("the cache is on a GPU device; k is on the CPU")
     dev = k.device
-    st = _stream_of(stream, dev)
-    with torch.cuda.device(dev), torch.cuda.stream(st):
-        code, L, P, ps, Hkv, dk, dv = _layers(k_cache, v_cache, dev)
-        lead = (L,) if k_cache.dim() == 5 else ()
-        T = int(k.shape[len(lead)])
-        N, MP = int(lens.shape[0]), int(block_table.shape[1])
-        if cu_new is None:
-            if T != N:
-                raise ValueError(f"without cu_new there is one token per sequence: {T} tokens, {N} sequences")
-            cu_new = torch.arange(N + 1, dtype=torch.int32, device=dev)
-        _need(k, "k", lead + (T, Hkv, dk), k_cache.dtype, dev)
-        _need(v, "v", lead + (T, Hkv, dv), k_cache.dtype, dev)
-        _need(block_table, "block_table", (N, MP), torch.int32, dev)
-        _need(lens, "lens", (N,), torch.int32, dev)
-        _need(cu_new, "cu_new", (N + 1,), torch.int32, dev)
-        _check(kv_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                         lens.data_ptr(), cu_new.data_ptr(), N, T, L, Hkv, dk, dv, P, ps, MP, code,
-                         int(st.cuda_stream)))
+    code, L, P, ps, Hkv, dk, dv = _layers(k_cache, v_cache, dev)
+    lead = (L,) if k_cache.dim() == 5 else ()
+    if k.dim() != 3 + len(lead) or block_table.dim() != 2:
+        raise ValueError("k must be [n_layers, T, H_kv, d_k] (one layer: [T, H_kv, d_k]) and block_table [N, max_pages]")
+    T, N, MP = k.shape[len(lead)], lens.shape[0], block_table.shape[1]
+    if cu_new is None:
+        if T != N:
+            raise ValueError(f"without cu_new there is one token per sequence: {T} tokens, {N} sequences")
+        cu_new = torch.arange(N + 1, dtype=torch.int32, device=dev)
+    _need(k, "k", lead + (T, Hkv, dk), k_cache.dtype, dev)
+    _need(v, "v", lead + (T, Hkv, dv), k_cache.dtype, dev)
+    _need(block_table, "block_table", (N, MP), torch.int32, dev)
+    _need(lens, "lens", (N,), torch.int32, dev)
+    _need(cu_new, "cu_new", (N + 1,), torch.int32, dev)
+    _check(kv_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                     lens.data_ptr(), cu_new.data_ptr(), N, T, L, Hkv, dk, dv, P, ps, MP, code, stream))
 
 
 def kv_compact_t(k_cache, v_cache, block_table, lens, accepted, cu_accepted, *, new_lens=None, stream=None):
@@ -394,22 +441,26 @@ def kv_compact_t(k_cache, v_cache, block_table, lens, accepted, cu_accepted, *, 
     committed positions (all layers): ``accepted`` int32 [A], their numbers in
     the draft, rising, packed by ``cu_accepted`` int32 [N + 1].  Returns the
     new lengths, int32 [N]."""
+    return _on_stream(stream, _gpu(k_cache, "k_cache"), _kv_compact_on, k_cache, v_cache, block_table, lens, accepted,
+                      cu_accepted, new_lens)
+
+
+def _kv_compact_on(k_cache, v_cache, block_table, lens, accepted, cu_accepted, new_lens, stream):
     import torch
-    if not k_cache.is_cuda:
-        raise ValueError("the cache is on a GPU device; k_cache is on the CPU")
     dev = k_cache.device
-    st = _stream_of(stream, dev)
-    with torch.cuda.device(dev), torch.cuda.stream(st):
-        code, L, P, ps, Hkv, dk, dv = _layers(k_cache, v_cache, dev)
-        N, MP, A = int(lens.shape[0]), int(block_table.shape[1]), int(accepted.shape[0])
-        _need(block_table, "block_table", (N, MP), torch.int32, dev)
-        _need(lens, "lens", (N,), torch.int32, dev)
-        _need(accepted, "accepted", (A,), torch.int32, dev)
-        _need(cu_accepted, "cu_accepted", (N + 1,), torch.int32, dev)
-        if new_lens is None:
-            new_lens = torch.empty(N, dtype=torch.int32, device=dev)
+    code, L, P, ps, Hkv, dk, dv = _layers(k_cache, v_cache, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [N, max_pages]")
+    N, MP, A = lens.shape[0], block_table.shape[1], accepted.shape[0]
+    _need(block_table, "block_table", (N, MP), torch.int32, dev)
+    _need(lens, "lens", (N,), torch.int32, dev)
+    _need(accepted, "accepted", (A,), torch.int32, dev)
+    _need(cu_accepted, "cu_accepted", (N + 1,), torch.int32, dev)
+    if new_lens is None:
+        new_lens = torch.empty(N, dtype=torch.int32, device=dev)
+    else:
         _need(new_lens, "new_lens", (N,), torch.int32, dev)
-        _check(kv_compact(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
-                          accepted.data_ptr(), cu_accepted.data_ptr(), N, A, L, Hkv, dk, dv, P, ps, MP, code,
-                          new_lens.data_ptr(), int(st.cuda_stream)))
+    _check(kv_compact(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+                      accepted.data_ptr(), cu_accepted.data_ptr(), N, A, L, Hkv, dk, dv, P, ps, MP, code,
+                      new_lens.data_ptr(), stream))
     return new_lens

@@ -90,7 +90,8 @@ kda_status attn_prefill(const void* q, const void* k, const void* v, const int32
     if (T_tot == 0) return KDA_OK;
     const kda::AttnArgs a{q, k, v, cu_seqlens, N, static_cast<int32_t>(T_tot), H_q, H_kv, d_k, d_v,
                           static_cast<int32_t>(q_stride), static_cast<int32_t>(k_stride), static_cast<int32_t>(v_stride),
-                          scale, dtype == KDA_DTYPE_BF16, o, lse, stream};
+                          scale, dtype == KDA_DTYPE_BF16, o, lse, stream,
+                          kda::attn_split(N, T_tot, H_q, kda::device_cus_or_default())};
     (void)hipGetLastError();  // report only this launch's status
     const hipError_t e = kda::launch_attn_prefill(a);
     return e == hipSuccess ? KDA_OK : hip_fail(e, "attention kernel launch");
@@ -120,9 +121,11 @@ kda_status attn_prefill_backward(const void* q, const void* k, const void* v, co
     if (T_tot == 0) return KDA_OK;
     const kda::AttnArgs a{q, k, v, cu_seqlens, N, static_cast<int32_t>(T_tot), H_q, H_kv, d_k, d_v,
                           static_cast<int32_t>(q_stride), static_cast<int32_t>(k_stride), static_cast<int32_t>(v_stride),
-                          scale, dtype == KDA_DTYPE_BF16, const_cast<void*>(o), const_cast<float*>(lse), stream};
+                          scale, dtype == KDA_DTYPE_BF16, const_cast<void*>(o), const_cast<float*>(lse), stream,
+                          kda::attn_split(N, T_tot, H_q, kda::device_cus_or_default())};
     (void)hipGetLastError();  // report only this launch's status
-    const hipError_t e = kda::launch_attn_bwd({a, d_o, d_q, d_k_out, d_v_out, workspace});
+    const hipError_t e = kda::launch_attn_bwd({a, d_o, d_q, d_k_out, d_v_out, workspace,
+                                                kda::attn_split(N, T_tot, H_kv, kda::device_cus_or_default())});
     return e == hipSuccess ? KDA_OK : hip_fail(e, "attention backward kernel launch");
 }
 

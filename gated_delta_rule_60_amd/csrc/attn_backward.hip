@@ -258,6 +258,215 @@ __global__ __launch_bounds__(256, BF16 || DK + DV <= 128 ? 2 : 1) void attn_bwd_
     store_col_as_row<BF16, DV>(static_cast<G*>(b.d_v) + (tok * a.Hkv + g) * DV, dv, 1.f, half, live);
 }
 
+// The same two for batches that leave compute units idle: 32 rows (or keys) a
+// workgroup, its four waves on every fourth 32-key (or 32-row) tile, their
+// sums joined at the end.
+template <bool BF16, int DK, int DV>
+__global__ __launch_bounds__(256, 1) void attn_bwd_dq_split_kernel(AttnBwdArgs b, float c, Stats stats) {
+    using Op = AttnOp<BF16>;
+    using KT = AttnTile<BF16, DK>;
+    using VT = AttnTile<BF16, DV>;
+    using G = typename Op::G;
+    constexpr int TG = 32 * kWaves;
+    constexpr int KB = TG * KT::ROWB, VB = TG * VT::ROWB;
+    constexpr int NBUF = 2 * (KB + VB) <= 128 * 1024 ? 2 : 1;
+    constexpr int JOIN = 2 * KT::ND * 4096;
+    __shared__ __attribute__((aligned(1024))) char lds[NBUF * (KB + VB) > JOIN ? NBUF * (KB + VB) : JOIN];
+
+    const AttnArgs& a = b.f;
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hp = blockIdx.x % a.Hq;
+    const int group = a.Hq / a.Hkv;
+    const int g = hp % a.Hkv, h = g * group + hp / a.Hkv;
+    SeqTile st;
+    if (!find_tile<32>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hq, false, st)) return;
+
+    const int row0 = st.tile * 32;
+    const int qi = row0 + (lane & 31);
+    const bool live = qi < st.len;
+    const size_t tok = static_cast<size_t>(st.beg) + (live ? qi : 0);
+    const int ks = a.k_stride * Op::ES, vs = a.v_stride * Op::ES;
+    const char* kb = static_cast<const char*>(a.k) + (static_cast<size_t>(st.beg) * a.k_stride + static_cast<size_t>(g) * DK) * Op::ES;
+    const char* vb = static_cast<const char*>(a.v) + (static_cast<size_t>(st.beg) * a.v_stride + static_cast<size_t>(g) * DV) * Op::ES;
+    const auto ksrc = KT::template src<kWaves>(wave, lane, ks);
+    const auto vsrc = VT::template src<kWaves>(wave, lane, vs);
+    const int kat = KT::row_at(lane), vat = VT::row_at(lane);
+    const auto kct = KT::col_at(lane);
+    auto stage_group = [&](int t) __attribute__((always_inline)) {
+        char* l = lds + (NBUF == 2 ? t & 1 : 0) * (KB + VB);
+        KT::template stage<kWaves, TG>(l, kb + static_cast<size_t>(t) * TG * ks, st.len - t * TG, ks, ksrc, wave);
+        VT::template stage<kWaves, TG>(l + KB, vb + static_cast<size_t>(t) * TG * vs, st.len - t * TG, vs, vsrc, wave);
+    };
+    stage_group(0);
+
+    RowFrags<BF16, DK> q;
+    RowFrags<BF16, DV> d_o;
+    load_row_frags<BF16, DK>(q, static_cast<const G*>(a.q) + tok * a.q_stride + static_cast<size_t>(h) * DK, half, live);
+    load_row_frags<BF16, DV>(d_o, static_cast<const G*>(b.d_o) + (tok * a.Hq + h) * DV, half, live);
+    float lse2 = 0.f, D = 0.f;
+    {
+        RowFrags<BF16, DV> o;
+        load_row_frags<BF16, DV>(o, static_cast<const G*>(a.o) + (tok * a.Hq + h) * DV, half, live);
+#pragma unroll
+        for (int kk = 0; kk < VT::NF; ++kk) D += Op::dot(o[kk], d_o[kk]);
+        D = half_sum(D);
+        if (live) lse2 = a.lse[tok * a.Hq + h] * kLog2e;
+    }
+    if (live && half == 0 && wave == 0) {
+        stats.lse2[static_cast<size_t>(h) * a.T_tot + tok] = lse2;
+        stats.D[static_cast<size_t>(h) * a.T_tot + tok] = D;
+    }
+
+    f32x16_t dq[KT::ND];
+#pragma unroll
+    for (int dt = 0; dt < KT::ND; ++dt) dq[dt] = f32x16_t{};
+    const int groups = (row0 + TG) / TG;
+    for (int t = 0; t < groups; ++t) {
+        lds_ready();
+        if (NBUF == 2 && t + 1 < groups) stage_group(t + 1);
+        const int key0 = t * TG + 32 * wave;
+        if (key0 <= row0) {
+            const char* kt = lds + (NBUF == 2 ? t & 1 : 0) * (KB + VB);
+            f32x16_t s = KT::rows_times(f32x16_t{}, kt, kat, 32 * wave, q);
+            const f32x16_t dp = VT::rows_times(f32x16_t{}, kt + KB, vat, 32 * wave, d_o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse2)) * (dp[i] - D);
+            if (key0 == row0) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = key0 + 8 * (i >> 2) + 4 * half + (i & 3) <= qi ? s[i] : 0.f;
+            }
+            ColOp<BF16> ds;
+            ds.set(s);
+#pragma unroll
+            for (int dt = 0; dt < KT::ND; ++dt) dq[dt] = KT::cols_times(dq[dt], kt, kct, 32 * wave, dt, ds);
+        }
+        if (NBUF == 1 && t + 1 < groups) {
+            lds_ready();
+            stage_group(t + 1);
+        }
+    }
+    join_waves(dq, lds, wave, lane);
+    if (wave == 0) store_col_as_row<BF16, DK>(static_cast<G*>(b.d_q) + (tok * a.Hq + h) * DK, dq, a.scale, half, live);
+}
+
+template <bool BF16, int DK, int DV>
+__global__ __launch_bounds__(256, 1) void attn_bwd_dkv_split_kernel(AttnBwdArgs b, float c, Stats stats) {
+    using Op = AttnOp<BF16>;
+    using QT = AttnTile<BF16, DK>;
+    using OT = AttnTile<BF16, DV>;
+    using G = typename Op::G;
+    constexpr int TG = 32 * kWaves;  // query rows the waves take together
+    constexpr int QB = TG * QT::ROWB, OB = TG * OT::ROWB, SB = TG * 4;
+    constexpr int NBUF = 2 * (QB + OB + 2 * SB) <= 144 * 1024 ? 2 : 1;
+    constexpr int SLOT = (QB + OB + 2 * SB + 1023) / 1024 * 1024;
+    constexpr int JOIN = 2 * 4096 * (QT::ND > OT::ND ? QT::ND : OT::ND);
+    __shared__ __attribute__((aligned(1024))) char lds[NBUF * SLOT > JOIN ? NBUF * SLOT : JOIN];
+
+    const AttnArgs& a = b.f;
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = blockIdx.x % a.Hkv;
+    const int group = a.Hq / a.Hkv;
+    SeqTile st;
+    if (!find_tile<32>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hkv, true, st)) return;
+
+    const int key0 = st.tile * 32;
+    const int kj = key0 + (lane & 31);
+    const bool live = kj < st.len;
+    const size_t tok = static_cast<size_t>(st.beg) + (live ? kj : 0);
+    const int qs = a.q_stride * Op::ES, os = a.Hq * DV * Op::ES;
+    const auto qsrc = QT::template src<kWaves>(wave, lane, qs);
+    const auto osrc = OT::template src<kWaves>(wave, lane, os);
+    const int qat = QT::row_at(lane), oat = OT::row_at(lane);
+    const auto qct = QT::col_at(lane);
+    const auto oct = OT::col_at(lane);
+
+    const int first = key0 / TG, groups = (st.len + TG - 1) / TG - first;  // row groups of a head
+    auto stage_group = [&](int slot, int hh, int t) __attribute__((always_inline)) {
+        char* l = lds + slot * SLOT;
+        const int h = g * group + hh;
+        const size_t r = static_cast<size_t>(st.beg) + static_cast<size_t>(t) * TG;
+        const int left = st.len - t * TG;
+        QT::template stage<kWaves, TG>(l, static_cast<const char*>(a.q) + (r * a.q_stride + static_cast<size_t>(h) * DK) * Op::ES, left,
+                                       qs, qsrc, wave);
+        OT::template stage<kWaves, TG>(l + QB, static_cast<const char*>(b.d_o) + (r * a.Hq + h) * DV * Op::ES, left, os, osrc, wave);
+        // two waves a statistic, 64 rows each
+        const float* p = (wave < 2 ? stats.lse2 : stats.D) + static_cast<size_t>(h) * a.T_tot + r;
+        load_lds4(buffer_rsrc(p, (left < TG ? left : TG) * 4), l + QB + OB + wave * 256, ((wave & 1) * 64 + lane) * 4, 0);
+    };
+    stage_group(0, 0, first);
+
+    RowFrags<BF16, DK> k;
+    RowFrags<BF16, DV> v;
+    load_row_frags<BF16, DK>(k, static_cast<const G*>(a.k) + tok * a.k_stride + static_cast<size_t>(g) * DK, half, live);
+    load_row_frags<BF16, DV>(v, static_cast<const G*>(a.v) + tok * a.v_stride + static_cast<size_t>(g) * DV, half, live);
+    f32x16_t dk[QT::ND], dv[OT::ND];
+#pragma unroll
+    for (int dt = 0; dt < QT::ND; ++dt) dk[dt] = f32x16_t{};
+#pragma unroll
+    for (int dt = 0; dt < OT::ND; ++dt) dv[dt] = f32x16_t{};
+
+    const int steps = groups * group;
+    int hh = 0, t = first, slot = 0;
+    for (int n = 0; n < steps; ++n) {
+        int nh = hh, nt = t + 1;
+        if (nt == first + groups) {
+            nt = first;
+            ++nh;
+        }
+        lds_ready();
+        if (NBUF == 2 && n + 1 < steps) stage_group(slot ^ 1, nh, nt);
+        const int r0 = t * TG + 32 * wave;  // the wave's first row
+        if (r0 >= key0 && r0 < st.len) {
+            const char* qt = lds + slot * SLOT;
+            const char* ot = qt + QB;
+            const float* sl = reinterpret_cast<const float*>(ot + OB) + 32 * wave;
+            const float* sd = sl + TG;
+            f32x16_t s = QT::rows_times(f32x16_t{}, qt, qat, 32 * wave, k);
+            f32x16_t dp = OT::rows_times(f32x16_t{}, ot, oat, 32 * wave, v);
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+                const f32x4_t l2 = *reinterpret_cast<const f32x4_t*>(sl + 8 * i4 + 4 * half);
+                const f32x4_t dd = *reinterpret_cast<const f32x4_t*>(sd + 8 * i4 + 4 * half);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * i4 + e;
+                    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -l2[e]));
+                    dp[i] = s[i] * (dp[i] - dd[e]);
+                }
+            }
+            if (r0 == key0) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const bool sees = kj <= r0 + 8 * (i >> 2) + 4 * half + (i & 3);
+                    s[i] = sees ? s[i] : 0.f;
+                    dp[i] = sees ? dp[i] : 0.f;
+                }
+            }
+            ColOp<BF16> p, ds;
+            p.set(s);
+            ds.set(dp);
+#pragma unroll
+            for (int dt = 0; dt < OT::ND; ++dt) dv[dt] = OT::cols_times(dv[dt], ot, oct, 32 * wave, dt, p);
+#pragma unroll
+            for (int dt = 0; dt < QT::ND; ++dt) dk[dt] = QT::cols_times(dk[dt], qt, qct, 32 * wave, dt, ds);
+        }
+        if (NBUF == 1 && n + 1 < steps) {
+            lds_ready();
+            stage_group(0, nh, nt);
+        }
+        hh = nh;
+        t = nt;
+        if (NBUF == 2) slot ^= 1;
+    }
+    join_waves(dk, lds, wave, lane);
+    join_waves(dv, lds, wave, lane);
+    if (wave != 0) return;
+    store_col_as_row<BF16, DK>(static_cast<G*>(b.d_k) + (tok * a.Hkv + g) * DK, dk, a.scale, half, live);
+    store_col_as_row<BF16, DV>(static_cast<G*>(b.d_v) + (tok * a.Hkv + g) * DV, dv, 1.f, half, live);
+}
+
 namespace {
 
 template <bool BF16, int DK, int DV>
@@ -268,12 +477,18 @@ hipError_t launch(const AttnBwdArgs& b) {
     const Stats stats{static_cast<float*>(b.workspace), static_cast<float*>(b.workspace) + n};
     const hipStream_t st = static_cast<hipStream_t>(a.stream);
     const float c = a.scale * kLog2e;
-    hipLaunchKernelGGL((attn_bwd_dq_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hq)), dim3(64 * kWaves), 0, st,
-                       b, c, stats);
+    const int64_t units32 = (static_cast<int64_t>(a.T_tot) + 31) / 32 + a.N;
+    const dim3 threads(64 * kWaves);
+    if (a.split)
+        hipLaunchKernelGGL((attn_bwd_dq_split_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units32 * a.Hq)), threads, 0, st, b, c, stats);
+    else
+        hipLaunchKernelGGL((attn_bwd_dq_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hq)), threads, 0, st, b, c, stats);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_bwd_dkv_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hkv)), dim3(64 * kWaves), 0, st,
-                       b, c, stats);
+    if (b.split_kv)
+        hipLaunchKernelGGL((attn_bwd_dkv_split_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units32 * a.Hkv)), threads, 0, st, b, c, stats);
+    else
+        hipLaunchKernelGGL((attn_bwd_dkv_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hkv)), threads, 0, st, b, c, stats);
     return hipGetLastError();
 }
 

@@ -426,6 +426,37 @@ __device__ __forceinline__ void store_col_as_row(typename AttnOp<BF16>::G* p, co
     }
 }
 
+// ---------------------------------------------------------------------------
+// Four waves with accumulators of the same 32 columns and different shares of
+// the reduction: their sum in wave 0, in a fixed order.  `lds`: 2 NA 4 KB.
+// ---------------------------------------------------------------------------
+template <int NA>
+__device__ __forceinline__ void join_waves(f32x16_t (&acc)[NA], char* lds, int wave, int lane) {
+#pragma unroll
+    for (int w = 2; w >= 1; --w) {
+        f32x4_t* p = reinterpret_cast<f32x4_t*>(lds) + (wave & (w - 1)) * NA * 256;
+        __syncthreads();
+        if (wave >= w && wave < 2 * w) {
+#pragma unroll
+            for (int n = 0; n < NA; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    p[(n * 4 + i) * 64 + lane] = f32x4_t{acc[n][4 * i], acc[n][4 * i + 1], acc[n][4 * i + 2], acc[n][4 * i + 3]};
+        }
+        __syncthreads();
+        if (wave < w) {
+#pragma unroll
+            for (int n = 0; n < NA; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4_t y = p[(n * 4 + i) * 64 + lane];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[n][4 * i + e] += y[e];
+                }
+        }
+    }
+}
+
 // All loads into LDS this wave issued have landed and its LDS reads are done;
 // then every wave's.
 __device__ __forceinline__ void lds_ready() {

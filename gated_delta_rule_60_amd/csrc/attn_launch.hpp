@@ -24,7 +24,12 @@ struct AttnArgs {
     void* o;     // [T_tot, Hq, d_v]
     float* lse;  // [T_tot, Hq], natural log
     void* stream;
+    bool split;  // attn_split
 };
+
+// Whether a batch leaves so many compute units idle that its pieces are split
+// over the waves of four times as many workgroups.
+bool attn_split(int32_t N, int64_t T_tot, int32_t heads, int cus);
 
 struct AttnBwdArgs {
     AttnArgs f;        // o and lse are read
@@ -33,6 +38,7 @@ struct AttnBwdArgs {
     void* d_k;         // [T_tot, Hkv, d_k]
     void* d_v;         // [T_tot, Hkv, d_v]
     void* workspace;   // attn_bwd_workspace_bytes
+    bool split_kv;     // attn_split over the key heads
 };
 
 // Attention of drafted tokens over a paged cache.

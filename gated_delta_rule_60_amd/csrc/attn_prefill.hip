@@ -158,14 +158,149 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a, float 
     for (; t < tiles; ++t) next(t);
 
     l = half_sum(l);
-    if (live && half == 0) a.lse[tok * a.Hq + h] = (mc + log2f(l)) * kLn2;
+    if (a.lse && live && half == 0) a.lse[tok * a.Hq + h] = (mc + log2f(l)) * kLn2;
     store_col_as_row<BF16, DV>(static_cast<G*>(a.o) + (tok * a.Hq + h) * DV, o, 1.f / l, half, live);
+}
+
+// The same for batches that leave compute units idle: 32 query rows a
+// workgroup, its four waves on every fourth 32-key tile, joined at the end.
+// Four times the workgroups and a quarter of the steps one after another.
+template <bool BF16, int DK, int DV>
+__global__ __launch_bounds__(256, 1) void attn_prefill_split_kernel(AttnArgs a, float c) {
+    using Op = AttnOp<BF16>;
+    using KT = AttnTile<BF16, DK>;
+    using VT = AttnTile<BF16, DV>;
+    using G = typename Op::G;
+    constexpr int TG = 32 * kWaves;  // keys the waves take together
+    constexpr int KB = TG * KT::ROWB, VB = TG * VT::ROWB;
+    constexpr int NBUF = 2 * (KB + VB) <= 128 * 1024 ? 2 : 1;
+    constexpr int JOIN = 2 * VT::ND * 4096 + kWaves * 32 * 8;
+    __shared__ __attribute__((aligned(1024))) char lds[NBUF * (KB + VB) > JOIN ? NBUF * (KB + VB) : JOIN];
+
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hp = blockIdx.x % a.Hq;
+    const int group = a.Hq / a.Hkv;
+    const int g = hp % a.Hkv, h = g * group + hp / a.Hkv;
+    SeqTile st;
+    if (!find_tile<32>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hq, false, st)) return;
+
+    const int row0 = st.tile * 32;
+    const int qi = row0 + (lane & 31);
+    const bool live = qi < st.len;
+    const size_t tok = static_cast<size_t>(st.beg) + (live ? qi : 0);
+    RowFrags<BF16, DK> q;
+    load_row_frags<BF16, DK>(q, static_cast<const G*>(a.q) + tok * a.q_stride + static_cast<size_t>(h) * DK, half, live);
+
+    const int ks = a.k_stride * Op::ES, vs = a.v_stride * Op::ES;
+    const char* kb = static_cast<const char*>(a.k) + (static_cast<size_t>(st.beg) * a.k_stride + static_cast<size_t>(g) * DK) * Op::ES;
+    const char* vb = static_cast<const char*>(a.v) + (static_cast<size_t>(st.beg) * a.v_stride + static_cast<size_t>(g) * DV) * Op::ES;
+    const auto ksrc = KT::template src<kWaves>(wave, lane, ks);
+    const auto vsrc = VT::template src<kWaves>(wave, lane, vs);
+    const int kat = KT::row_at(lane);
+    const auto vat = VT::col_at(lane);
+    auto stage_group = [&](int t) __attribute__((always_inline)) {
+        char* b = lds + (NBUF == 2 ? t & 1 : 0) * (KB + VB);
+        KT::template stage<kWaves, TG>(b, kb + static_cast<size_t>(t) * TG * ks, st.len - t * TG, ks, ksrc, wave);
+        VT::template stage<kWaves, TG>(b + KB, vb + static_cast<size_t>(t) * TG * vs, st.len - t * TG, vs, vsrc, wave);
+    };
+
+    f32x16_t o[VT::ND];
+#pragma unroll
+    for (int dt = 0; dt < VT::ND; ++dt) o[dt] = f32x16_t{};
+    float mc = -INFINITY, l = 0.f;
+
+    const int groups = (row0 + TG) / TG;  // row0 is a multiple of 32: up to the diagonal
+    stage_group(0);
+    for (int t = 0; t < groups; ++t) {
+        lds_ready();
+        if (NBUF == 2 && t + 1 < groups) stage_group(t + 1);
+        const int key0 = t * TG + 32 * wave;
+        if (key0 <= row0) {
+            const char* kt = lds + (NBUF == 2 ? t & 1 : 0) * (KB + VB);
+            const char* vt = kt + KB + 32 * wave * VT::ROWB;
+            f32x16_t s = KT::rows_times(f32x16_t{}, kt, kat, 32 * wave, q);
+            const bool diagonal = key0 == row0;
+            if (diagonal) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = key0 + 8 * (i >> 2) + 4 * half + (i & 3) <= qi ? s[i] : -INFINITY;
+            }
+            float mx = s[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
+            mx = half_max(mx) * c;
+            if (__any(mx > mc + kLazyLog2)) {
+                const float m1 = mx > mc + kLazyLog2 ? mx : mc;
+                const float r = m1 > mc ? exp2f(mc - m1) : 1.f;
+                mc = m1;
+                l *= r;
+#pragma unroll
+                for (int dt = 0; dt < VT::ND; ++dt)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[dt][i] *= r;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
+                l += s[i];
+            }
+            ColOp<BF16> p;
+            p.set(s);
+            if (diagonal && VT::template any_nonfinite<32>(vt, lane)) {
+#pragma unroll
+                for (int dt = 0; dt < VT::ND; ++dt) o[dt] = VT::template cols_times<true>(o[dt], vt, vat, 0, dt, p);
+#pragma unroll 1
+                for (int j = 0; j < 32; ++j) VT::add_nonfinite(o, vt, j, half, key0 + j <= qi);
+            } else {
+#pragma unroll
+                for (int dt = 0; dt < VT::ND; ++dt) o[dt] = VT::cols_times(o[dt], vt, vat, 0, dt, p);
+            }
+        }
+        if (NBUF == 1 && t + 1 < groups) {
+            lds_ready();
+            stage_group(t + 1);
+        }
+    }
+
+    // the row's maximum and sum over the waves; each scales its part to them
+    l = half_sum(l);
+    float* sm = reinterpret_cast<float*>(lds + 2 * VT::ND * 4096);  // [kWaves][32][2]
+    __syncthreads();
+    if (half == 0) {
+        sm[(wave * 32 + lane) * 2] = mc;
+        sm[(wave * 32 + lane) * 2 + 1] = l;
+    }
+    __syncthreads();
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sm[(w * 32 + (lane & 31)) * 2]);
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const float mw = sm[(w * 32 + (lane & 31)) * 2];
+        sum = fmaf(sm[(w * 32 + (lane & 31)) * 2 + 1], mw == m ? 1.f : exp2f(mw - m), sum);
+    }
+    const float r = mc == m ? 1.f : exp2f(mc - m);
+#pragma unroll
+    for (int dt = 0; dt < VT::ND; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[dt][i] *= r;
+    join_waves(o, lds, wave, lane);
+    if (wave != 0) return;
+    if (a.lse && live && half == 0) a.lse[tok * a.Hq + h] = (m + log2f(sum)) * kLn2;
+    store_col_as_row<BF16, DV>(static_cast<G*>(a.o) + (tok * a.Hq + h) * DV, o, 1.f / sum, half, live);
 }
 
 namespace {
 
 template <bool BF16, int DK, int DV>
 hipError_t launch(const AttnArgs& a) {
+    if (a.split) {
+        const int64_t units = (static_cast<int64_t>(a.T_tot) + 31) / 32 + a.N;
+        hipLaunchKernelGGL((attn_prefill_split_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hq)), dim3(64 * kWaves), 0,
+                           static_cast<hipStream_t>(a.stream), a, a.scale * kLog2e);
+        return hipGetLastError();
+    }
     const int64_t units = (static_cast<int64_t>(a.T_tot) + kBM - 1) / kBM + a.N;
     hipLaunchKernelGGL((attn_prefill_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hq)), dim3(64 * kWaves), 0,
                        static_cast<hipStream_t>(a.stream), a, a.scale * kLog2e);
@@ -191,6 +326,10 @@ hipError_t launch_dk(const AttnArgs& a) {
 }
 
 }  // namespace
+
+bool attn_split(int32_t N, int64_t T_tot, int32_t heads, int cus) {
+    return (T_tot / kBM + N) * heads <= cus;
+}
 
 hipError_t launch_attn_prefill(const AttnArgs& a) {
     if (a.T_tot == 0) return hipSuccess;

@@ -198,6 +198,7 @@ __global__ __launch_bounds__(kThreads) void kv_free_kernel(PageArgs a, const int
         for (int b = 0; b < kBatch; ++b) ref[b] = page[b] >= 0 ? load_ref(&a.refs[page[b]]) : 1;
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
+            if (e0 + b * kThreads >= total) break;  // the same for every thread
             const bool first = ref[b] == static_cast<int>(e0 + b * kThreads + i) - kMark;
             int64_t all;
             const int64_t upto = block_scan(first ? 1 : 0, s_wave, all);

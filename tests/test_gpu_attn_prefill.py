@@ -39,6 +39,22 @@ def test_head_sizes(dtype, dk, dv):
     _check_all([70, 131], 2, 1, dk, dv, dtype, 100 + dk + dv)
 
 
+# Batches that fill the device run whole 128-row blocks; the small ones above and below split their
+# keys (or rows) over the waves of a block.
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk", [32, 64, 128])
+@pytest.mark.parametrize("dv", [32, 64, 128])
+def test_head_sizes_of_a_full_batch(dtype, dk, dv):
+    _check_all([70, 131] * 30, 4, 4, dk, dv, dtype, 200 + dk + dv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,hq,hkv", [([1, 0, 300, 129, 128, 127, 65, 64, 63, 33, 32, 31] * 8, 6, 3), ([200] * 90, 6, 3),
+                                         ([1] * 300, 1, 1), ([700, 1, 513], 40, 40), ([1000], 66, 33)])
+def test_lengths_and_groups_of_a_full_batch(dtype, lens, hq, hkv):
+    _check_all(lens, hq, hkv, 64, 64, dtype, len(lens))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 3), (8, 2), (6, 2), (5, 1), (9, 9)])
 def test_head_groups(dtype, hq, hkv):
@@ -131,21 +147,22 @@ def test_a_sequence_does_not_see_its_neighbours_values(dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("at", [0, 5, 31, 32, 63, 64, 130, 199])
 @pytest.mark.parametrize("dv", [32, 128])
-def test_earlier_rows_do_not_see_a_later_token(dtype, at, dv):
+@pytest.mark.parametrize("full", [False, True])
+def test_earlier_rows_do_not_see_a_later_token(dtype, at, dv, full):
     """NaN and infinite keys and values of token `at`: the rows before it keep
     their bits, its own and the later ones turn NaN (or infinite)."""
-    q, k, v, _, cu = _make([200], 2, 1, 64, dv, dtype, 17)
+    q, k, v, _, cu = _make([200] + [64] * (150 if full else 0), 2, 1, 64, dv, dtype, 17)
+    n = 200  # the rows that may change
     want, lse_want = kda.attn_prefill_t(q, k, v, cu)
     for bad in (float("nan"), float("inf"), -float("inf")):
         v2 = v.clone()
         v2[at, 0, 3] = bad
         o, lse = kda.attn_prefill_t(q, k, v2, cu)
-        assert torch.equal(o[:at], want[:at]) and torch.equal(lse, lse_want)
-        assert not torch.isfinite(o[at:, :, 3]).any()
+        assert torch.equal(o[:at], want[:at]) and torch.equal(o[n:], want[n:]) and torch.equal(lse, lse_want)
         if bad != bad:
-            assert torch.isnan(o[at:, :, 3]).all()
+            assert torch.isnan(o[at:n, :, 3]).all()
         else:
-            assert (o[at:, :, 3].float() == bad).all()
+            assert (o[at:n, :, 3].float() == bad).all()
         rest = [i for i in range(dv) if i != 3]
         assert torch.equal(o[..., rest], want[..., rest])
         k2 = k.clone()
