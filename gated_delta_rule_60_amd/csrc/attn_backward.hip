@@ -97,6 +97,7 @@ __global__ __launch_bounds__(256, BF16 || DK < 128 ? 2 : 1) void attn_bwd_dq_ker
     for (int dt = 0; dt < KT::ND; ++dt) dq[dt] = f32x16_t{};
 
     stage_tile(0);
+    loads_done();
     for (int t = 0; t < tiles; ++t) {
         lds_ready();
         if (t + 1 < tiles) stage_tile(t + 1);
@@ -201,6 +202,7 @@ __global__ __launch_bounds__(256, BF16 || DK + DV <= 128 ? 2 : 1) void attn_bwd_
 
     int hh = 0, t = t0, slot = 0;
     stage_tile(0, 0, t0);
+    loads_done();
     while (hh < group) {
         int nh = hh, nt = t + 1;
         if (nt == t1) {
@@ -322,6 +324,7 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_dq_split_kernel(AttnBwdArgs b
 #pragma unroll
     for (int dt = 0; dt < KT::ND; ++dt) dq[dt] = f32x16_t{};
     const int groups = (row0 + TG) / TG;
+    loads_done();
     for (int t = 0; t < groups; ++t) {
         lds_ready();
         if (NBUF == 2 && t + 1 < groups) stage_group(t + 1);
@@ -409,6 +412,7 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_dkv_split_kernel(AttnBwdArgs 
 
     const int steps = groups * group;
     int hh = 0, t = first, slot = 0;
+    loads_done();
     for (int n = 0; n < steps; ++n) {
         int nh = hh, nt = t + 1;
         if (nt == first + groups) {

@@ -36,18 +36,24 @@ __device__ __forceinline__ float half_sum(float x) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// 16 bytes a lane from a buffer range to LDS at `lds` (the wave's base) + 16 lane.  The host
-// pass does not know the 16-byte form.
+// 16 (4) bytes a lane from a buffer range to LDS at `lds` (the wave's base) + 16 (4) lane.  Written
+// out, because the compiler waits for every load into LDS it knows of before each column read
+// (ds_read_b64_tr_b16), the next tile's among them.  The load has no output register; whoever
+// reads the tile waits for it with lds_ready().  m0 holds the LDS base, one wait state ahead; the
+// kernels that use these have no other use of it.
+__device__ __forceinline__ unsigned lds_offset(const char* p) {
+    return __builtin_amdgcn_readfirstlane(static_cast<unsigned>(reinterpret_cast<uintptr_t>((KDA_LDS const char*)p)));
+}
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, char* lds, int voff, int soff) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (KDA_LDS void*)lds, 16, voff, soff, 0, 0);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(lds_offset(lds)), "v"(voff), "s"(r), "s"(soff) : "memory");
 #endif
 }
-
-// 4 bytes a lane, to `lds` + 4 lane.
 __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, char* lds, int voff, int soff) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (KDA_LDS void*)lds, 4, voff, soff, 0, 0);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :: "s"(lds_offset(lds)), "v"(voff), "s"(r), "s"(soff) : "memory");
 #endif
 }
 
@@ -456,6 +462,10 @@ __device__ __forceinline__ void join_waves(f32x16_t (&acc)[NA], char* lds, int w
         }
     }
 }
+
+// Every load so far has arrived, as the compiler knows too: without it the waits for the loads
+// before a loop would be repeated inside it, where they hold up the loads into LDS.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
 // All loads into LDS this wave issued have landed and its LDS reads are done;
 // then every wave's.

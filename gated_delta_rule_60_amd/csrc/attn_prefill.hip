@@ -145,6 +145,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a, float 
         if (t + 1 < tiles) stage_tile(t + 1);
     };
     stage_tile(0);
+    loads_done();
     int t = 0;
     for (; t < wtiles - 1; ++t) {
         next(t);
@@ -212,6 +213,7 @@ __global__ __launch_bounds__(256, 1) void attn_prefill_split_kernel(AttnArgs a, 
 
     const int groups = (row0 + TG) / TG;  // row0 is a multiple of 32: up to the diagonal
     stage_group(0);
+    loads_done();
     for (int t = 0; t < groups; ++t) {
         lds_ready();
         if (NBUF == 2 && t + 1 < groups) stage_group(t + 1);

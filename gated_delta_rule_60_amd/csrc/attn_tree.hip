@@ -44,7 +44,8 @@ template <bool BF16, int DK, int DV, int NQ, int RW>
 struct TreeShape {
     static constexpr int ES = BF16 ? 2 : 4;
     static constexpr int KB = kTK * DK * ES, VB = kTK * DV * ES;  // tile bytes
-    static constexpr int NW = RW > 1 || 8 * (KB + VB) <= 128 * 1024 ? 4 : 2;
+    // two waves a SIMD where the tiles have a load for each (329 drafted tokens of 12 trees: 241 us with one)
+    static constexpr int NW = RW == 1 ? (8 * (KB + VB) <= 128 * 1024 ? 4 : 2) : BF16 && DK >= 64 && DV >= 64 ? 8 : 4;
     static constexpr int KW = NW / RW;
     static constexpr int R = 16 * NQ * RW;  // query rows
     // slots: of one wave's tile (RW = 1), or of two tiles that all waves load
@@ -54,6 +55,7 @@ struct TreeShape {
     static constexpr int JOIN = KW / 2 * R * (DV + 2) * 4 + NW * 4;
     static constexpr int TILES = (RW == 1 ? NW : 1) * NS * SLOT;
     static constexpr int LDS = TILES > JOIN ? TILES : JOIN;
+    static constexpr int WPS = NW == 8 || (LDS <= 80 * 1024 && NW == 4) ? 2 : 1;  // waves a SIMD
 };
 
 }  // namespace
@@ -151,7 +153,7 @@ __device__ __forceinline__ void load_lds16_from(const char* p, char* lds) {
 }
 
 template <bool BF16, int DK, int DV, int NQ, int RW>
-__global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW)) void attn_tree_kernel(TreeArgs a, float c) {
+__global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW), (TreeShape<BF16, DK, DV, NQ, RW>::WPS)) void attn_tree_kernel(TreeArgs a, float c) {
     using Sh = TreeShape<BF16, DK, DV, NQ, RW>;
     using T = Elem<BF16>;
     using KT = AttnTile<BF16, DK>;
@@ -590,7 +592,7 @@ hipError_t launch_rows(const TreeArgs& a, const TreePlan& p) {
     switch (p.rows) {
         case 16: return launch<BF16, DK, DV, 1, 1>(a, p);
         case 32: return launch<BF16, DK, DV, 2, 1>(a, p);
-        case 64: return launch<BF16, DK, DV, 2, 2>(a, p);
+        case 64: return launch<BF16, DK, DV, 1, 4>(a, p);
         default: return launch<BF16, DK, DV, 2, 4>(a, p);
     }
 }
@@ -616,7 +618,7 @@ hipError_t launch_dk(const TreeArgs& a, const TreePlan& p) {
 }  // namespace
 
 // Query rows a pass: the smallest of 16, 32, 64 and 128 that holds an average
-// sequence's rows.  Chunks: eight workgroups a compute unit, so that uneven
+// sequence's rows.  Chunks: four workgroups a compute unit, so that uneven
 // sequences end together; never more than the cache's blocks.
 TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus) {
     TreePlan p;
@@ -626,7 +628,7 @@ TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v,
     p.tiles = rows / p.rows + N;
     if (p.tiles > rows) p.tiles = rows;
     const int64_t blocks = (room + kBlock - 1) / kBlock;
-    int64_t target = 8 * static_cast<int64_t>(cus) / Hkv;
+    int64_t target = 4 * static_cast<int64_t>(cus) / Hkv;
     if (target < 1) target = 1;
     p.target = static_cast<int32_t>(target);
     p.split = blocks > 1 && T_q > 0;
