@@ -57,6 +57,22 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, char* lds, i
 #endif
 }
 
+// Column quads at LDS offsets p[0 .. N - 1] (each lane's own), and the wait for them in the same
+// block: for kernels whose loads into LDS the compiler knows (see load_lds16).
+template <int N>
+__device__ __forceinline__ void read_quads(bf16x4_t (&x)[N], const unsigned (&p)[N]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    static_assert(N == 4, "one block of four reads");
+    u32x2_t y[4];
+    asm volatile("ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %5\n\t"
+                 "ds_read_b64_tr_b16 %2, %6\n\tds_read_b64_tr_b16 %3, %7\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+                 : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __builtin_bit_cast(bf16x4_t, y[i]);
+#endif
+}
+
 // Sum over the wave, in every lane's scalar register.
 __device__ __forceinline__ int wave_sum(int x) {
     x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);  // row_shr:1

@@ -145,6 +145,13 @@ __device__ __forceinline__ float quad_sum(float x) {
     return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
+// An LDS address, and a read from one.
+__device__ __forceinline__ unsigned lds_at(const char* p) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>((KDA_LDS const char*)p)); }
+template <class V>
+__device__ __forceinline__ V lds_read(unsigned at) {
+    return *reinterpret_cast<KDA_LDS const V*>(at);
+}
+
 // 16 bytes a lane from its own address to LDS at `lds` + 16 lane.
 __device__ __forceinline__ void load_lds16_from(const char* p, char* lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -269,36 +276,43 @@ __global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW), (TreeSh
         for (int d = 0; d < ND; ++d) o[x][d] = f32x4_t{};
     }
 
-    // element [row][unit of the lane's fragment] of a tile
-    auto kfrag = [&](const char* kt, int r, int kk) __attribute__((always_inline)) {
+    // The lane's places in a tile: row lane & 15 and its unit 0 for keys, the quads of columns 0..15
+    // for values.  Others differ by bits of the unit alone; taken off the slot's address, which
+    // changes, they cost an instruction each and no register.
+    const int kat = (lane & 15) * KT::ROWB + (((BF16 ? g4 : 2 * g4) ^ KT::swz(lane & 15)) << 4);
+    auto kfrag = [&](const char* kt, int y, int kk) __attribute__((always_inline)) {
+        const unsigned p = lds_at(kt) + kat + 16 * y * KT::ROWB;
         if constexpr (BF16) {
-            return *reinterpret_cast<const typename T::F8*>(kt + r * KT::ROWB + (((4 * kk + g4) ^ KT::swz(r)) << 4));
+            return lds_read<typename T::F8>(p ^ (kk << 6));
         } else {
-            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(kt + r * KT::ROWB + (((8 * kk + 2 * g4) ^ KT::swz(r)) << 4));
-            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(kt + r * KT::ROWB + (((8 * kk + 2 * g4 + 1) ^ KT::swz(r)) << 4));
+            const f32x4_t lo = lds_read<f32x4_t>(p ^ (kk << 7)), hi = lds_read<f32x4_t>(p ^ (kk << 7) ^ 16);
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     };
-    // columns 16 d .. 16 d + 15 of the tile's rows, as the A operand over its 32 rows
-    auto vfrag = [&](const char* vt, int d) __attribute__((always_inline)) {
-        typename T::F8 f;
+    const int vrow0 = 4 * g4 + ((lane & 15) >> 2);
+    const int vat0 = vrow0 * VT::ROWB + ((((lane & 3) >> 1) ^ VT::swz(vrow0)) << 4) + (lane & 1) * 8;
+    // columns 16 d .. 16 d + 15 of the tile's rows, as the A operand over its 32 rows, for d = d0 and d0 + 1
+    auto vfrags = [&](typename T::F8 (&f)[2], const char* vt, int d0) __attribute__((always_inline)) {
         if constexpr (BF16) {
+            unsigned at[4];
+            bf16x4_t x[4];
+            // rows r and r + 16 have the same permutation
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const int i = lane & 15, r = 16 * hh + 4 * g4 + (i >> 2), u = 2 * d + ((i & 3) >> 1);
-                const char* p = vt + r * VT::ROWB + ((u ^ VT::swz(r)) << 4) + (i & 1) * 8;
-                const auto x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((KDA_LDS bf16x4_t*)p);
+            for (int n = 0; n < 4; ++n) at[n] = (lds_at(vt) + vat0 + 16 * (n & 1) * VT::ROWB) ^ ((d0 + n / 2) << 5);
+            read_quads<4>(x, at);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[4 * hh + e] = x[e];
-            }
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[n / 2][4 * (n & 1) + e] = x[n][e];
         } else {
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int r = 16 * (s >> 2) + 4 * g4 + (s & 3), u = 4 * d + ((lane & 15) >> 2);
-                f[s] = *reinterpret_cast<const float*>(vt + r * VT::ROWB + ((u ^ VT::swz(r)) << 4) + (lane & 3) * 4);
-            }
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const int r = 16 * (s >> 2) + 4 * g4 + (s & 3), u = 4 * (d0 + n) + ((lane & 15) >> 2);
+                    f[n][s] = *reinterpret_cast<const float*>(vt + r * VT::ROWB + ((u ^ VT::swz(r)) << 4) + (lane & 3) * 4);
+                }
         }
-        return f;
     };
 
     // One tile into the rows' statistics and outputs.  MASKED: the tile holds drafted positions or
@@ -313,7 +327,7 @@ __global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW), (TreeSh
         for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) {
-                const typename T::F8 k = kfrag(kt, 16 * y + (lane & 15), kk);
+                const typename T::F8 k = kfrag(kt, y, kk);
 #pragma unroll
                 for (int x = 0; x < NQ; ++x) s[x][y] = mma8<BF16>(s[x][y], k, q[x][kk]);
             }
@@ -371,10 +385,13 @@ __global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW), (TreeSh
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            const typename T::F8 v = vfrag(vt, d);
+        for (int d = 0; d < ND; d += 2) {
+            typename T::F8 v[2];
+            vfrags(v, vt, d);
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) o[x][d] = mma8<BF16>(o[x][d], v, p[x]);
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) o[x][d + n] = mma8<BF16>(o[x][d + n], v[n], p[x]);
         }
     };
 
@@ -382,6 +399,7 @@ __global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW), (TreeSh
     int tok[NS + 1];
 #pragma unroll
     for (int n = 0; n < NS; ++n) tok[n] = lookup(n);
+    loads_done();
 #pragma unroll
     for (int n = 0; n < NS - 1; ++n)
         if (n < slots) stage(n, tok[n]);
