@@ -67,10 +67,13 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a, float 
     const int wrow = row0 + 32 * wave;               // the wave's first row
     const int wtiles = wrow < st.len ? (wrow + 31) / BN + 1 : 0;  // tiles it needs
 
-    auto stage_tile = [&](int t) __attribute__((always_inline)) {
-        char* b = lds[t & 1];
-        KT::template stage<kWaves, BN>(b, kb + static_cast<size_t>(t) * BN * ks, st.len - t * BN, ks, ksrc, wave);
-        VT::template stage<kWaves, BN>(b + KB, vb + static_cast<size_t>(t) * BN * vs, st.len - t * BN, vs, vsrc, wave);
+    // Keys go two tiles ahead, values one: while a tile's weights are formed, the next tile's scores
+    // are (below), so its keys are needed a step earlier.
+    auto stage_k = [&](int t) __attribute__((always_inline)) {
+        KT::template stage<kWaves, BN>(lds[t & 1], kb + static_cast<size_t>(t) * BN * ks, st.len - t * BN, ks, ksrc, wave);
+    };
+    auto stage_v = [&](int t) __attribute__((always_inline)) {
+        VT::template stage<kWaves, BN>(lds[t & 1] + KB, vb + static_cast<size_t>(t) * BN * vs, st.len - t * BN, vs, vsrc, wave);
     };
 
     f32x16_t o[VT::ND];
@@ -79,14 +82,15 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a, float 
     float mc = -INFINITY;  // running maximum of c s
     float l = 0.f;         // this half-wave's part of the row's sum
 
-    // One tile into the row's statistics and O.  LAST: the wave's last tile, which holds the
-    // diagonal; a step of its own keeps the masks out of the loop over the others.
-    auto step = [&](int t, auto LAST) __attribute__((always_inline)) {
-        const char* kt = lds[t & 1];
-        const char* vt = kt + KB;
-        f32x16_t s[NS];
+    auto scores = [&](int t, f32x16_t (&s)[NS]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int n = 0; n < NS; ++n) s[n] = KT::rows_times(f32x16_t{}, kt, kat, 32 * n, q);
+        for (int n = 0; n < NS; ++n) s[n] = KT::rows_times(f32x16_t{}, lds[t & 1], kat, 32 * n, q);
+    };
+    // One tile's scores into the row's statistics and O.  LAST: the wave's last tile, which holds the
+    // diagonal; otherwise the next tile's scores go to `s1`, between the two dependent halves of the
+    // step: their products run while the weights are formed.
+    auto step = [&](int t, f32x16_t (&s)[NS], f32x16_t (&s1)[NS], auto LAST) __attribute__((always_inline)) {
+        const char* vt = lds[t & 1] + KB;
         if constexpr (LAST) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
@@ -113,6 +117,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a, float 
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[dt][i] *= r;
         }
+        if constexpr (!LAST) scores(t + 1, s1);
         ColOp<BF16> p[NS];
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
@@ -139,21 +144,37 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a, float 
         }
     };
 
-    // every wave passes every tile's barrier; each works on its own tiles
+    // Every wave passes every tile's barrier; each works on its own tiles.  Past it, tile t's values
+    // and tile t + 1's keys are there, and nobody reads tile t's keys or tile t - 1's values any more.
     auto next = [&](int t) __attribute__((always_inline)) {
         lds_ready();
-        if (t + 1 < tiles) stage_tile(t + 1);
+        if (t + 2 < tiles) stage_k(t + 2);
+        if (t + 1 < tiles) stage_v(t + 1);
     };
-    stage_tile(0);
+    stage_k(0);
+    stage_v(0);
     loads_done();
+    lds_ready();
+    if (1 < tiles) stage_k(1);
+    f32x16_t sa[NS], sb[NS];
+    if (wtiles > 0) scores(0, sa);
     int t = 0;
-    for (; t < wtiles - 1; ++t) {
+    for (; t + 2 < wtiles; t += 2) {
         next(t);
-        step(t, std::false_type{});
+        step(t, sa, sb, std::false_type{});
+        next(t + 1);
+        step(t + 1, sb, sa, std::false_type{});
+    }
+    if (t + 1 < wtiles) {
+        next(t);
+        step(t, sa, sb, std::false_type{});
+        ++t;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) sa[n] = sb[n];
     }
     if (t < wtiles) {
         next(t);
-        step(t, std::true_type{});
+        step(t, sa, sb, std::true_type{});
         ++t;
     }
     for (; t < tiles; ++t) next(t);
