@@ -33,8 +33,8 @@ def attn_prefill_backward(q, k, v, o, lse, d_o, cu_seqlens, N, T_tot, H_q, H_kv,
                                         workspace_bytes, stream)
 
 
-def attn_prefill_backward_workspace_size(T_tot, H_q) -> int:
-    return int(load().attn_prefill_backward_workspace_size(T_tot, H_q))
+def attn_prefill_backward_workspace_size(N, T_tot, H_q, H_kv, d_k, d_v, dtype) -> int:
+    return int(load().attn_prefill_backward_workspace_size(N, T_tot, H_q, H_kv, d_k, d_v, dtype))
 
 
 def attn_tree_decode(q, k_cache, v_cache, block_table, ctx_lens, cu_q, tree_mask, N, T_q, H_q, H_kv, d_k, d_v, n_pages,
@@ -207,7 +207,7 @@ def _attn_backward_on(q, k, v, o, lse, d_o, cu_seqlens, scale, workspace, stream
     d_q = torch.empty((T, Hq, dk), dtype=q.dtype, device=dev)
     d_k = torch.empty((T, Hkv, dk), dtype=q.dtype, device=dev)
     d_v = torch.empty((T, Hkv, dv), dtype=q.dtype, device=dev)
-    ws = _workspace(workspace, attn_prefill_backward_workspace_size(T, Hq), dev)
+    ws = _workspace(workspace, attn_prefill_backward_workspace_size(N, T, Hq, Hkv, dk, dv, code), dev)
     _check(attn_prefill_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), d_o.data_ptr(),
                                  cu_seqlens.data_ptr(), N, T, Hq, Hkv, dk, dv, *strides, _scale(scale, dk), code,
                                  d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(), ws.data_ptr(), ws.numel(), stream))

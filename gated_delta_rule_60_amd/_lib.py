@@ -69,7 +69,7 @@ SIGNATURES = {
     "attn_prefill_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _fp, _vp, _ip, _i32, _i64, _i32, _i32, _i32, _i32,
                                              _i64, _i64, _i64, ctypes.c_float, ctypes.c_int, _vp, _vp, _vp, _vp, _sz,
                                              _vp]),
-    "attn_prefill_backward_workspace_size": (_sz, [_i64, _i32]),
+    "attn_prefill_backward_workspace_size": (_sz, [_i32, _i64, _i32, _i32, _i32, _i32, ctypes.c_int]),
     "attn_tree_decode": (ctypes.c_int, [_vp, _vp, _vp, _ip, _ip, _ip, _vp, _i32, _i64, _i32, _i32, _i32, _i32, _i32,
                                         _i32, _i32, _i64, ctypes.c_float, ctypes.c_int, _vp, _fp, _vp, _sz, _vp]),
     "attn_tree_decode_workspace_size": (_sz, [_i32, _i64, _i32, _i32, _i32, _i32, _i32]),

@@ -91,15 +91,18 @@ kda_status attn_prefill(const void* q, const void* k, const void* v, const int32
     const kda::AttnArgs a{q, k, v, cu_seqlens, N, static_cast<int32_t>(T_tot), H_q, H_kv, d_k, d_v,
                           static_cast<int32_t>(q_stride), static_cast<int32_t>(k_stride), static_cast<int32_t>(v_stride),
                           scale, dtype == KDA_DTYPE_BF16, o, lse, stream,
-                          kda::attn_split(N, T_tot, H_q, kda::device_cus_or_default())};
+                          kda::attn_split(N, T_tot, H_q, dtype == KDA_DTYPE_BF16, kda::device_cus_or_default())};
     (void)hipGetLastError();  // report only this launch's status
     const hipError_t e = kda::launch_attn_prefill(a);
     return e == hipSuccess ? KDA_OK : hip_fail(e, "attention kernel launch");
 }
 
-size_t attn_prefill_backward_workspace_size(int64_t T_tot, int32_t H_q) {
-    if (T_tot < 0 || T_tot > (int64_t{1} << 30) || H_q < 1 || H_q > 4096) return 0;
-    return kda::attn_bwd_workspace_bytes(T_tot, H_q);
+size_t attn_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k, int32_t d_v,
+                                            kda_dtype dtype) {
+    if (N < 1 || T_tot < 0 || T_tot > (int64_t{1} << 30) || H_kv < 1 || H_q < 1 || H_q > 4096 || H_q % H_kv != 0 ||
+        !supported_dim(d_k) || !supported_dim(d_v) || (dtype != KDA_DTYPE_BF16 && dtype != KDA_DTYPE_F32))
+        return 0;
+    return kda::attn_bwd_plan(N, T_tot, H_q, H_kv, d_k, d_v, dtype == KDA_DTYPE_BF16, kda::device_cus_or_default()).bytes;
 }
 
 kda_status attn_prefill_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
@@ -114,7 +117,9 @@ kda_status attn_prefill_backward(const void* q, const void* k, const void* v, co
         return fail(KDA_ERR_INVALID_ARG, "lse, d_o, d_q, d_k and d_v must not be NULL when T_tot > 0");
     for (const void* p : {d_o, static_cast<const void*>(d_q), static_cast<const void*>(d_k_out), static_cast<const void*>(d_v_out)})
         if (!aligned(p, 16)) return fail(KDA_ERR_INVALID_ARG, "gradient pointers must be 16-byte aligned");
-    if (workspace_bytes < kda::attn_bwd_workspace_bytes(T_tot, H_q))
+    const kda::BwdPlan plan =
+        kda::attn_bwd_plan(N, T_tot, H_q, H_kv, d_k, d_v, dtype == KDA_DTYPE_BF16, kda::device_cus_or_default());
+    if (workspace_bytes < plan.bytes)
         return fail(KDA_ERR_INVALID_ARG, "workspace smaller than attn_prefill_backward_workspace_size");
     if (T_tot > 0 && !workspace) return fail(KDA_ERR_INVALID_ARG, "workspace must not be NULL");
     if (!aligned(workspace, 256)) return fail(KDA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -122,10 +127,11 @@ kda_status attn_prefill_backward(const void* q, const void* k, const void* v, co
     const kda::AttnArgs a{q, k, v, cu_seqlens, N, static_cast<int32_t>(T_tot), H_q, H_kv, d_k, d_v,
                           static_cast<int32_t>(q_stride), static_cast<int32_t>(k_stride), static_cast<int32_t>(v_stride),
                           scale, dtype == KDA_DTYPE_BF16, const_cast<void*>(o), const_cast<float*>(lse), stream,
-                          kda::attn_split(N, T_tot, H_q, kda::device_cus_or_default())};
+                          kda::attn_split(N, T_tot, H_q, dtype == KDA_DTYPE_BF16, kda::device_cus_or_default())};
     (void)hipGetLastError();  // report only this launch's status
     const hipError_t e = kda::launch_attn_bwd({a, d_o, d_q, d_k_out, d_v_out, workspace,
-                                                kda::attn_split(N, T_tot, H_kv, kda::device_cus_or_default())});
+                                                reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.stats_bytes),
+                                                plan.head_parts});
     return e == hipSuccess ? KDA_OK : hip_fail(e, "attention backward kernel launch");
 }
 

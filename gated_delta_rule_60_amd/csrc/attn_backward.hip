@@ -371,6 +371,8 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_dkv_split_kernel(AttnBwdArgs 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = blockIdx.x % a.Hkv;
     const int group = a.Hq / a.Hkv;
+    // the query heads of this workgroup, of those of the key head
+    const int h0 = group * blockIdx.y / b.head_parts, heads = group * (blockIdx.y + 1) / b.head_parts - h0;
     SeqTile st;
     if (!find_tile<32>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hkv, true, st)) return;
 
@@ -388,7 +390,7 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_dkv_split_kernel(AttnBwdArgs 
     const int first = key0 / TG, groups = (st.len + TG - 1) / TG - first;  // row groups of a head
     auto stage_group = [&](int slot, int hh, int t) __attribute__((always_inline)) {
         char* l = lds + slot * SLOT;
-        const int h = g * group + hh;
+        const int h = g * group + h0 + hh;
         const size_t r = static_cast<size_t>(st.beg) + static_cast<size_t>(t) * TG;
         const int left = st.len - t * TG;
         QT::template stage<kWaves, TG>(l, static_cast<const char*>(a.q) + (r * a.q_stride + static_cast<size_t>(h) * DK) * Op::ES, left,
@@ -410,7 +412,7 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_dkv_split_kernel(AttnBwdArgs 
 #pragma unroll
     for (int dt = 0; dt < OT::ND; ++dt) dv[dt] = f32x16_t{};
 
-    const int steps = groups * group;
+    const int steps = groups * heads;
     int hh = 0, t = first, slot = 0;
     loads_done();
     for (int n = 0; n < steps; ++n) {
@@ -467,8 +469,38 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_dkv_split_kernel(AttnBwdArgs 
     join_waves(dk, lds, wave, lane);
     join_waves(dv, lds, wave, lane);
     if (wave != 0) return;
+    if (b.head_parts > 1) {
+        float* p = b.parts + ((static_cast<size_t>(blockIdx.y) * a.T_tot + tok) * a.Hkv + g) * (DK + DV);
+        store_col_as_row<false, DK>(p, dk, a.scale, half, live);
+        store_col_as_row<false, DV>(p + DK, dv, 1.f, half, live);
+        return;
+    }
     store_col_as_row<BF16, DK>(static_cast<G*>(b.d_k) + (tok * a.Hkv + g) * DK, dk, a.scale, half, live);
     store_col_as_row<BF16, DV>(static_cast<G*>(b.d_v) + (tok * a.Hkv + g) * DV, dv, 1.f, half, live);
+}
+
+// Sums the parts of dk and dv that the workgroups of different query heads left, in their order.
+template <bool BF16, int DK, int DV>
+__global__ __launch_bounds__(256) void attn_bwd_join_kernel(AttnBwdArgs b) {
+    using T = Elem<BF16>;
+    const AttnArgs& a = b.f;
+    const int g = blockIdx.x % a.Hkv;
+    SeqTile st;
+    if (!find_tile<32>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hkv, true, st)) return;
+    constexpr int Q = (DK + DV) / 4;
+    for (int x = threadIdx.x; x < 32 * Q; x += 256) {
+        const int row = st.tile * 32 + x / Q, e = 4 * (x % Q);
+        if (row >= st.len) return;
+        const size_t at = (static_cast<size_t>(st.beg) + row) * a.Hkv + g;
+        const float* p = b.parts + at * (DK + DV) + e;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < b.head_parts; ++s) {
+            const f32x4_t z = *reinterpret_cast<const f32x4_t*>(p + static_cast<size_t>(s) * a.T_tot * a.Hkv * (DK + DV));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] += z[i];
+        }
+        T::store4(e < DK ? static_cast<typename T::G*>(b.d_k) + at * DK + e : static_cast<typename T::G*>(b.d_v) + at * DV + e - DK, y);
+    }
 }
 
 namespace {
@@ -489,7 +521,13 @@ hipError_t launch(const AttnBwdArgs& b) {
         hipLaunchKernelGGL((attn_bwd_dq_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hq)), threads, 0, st, b, c, stats);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (b.split_kv)
+    if (b.head_parts > 1) {
+        hipLaunchKernelGGL((attn_bwd_dkv_split_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units32 * a.Hkv), b.head_parts), threads,
+                           0, st, b, c, stats);
+        const hipError_t e2 = hipGetLastError();
+        if (e2 != hipSuccess) return e2;
+        hipLaunchKernelGGL((attn_bwd_join_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units32 * a.Hkv)), dim3(256), 0, st, b);
+    } else if (b.head_parts == 1)
         hipLaunchKernelGGL((attn_bwd_dkv_split_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units32 * a.Hkv)), threads, 0, st, b, c, stats);
     else
         hipLaunchKernelGGL((attn_bwd_dkv_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hkv)), threads, 0, st, b, c, stats);
@@ -516,7 +554,22 @@ hipError_t launch_dk(const AttnBwdArgs& b) {
 
 }  // namespace
 
-size_t attn_bwd_workspace_bytes(int64_t T_tot, int32_t Hq) { return static_cast<size_t>(T_tot) * Hq * 2 * sizeof(float); }
+// Where even the split blocks of the key heads leave compute units idle, the query heads of a key
+// head go to several workgroups and their sums are joined (5 ragged fp32 sequences of 924 tokens,
+// 8/2 heads of 64: dk/dv 107 us in one part).
+BwdPlan attn_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t d_k, int32_t d_v, bool bf16, int cus) {
+    BwdPlan p;
+    p.stats_bytes = (static_cast<size_t>(T_tot) * Hq * 2 * sizeof(float) + 255) / 256 * 256;
+    p.head_parts = 0;
+    p.bytes = p.stats_bytes;
+    if (T_tot > 0 && attn_split(N, T_tot, Hkv, bf16, cus)) {
+        const int64_t blocks = ((T_tot + 31) / 32 + N) * Hkv;
+        const int64_t parts = 2 * static_cast<int64_t>(cus) / blocks, group = Hq / Hkv;
+        p.head_parts = static_cast<int32_t>(parts < 1 ? 1 : parts > group ? group : parts);
+        if (p.head_parts > 1) p.bytes += static_cast<size_t>(p.head_parts) * T_tot * Hkv * (d_k + d_v) * sizeof(float);
+    }
+    return p;
+}
 
 hipError_t launch_attn_bwd(const AttnBwdArgs& b) {
     if (b.f.T_tot == 0) return hipSuccess;

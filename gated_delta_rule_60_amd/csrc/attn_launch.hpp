@@ -29,7 +29,7 @@ struct AttnArgs {
 
 // Whether a batch leaves so many compute units idle that its pieces are split
 // over the waves of four times as many workgroups.
-bool attn_split(int32_t N, int64_t T_tot, int32_t heads, int cus);
+bool attn_split(int32_t N, int64_t T_tot, int32_t heads, bool bf16, int cus);
 
 struct AttnBwdArgs {
     AttnArgs f;        // o and lse are read
@@ -37,9 +37,17 @@ struct AttnBwdArgs {
     void* d_q;         // [T_tot, Hq, d_k]
     void* d_k;         // [T_tot, Hkv, d_k]
     void* d_v;         // [T_tot, Hkv, d_v]
-    void* workspace;   // attn_bwd_workspace_bytes
-    bool split_kv;     // attn_split over the key heads
+    void* workspace;   // attn_bwd_plan's bytes
+    float* parts;      // [head_parts][T_tot][Hkv][d_k + d_v], if head_parts > 1
+    int32_t head_parts;  // 0: whole blocks of 128 keys; else blocks of 32, the query heads in so many parts
 };
+
+// Launch shape of the dk/dv pass, and what the backward needs: the row statistics, then the parts.
+struct BwdPlan {
+    size_t stats_bytes, bytes;
+    int32_t head_parts;
+};
+BwdPlan attn_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t d_k, int32_t d_v, bool bf16, int cus);
 
 // Attention of drafted tokens over a paged cache.
 struct TreeArgs {
@@ -111,6 +119,5 @@ hipError_t launch_kv_compact(const PageArgs& a, const CacheArgs& c, const int32_
 
 hipError_t launch_attn_prefill(const AttnArgs& a);
 hipError_t launch_attn_bwd(const AttnBwdArgs& a);
-size_t attn_bwd_workspace_bytes(int64_t T_tot, int32_t Hq);
 
 }  // namespace kda

@@ -452,9 +452,8 @@ kda_status attn_prefill(const void* q, const void* k, const void* v, const int32
  *   d_q [T_tot, H_q, d_k], d_k_out [T_tot, H_kv, d_k], d_v_out [T_tot, H_kv,
  *   d_v]: dtype, written, contiguous.  Sums are fp32; for bf16 p and ds are
  *   rounded to bf16 before the products that sum them.
- *   workspace  at least attn_prefill_backward_workspace_size bytes (two
- *   floats per row and head), 256-byte aligned, used until the queued work
- *   ends.
+ *   workspace  at least attn_prefill_backward_workspace_size bytes, 256-byte
+ *   aligned, used until the queued work ends.
  * Rows at or past cu[N] are not written.  Each gradient is summed in one
  * order: the same inputs give the same bits.  A non-finite input may reach
  * every gradient of its own sequence.
@@ -467,8 +466,11 @@ kda_status attn_prefill_backward(const void* q, const void* k, const void* v, co
                                  void* d_k_out, void* d_v_out, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
-/* Workspace bytes attn_prefill_backward needs (0 for unsupported sizes). */
-size_t attn_prefill_backward_workspace_size(int64_t T_tot, int32_t H_q);
+/* Workspace bytes attn_prefill_backward needs on the current device (0 for
+ * unsupported sizes): two floats per row and query head, and for small
+ * batches the parts of d_k and d_v that different query heads give. */
+size_t attn_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv,
+                                            int32_t d_k, int32_t d_v, kda_dtype dtype);
 
 /*
  * A paged cache holds the keys and values of many sequences of growing

@@ -90,6 +90,18 @@ def test_backward_refuses(kw, status, needle):
     assert needle in kda.kda_last_error()
 
 
+def test_backward_workspace():
+    size = kda.attn_prefill_backward_workspace_size
+    big = size(8, 32677, 32, 8, 128, 128, BF16)  # the batch fills the device: two floats a row and head
+    assert big == (32677 * 32 * 8 + 255) // 256 * 256
+    few = size(5, 924, 8, 2, 64, 64, F32)        # a part of dk and dv for every query head of a key head
+    assert few == 924 * 8 * 8 + 4 * 924 * 2 * 128 * 4
+    assert size(5, 924, 2, 2, 64, 64, F32) == (924 * 2 * 8 + 255) // 256 * 256  # one head: one part
+    for bad in ((0, 9, 4, 2, 64, 64, BF16), (1, -1, 4, 2, 64, 64, BF16), (1, 9, 3, 2, 64, 64, BF16),
+                (1, 9, 4, 2, 48, 64, BF16), (1, 9, 4, 2, 64, 64, 5)):
+        assert size(*bad) == 0
+
+
 def _tree(**kw):
     a = dict(q=FAKE, k_cache=FAKE, v_cache=FAKE, block_table=FAKE, ctx_lens=FAKE, cu_q=FAKE, tree_mask=FAKE, N=4, T_q=16,
              H_q=8, H_kv=2, d_k=64, d_v=128, n_pages=100, page_size=16, max_pages=32, q_stride=512, scale=0.1,
