@@ -48,8 +48,39 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* s_wave, int64_
     return before + x;
 }
 
+// The same for sums that fit 32 bits, by lane moves instead of shuffles.
+__device__ __forceinline__ int block_scan(int x, int* s_wave, int& total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    x = wave_scan(x);
+    __syncthreads();
+    if (lane == 63) s_wave[wave] = x;
+    __syncthreads();
+    const int all = wave_scan(lane < kThreads / 64 ? s_wave[lane & (kThreads / 64 - 1)] : 0);
+    total = __builtin_amdgcn_readlane(all, 63);
+    return x + (wave ? __builtin_amdgcn_readlane(all, __builtin_amdgcn_readfirstlane(wave) - 1) : 0);
+}
+
+// Whether an earlier request of `list` (n of them, in LDS, the rest of it -1) names the same row;
+// `among`: whether any request names `other`.
+__device__ __forceinline__ bool repeated(const int* list, int n, int i, int row, int other, bool& among) {
+    bool again = false;
+    among = false;
+    for (int j = 0; j < n; j += 8) {
+        int x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = list[j + e];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            again |= x[e] == row && j + e < i;
+            among |= x[e] == other;
+        }
+    }
+    return again;
+}
+
 // The request that entry e belongs to: the first whose inclusive sum passes e.
-__device__ __forceinline__ int request_of(const int64_t* upto, int n, int64_t e) {
+template <class N>
+__device__ __forceinline__ int request_of(const N* upto, int n, N e) {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -78,8 +109,8 @@ __global__ __launch_bounds__(kThreads) void kv_reserve_kernel(PageArgs a, const 
     const int row = i < n ? rows[i] : -1;
     s_row[i] = row;
     __syncthreads();
-    bool good = i < n && row >= 0 && row < a.n_rows;
-    for (int j = 0; j < i && good; ++j) good = s_row[j] != row;  // a row's first request counts
+    bool among;
+    bool good = !repeated(s_row, n, i, row, -2, among) && i < n && row >= 0 && row < a.n_rows;  // a row's first request counts
     int need = 0, held = 0;
     if (good) {
         const int64_t len = a.lens[row], more = n_tokens[i];
@@ -132,78 +163,78 @@ __global__ __launch_bounds__(kThreads) void kv_reserve_kernel(PageArgs a, const 
 // stays.
 __global__ __launch_bounds__(kThreads) void kv_free_kernel(PageArgs a, const int32_t* rows, int n) {
     constexpr int kMark = 1 << 30;  // n max_pages <= 2^29
-    __shared__ int s_row[kThreads];
-    __shared__ int64_t s_upto[kThreads], s_wave[kThreads / 64];
+    constexpr int kRound = kBatch * kThreads;
+    __shared__ int s_row[kThreads], s_upto[kThreads], s_wave[kThreads / 64];
     const int i = threadIdx.x;
     const int row = i < n ? rows[i] : -1;
     s_row[i] = row;
     __syncthreads();
-    bool good = i < n && row >= 0 && row < a.n_rows;
-    for (int j = 0; j < i && good; ++j) good = s_row[j] != row;
+    bool among;
+    const bool good = !repeated(s_row, n, i, row, -2, among) && i < n && row >= 0 && row < a.n_rows;
     int held = 0;
     if (good) {
         held = a.held[row];
         held = held < 0 ? 0 : (held > a.max_pages ? a.max_pages : held);
     }
-    int64_t total;
+    int total;
     s_upto[i] = block_scan(held, s_wave, total);
     __syncthreads();
     const int have = free_pages(a);
 
-    // where entry e lies in the table, and its page (-1: none)
-    auto entry = [&](int64_t e, int64_t& at) __attribute__((always_inline)) {
-        at = -1;
-        if (e >= total) return;
-        const int r = request_of(s_upto, n, e);
-        at = static_cast<int64_t>(s_row[r]) * a.max_pages + (e - (r ? s_upto[r - 1] : 0));
-    };
-    auto pages_of = [&](int64_t e0, int64_t (&at)[kBatch], int (&page)[kBatch]) __attribute__((always_inline)) {
+    // where the thread's entries e0 + b kThreads + i lie in the table, and their pages (-1: none);
+    // one round of them stays in registers
+    int64_t at[kBatch];
+    int page[kBatch], ref[kBatch];
+    auto entries = [&](int e0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) entry(e0 + b * kThreads + i, at[b]);
+        for (int b = 0; b < kBatch; ++b) {
+            const int e = e0 + b * kThreads + i;
+            at[b] = -1;
+            if (e0 + b * kThreads < total && e < total) {
+                const int r = request_of(s_upto, n, e);
+                at[b] = static_cast<int64_t>(s_row[r]) * a.max_pages + (e - (r ? s_upto[r - 1] : 0));
+            }
+        }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             page[b] = at[b] >= 0 ? a.table[at[b]] : -1;
             if (page[b] >= a.n_pages) page[b] = -1;
         }
     };
+    auto counts = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) ref[b] = page[b] >= 0 ? load_ref(&a.refs[page[b]]) : 1;
+    };
 
-    for (int64_t e0 = 0; e0 < total; e0 += kBatch * kThreads) {
-        int64_t at[kBatch];
-        int page[kBatch];
-        pages_of(e0, at, page);
+    for (int e0 = 0; e0 < total; e0 += kRound) {
+        entries(e0);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
             if (page[b] >= 0) atomicSub(&a.refs[page[b]], 1);
     }
     __threadfence();
     __syncthreads();
-    for (int64_t e0 = 0; e0 < total; e0 += kBatch * kThreads) {
-        int64_t at[kBatch];
-        int page[kBatch], ref[kBatch];
-        pages_of(e0, at, page);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) ref[b] = page[b] >= 0 ? load_ref(&a.refs[page[b]]) : 1;
+    for (int e0 = 0; e0 < total; e0 += kRound) {
+        if (total > kRound) entries(e0);
+        counts();
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
-            if (ref[b] == 0 || ref[b] < -(kMark / 2)) atomicMin(&a.refs[page[b]], static_cast<int>(e0 + b * kThreads + i) - kMark);
+            if (ref[b] == 0 || ref[b] < -(kMark / 2)) atomicMin(&a.refs[page[b]], e0 + b * kThreads + i - kMark);
     }
     __threadfence();
     __syncthreads();
-    int64_t pushed = 0;
-    for (int64_t e0 = 0; e0 < total; e0 += kBatch * kThreads) {
-        int64_t at[kBatch];
-        int page[kBatch], ref[kBatch];
-        pages_of(e0, at, page);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) ref[b] = page[b] >= 0 ? load_ref(&a.refs[page[b]]) : 1;
+    int pushed = 0;
+    for (int e0 = 0; e0 < total; e0 += kRound) {
+        if (total > kRound) entries(e0);
+        counts();
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             if (e0 + b * kThreads >= total) break;  // the same for every thread
-            const bool first = ref[b] == static_cast<int>(e0 + b * kThreads + i) - kMark;
-            int64_t all;
-            const int64_t upto = block_scan(first ? 1 : 0, s_wave, all);
+            const bool first = ref[b] == e0 + b * kThreads + i - kMark;
+            int all;
+            const int upto = block_scan(first ? 1 : 0, s_wave, all);
             if (first) {
-                const int64_t to = have + pushed + upto - 1;
+                const int to = have + pushed + upto - 1;
                 if (to < a.n_pages) a.free[to] = page[b];
                 a.refs[page[b]] = 0;
             }
@@ -215,23 +246,23 @@ __global__ __launch_bounds__(kThreads) void kv_free_kernel(PageArgs a, const int
         a.held[row] = 0;
         a.lens[row] = 0;
     }
-    if (i == 0 && pushed > 0) *a.n_free = static_cast<int>(have + pushed < a.n_pages ? have + pushed : a.n_pages);
+    if (i == 0 && pushed > 0) *a.n_free = have + pushed < a.n_pages ? have + pushed : a.n_pages;
 }
 
 // ---------------------------------------------------------------------------
 // fork: row dst[i] becomes a copy of row src[i]
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kThreads) void kv_fork_kernel(PageArgs a, const int32_t* src, const int32_t* dst, int n, int32_t* status) {
-    __shared__ int s_dst[kThreads];
-    __shared__ int64_t s_wave[kThreads / 64];
+    __shared__ int s_dst[kThreads], s_wave[kThreads / 64];
     const int i = threadIdx.x;
     const int from = i < n ? src[i] : -1, to = i < n ? dst[i] : -1;
     s_dst[i] = to;
     __syncthreads();
-    bool good = i < n && from >= 0 && from < a.n_rows && to >= 0 && to < a.n_rows;
     // every request sees the rows as they were: nobody copies a row that this call writes, and a
     // row's first request counts
-    for (int j = 0; j < n && good; ++j) good = s_dst[j] != from && (j >= i || s_dst[j] != to);
+    bool written;
+    bool good = !repeated(s_dst, n, i, to, from, written) && i < n && from >= 0 && from < a.n_rows && to >= 0 && to < a.n_rows;
+    good = good && !written;
     int len = 0, full = 0, part = 0;
     if (good) {
         len = a.lens[from];
@@ -242,8 +273,8 @@ __global__ __launch_bounds__(kThreads) void kv_fork_kernel(PageArgs a, const int
     }
     const int need = good ? part : 0;
     const int have = free_pages(a);
-    int64_t total;
-    const int64_t upto = block_scan(need, s_wave, total);
+    int total;
+    const int upto = block_scan(need, s_wave, total);
     const bool got = good && (need == 0 || upto <= have);
     if (i < n) status[i] = !good ? kBadRequest : got ? kOk : kNoPage;
     __syncthreads();  // every request has read the rows
@@ -256,7 +287,7 @@ __global__ __launch_bounds__(kThreads) void kv_fork_kernel(PageArgs a, const int
         a.lens[to] = len;
         a.held[to] = full + part;
     }
-    if (i == 0) *a.n_free = static_cast<int>(have - (total < have ? total : have));
+    if (i == 0) *a.n_free = have - (total < have ? total : have);
 }
 
 // The shared pages of request x (of one workgroup), and the rows of its last page that hold
