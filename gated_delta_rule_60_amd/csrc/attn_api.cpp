@@ -40,7 +40,8 @@ kda_status check_heads(int32_t H_q, int32_t H_kv, int32_t d_k, int32_t d_v, kda_
 }
 
 kda_status check_scale(float scale) {
-    if (!(scale > 0.f) || !std::isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "scale must be positive and finite");
+    if (!(scale > 0.f) || !std::isfinite(scale * 1.4427f))  // the kernels work in powers of two
+        return fail(KDA_ERR_INVALID_ARG, "scale must be positive, and scale log2(e) finite");
     return KDA_OK;
 }
 
@@ -152,10 +153,10 @@ kda_status check_cache(int32_t n_pages, int32_t page_size, int32_t max_pages) {
     return KDA_OK;
 }
 
-// Row tiles times key blocks must stay countable in 32 bits.
-bool tree_countable(const kda::TreePlan& p, int32_t max_pages, int32_t page_size, int32_t H_kv) {
+// Query rows, and row tiles times key blocks, must stay countable in 32 bits.
+bool tree_countable(const kda::TreePlan& p, int64_t T_q, int32_t max_pages, int32_t page_size, int32_t H_q, int32_t H_kv) {
     const int64_t blocks = static_cast<int64_t>(max_pages) * page_size / 128 + 1;
-    return p.tiles <= INT32_MAX / blocks && (p.items + p.tiles) * H_kv <= INT32_MAX;
+    return T_q * (H_q / H_kv) <= (int64_t{1} << 30) && p.tiles <= INT32_MAX / blocks && (p.items + p.tiles) * H_kv <= INT32_MAX;
 }
 
 }  // namespace
@@ -193,7 +194,7 @@ kda_status attn_tree_decode(const void* q, const void* k_cache, const void* v_ca
         return fail(KDA_ERR_INVALID_ARG, "lse, block_table, ctx_lens and cu_q must be 4-byte aligned");
     const kda::TreePlan plan = kda::tree_plan(N, T_q, H_q, H_kv, d_v, static_cast<int64_t>(max_pages) * page_size,
                                               kda::device_cus_or_default());
-    if (!tree_countable(plan, max_pages, page_size, H_kv))
+    if (!tree_countable(plan, T_q, max_pages, page_size, H_q, H_kv))
         return fail(KDA_ERR_INVALID_ARG, "too many drafted tokens for sequences this long");
     if (workspace_bytes < plan.bytes) return fail(KDA_ERR_INVALID_ARG, "workspace smaller than attn_tree_decode_workspace_size");
     if (plan.bytes > 0 && !workspace) return fail(KDA_ERR_INVALID_ARG, "workspace must not be NULL");

@@ -114,6 +114,7 @@ __device__ __forceinline__ bool find_item(const TreeArgs& a, int p, int rows, bo
         if (p < total) {
             const int l = __builtin_ctzll(__ballot(upto > p));
             const int r = p - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l));
+            if (r < 0) return false;  // offsets that overlap so far that the counts wrap
             t.chunks = __builtin_amdgcn_readlane(chunks, l);
             t.n = n0 + l;
             t.tok0 = __builtin_amdgcn_readlane(s.tok0, l);

@@ -423,7 +423,7 @@ kda_status kda_prefill_noalloc(const void* q, const void* k, const void* v,
  *              heads of a token are contiguous): at least H * d, a multiple
  *              of 16 bytes, at most 2^22.  Slices of one fused projection
  *              need no copy.
- *   scale      positive and finite
+ *   scale      positive, with scale log2(e) finite
  *   dtype      storage type of q, k, v and o.  Sums and softmax statistics
  *              are fp32; for bf16 the weights exp(s - max) are rounded to
  *              bf16 before they meet v.
@@ -432,7 +432,9 @@ kda_status kda_prefill_noalloc(const void* q, const void* k, const void* v,
  *              NULL if not wanted.  The backward pass needs it.
  * Rows of o and lse at or past cu[N] are not written.  A non-finite value in
  * a token's k or v reaches the rows of that token and the later ones of its
- * sequence only.
+ * sequence only.  Batches too small to fill the device split their keys over
+ * the waves of a workgroup, which changes rounding only: a sequence gives the
+ * same bits in any batch on the same side of that rule.
  */
 kda_status attn_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
                         int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k,

@@ -142,6 +142,8 @@ CACHE = [
     (dict(workspace=None), BAD, "workspace must not be NULL"),
     (dict(workspace=FAKE + 128), BAD, "256-byte aligned"),
     (dict(T_q=1 << 24, max_pages=1 << 26), BAD, "too many drafted tokens"),
+    (dict(T_q=1 << 24, H_q=256, q_stride=256 * 64), BAD, "too many drafted tokens"),
+    (dict(scale=3e38), BAD, "scale"),
 ])
 def test_tree_refuses(kw, status, needle):
     assert _tree(**kw) == status

@@ -248,6 +248,34 @@ def test_another_stream_and_graph_replays(dtype):
             assert torch.equal(x, y), f"replay {n}"
 
 
+@pytest.mark.parametrize("lens", [[40, 9], [300] * 60])
+def test_the_row_statistics_may_be_left_out(lens):
+    q, k, v, _, cu = _make(lens, 4, 2, 64, 32, "bf16", 6)
+    want, _ = kda.attn_prefill_t(q, k, v, cu)
+    o = torch.empty_like(want)
+    st = torch.cuda.current_stream().cuda_stream
+    rc = kda.attn_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu.data_ptr(), len(lens), sum(lens), 4, 2, 64, 32, 256, 128, 64,
+                          1 / 8, kda.KDA_DTYPE_BF16, o.data_ptr(), None, st)
+    assert rc == kda.KDA_OK
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
+
+
+def test_two_backward_calls_at_once():
+    a, b = _make([500, 33], 8, 2, 64, 64, "bf16", 1), _make([300, 7], 8, 2, 64, 64, "bf16", 2)
+    fwd = [kda.attn_prefill_t(*x[:3], x[4]) for x in (a, b)]
+    want = [kda.attn_prefill_backward_t(*x[:3], *f, x[3], x[4]) for x, f in zip((a, b), fwd)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, (x, f) in enumerate(zip((a, b), fwd)):
+            got[i].append(kda.attn_prefill_backward_t(*x[:3], *f, x[3], x[4], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(p, q) for g in got[i] for p, q in zip(g, want[i]))
+
+
 def test_offsets_past_32_bits():
     """Token rows 2^31 elements and more into a wide fused buffer."""
     stride, t = 1 << 16, 33000  # 2.16e9 elements, 4.3 GB
@@ -256,11 +284,13 @@ def test_offsets_past_32_bits():
     fused[:, :512] = torch.randn(t, 512, generator=g, device="cuda")
     q, k, v = fused[:, :256].view(t, 2, 128), fused[:, 256:384].view(t, 1, 128), fused[:, 384:512].view(t, 1, 128)
     cu = torch.tensor([0, 32800, 33000], dtype=torch.int32).cuda()
+    d_o = torch.randn(t, 2, 128, generator=g, device="cuda").bfloat16()
     o, lse = kda.attn_prefill_t(q, k, v, cu)
+    grads = kda.attn_prefill_backward_t(q, k, v, o, lse, d_o, cu)
     tail = [x[32800:].contiguous() for x in (q, k, v)]
-    want = attn_ref.prefill(*tail, [200], 1 / math.sqrt(128))
-    attn_ref.check(o[32800:], want["o"], "o")
-    attn_ref.check(lse[32800:], want["lse"], "lse")
+    want = attn_ref.prefill(*tail, [200], 1 / math.sqrt(128), d_o[32800:])
+    for name, got in zip(("o", "lse", "d_q", "d_k", "d_v"), (o, lse, *grads)):
+        attn_ref.check(got[32800:], want[name], name)
 
 
 def test_torch_helper_refusals():
