@@ -10,6 +10,12 @@
 // query rows of a block of keys (dk, dv).  Scores are formed in both, 7
 // products instead of 5, and in return every sum has one owner and one
 // order: no atomics, the same bits every time.
+//
+// D_i = do_i . o_i takes o as stored.  In bf16 its rounding matters where a
+// row has few keys (o is then as large as v, and ds is too): the first 128
+// rows of a sequence take D_i = sum_j p_ij dp_ij instead, the same number
+// from unrounded weights (77 tokens, 128/64 channels: d_q 2.4e-3 from its
+// value instead of 2.8e-3; 1.7e-3 is its own rounding).
 #include <hip/hip_runtime.h>
 
 #include "attn_device.hpp"
@@ -69,11 +75,6 @@ __global__ __launch_bounds__(256, BF16 || DK < 128 ? 2 : 1) void attn_bwd_dq_ker
         D = half_sum(D);
         if (live) lse2 = a.lse[tok * a.Hq + h] * kLog2e;
     }
-    if (live && half == 0) {
-        stats.lse2[static_cast<size_t>(h) * a.T_tot + tok] = lse2;
-        stats.D[static_cast<size_t>(h) * a.T_tot + tok] = D;
-    }
-
     const int ks = a.k_stride * Op::ES, vs = a.v_stride * Op::ES;
     const char* kb = static_cast<const char*>(a.k) + (static_cast<size_t>(st.beg) * a.k_stride + static_cast<size_t>(g) * DK) * Op::ES;
     const char* vb = static_cast<const char*>(a.v) + (static_cast<size_t>(st.beg) * a.v_stride + static_cast<size_t>(g) * DV) * Op::ES;
@@ -91,6 +92,34 @@ __global__ __launch_bounds__(256, BF16 || DK < 128 ? 2 : 1) void attn_bwd_dq_ker
         KT::template stage<kWaves, BN>(l, kb + static_cast<size_t>(t) * BN * ks, st.len - t * BN, ks, ksrc, wave);
         VT::template stage<kWaves, BN>(l + KB, vb + static_cast<size_t>(t) * BN * vs, st.len - t * BN, vs, vsrc, wave);
     };
+
+    if (BF16 && st.tile == 0) {  // D from the weights: the same walk over the keys, two or three tiles
+        float sum = 0.f;
+        stage_tile(0);
+        loads_done();
+        for (int t = 0; t < tiles; ++t) {
+            lds_ready();
+            if (t + 1 < tiles) stage_tile(t + 1);
+            if (t >= wtiles) continue;
+            const char* kt = lds[t & 1];
+#pragma unroll 1
+            for (int n = 0; n < BN / 32; ++n) {
+                const f32x16_t s = KT::rows_times(f32x16_t{}, kt, kat, 32 * n, q);
+                const f32x16_t dp = VT::rows_times(f32x16_t{}, kt + KB, vat, 32 * n, d_o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse2)) * dp[i];
+                    sum += t * BN + 32 * n + 8 * (i >> 2) + 4 * half + (i & 3) <= qi ? x : 0.f;
+                }
+            }
+        }
+        D = half_sum(sum);
+        lds_ready();  // the tiles are read: they are filled again from the first
+    }
+    if (live && half == 0) {
+        stats.lse2[static_cast<size_t>(h) * a.T_tot + tok] = lse2;
+        stats.D[static_cast<size_t>(h) * a.T_tot + tok] = D;
+    }
 
     f32x16_t dq[KT::ND];
 #pragma unroll
@@ -274,6 +303,7 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_dq_split_kernel(AttnBwdArgs b
     constexpr int NBUF = 2 * (KB + VB) <= 128 * 1024 ? 2 : 1;
     constexpr int JOIN = 2 * KT::ND * 4096;
     __shared__ __attribute__((aligned(1024))) char lds[NBUF * (KB + VB) > JOIN ? NBUF * (KB + VB) : JOIN];
+    __shared__ float s_D[kWaves][32];
 
     const AttnArgs& a = b.f;
     const int lane = threadIdx.x & 63, half = lane >> 5;
@@ -315,30 +345,52 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_dq_split_kernel(AttnBwdArgs b
         D = half_sum(D);
         if (live) lse2 = a.lse[tok * a.Hq + h] * kLog2e;
     }
-    if (live && half == 0 && wave == 0) {
-        stats.lse2[static_cast<size_t>(h) * a.T_tot + tok] = lse2;
-        stats.D[static_cast<size_t>(h) * a.T_tot + tok] = D;
-    }
-
     f32x16_t dq[KT::ND];
 #pragma unroll
     for (int dt = 0; dt < KT::ND; ++dt) dq[dt] = f32x16_t{};
     const int groups = (row0 + TG) / TG;
+    auto put_stats = [&]() __attribute__((always_inline)) {
+        if (live && half == 0 && wave == 0) {
+            stats.lse2[static_cast<size_t>(h) * a.T_tot + tok] = lse2;
+            stats.D[static_cast<size_t>(h) * a.T_tot + tok] = D;
+        }
+    };
+    const bool few = BF16 && row0 < TG;  // one group of keys: D from the weights, which are all here
+    if (!few) put_stats();
     loads_done();
     for (int t = 0; t < groups; ++t) {
         lds_ready();
         if (NBUF == 2 && t + 1 < groups) stage_group(t + 1);
         const int key0 = t * TG + 32 * wave;
-        if (key0 <= row0) {
-            const char* kt = lds + (NBUF == 2 ? t & 1 : 0) * (KB + VB);
-            f32x16_t s = KT::rows_times(f32x16_t{}, kt, kat, 32 * wave, q);
-            const f32x16_t dp = VT::rows_times(f32x16_t{}, kt + KB, vat, 32 * wave, d_o);
+        const bool mine = key0 <= row0;
+        const char* kt = lds + (NBUF == 2 ? t & 1 : 0) * (KB + VB);
+        f32x16_t s = {}, dp = {};
+        if (mine) {
+            s = KT::rows_times(s, kt, kat, 32 * wave, q);
+            dp = VT::rows_times(dp, kt + KB, vat, 32 * wave, d_o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse2)) * (dp[i] - D);
+            for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse2));
             if (key0 == row0) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[i] = key0 + 8 * (i >> 2) + 4 * half + (i & 3) <= qi ? s[i] : 0.f;
             }
+        }
+        if (few) {  // the same for every wave
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum += s[i] != 0.f ? s[i] * dp[i] : 0.f;
+            sum = half_sum(sum);
+            if (half == 0) s_D[wave][lane] = sum;
+            __syncthreads();
+            D = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) D += s_D[w][lane & 31];
+            put_stats();
+        }
+        if (mine) {
+            // a weight of zero: what stands behind the mask may be anything
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = s[i] != 0.f ? s[i] * (dp[i] - D) : 0.f;
             ColOp<BF16> ds;
             ds.set(s);
 #pragma unroll
