@@ -315,14 +315,16 @@ __global__ __launch_bounds__(256) void kv_fork_copy_kernel(PageArgs a, CacheArgs
     const u32x4_t* x = base + p0 * page;
     u32x4_t* y = base + p1 * page;
     const int units = static_cast<int>(used * row);
+    // cached loads and stores: a parent's page is read by each of its children, and the copies are the
+    // next step's to read (128 children, 267 MB read and written: 43 us against 65 past the caches)
     constexpr int B = 8;
     for (int u0 = threadIdx.x; u0 < units; u0 += 256 * B) {
         u32x4_t w[B];
 #pragma unroll
-        for (int b = 0; b < B; ++b) w[b] = u0 + b * 256 < units ? __builtin_nontemporal_load(x + u0 + b * 256) : u32x4_t{};
+        for (int b = 0; b < B; ++b) w[b] = u0 + b * 256 < units ? x[u0 + b * 256] : u32x4_t{};
 #pragma unroll
         for (int b = 0; b < B; ++b)
-            if (u0 + b * 256 < units) __builtin_nontemporal_store(w[b], y + u0 + b * 256);
+            if (u0 + b * 256 < units) y[u0 + b * 256] = w[b];
     }
 }
 
@@ -358,7 +360,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(PageArgs a, CacheArgs c,
         for (int l0 = blockIdx.y * B; l0 < c.n_layers; l0 += gridDim.y * B) {
             u32x4_t z[B];
 #pragma unroll
-            for (int b = 0; b < B; ++b) z[b] = l0 + b < c.n_layers ? __builtin_nontemporal_load(x + static_cast<int64_t>(l0 + b) * T * r) : u32x4_t{};
+            for (int b = 0; b < B; ++b) z[b] = l0 + b < c.n_layers ? x[static_cast<int64_t>(l0 + b) * T * r] : u32x4_t{};
 #pragma unroll
             for (int b = 0; b < B; ++b)
                 if (l0 + b < c.n_layers) y[static_cast<int64_t>(l0 + b) * positions * r] = z[b];
