@@ -201,6 +201,13 @@ __global__ __launch_bounds__(kThreads) void kv_free_kernel(PageArgs a, const int
             if (page[b] >= a.n_pages) page[b] = -1;
         }
     };
+    // Every thread's changes to the counts are made.  They are atomics, made in the L2 that this
+    // workgroup's compute unit shares, and are read there (load_ref): to wait for them is enough, and
+    // a fence for the whole device, which writes that L2 back, is not needed.
+    auto counted = [&]() __attribute__((always_inline)) {
+        loads_done();
+        __syncthreads();
+    };
     auto counts = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) ref[b] = page[b] >= 0 ? load_ref(&a.refs[page[b]]) : 1;
@@ -212,8 +219,7 @@ __global__ __launch_bounds__(kThreads) void kv_free_kernel(PageArgs a, const int
         for (int b = 0; b < kBatch; ++b)
             if (page[b] >= 0) atomicSub(&a.refs[page[b]], 1);
     }
-    __threadfence();
-    __syncthreads();
+    counted();
     for (int e0 = 0; e0 < total; e0 += kRound) {
         if (total > kRound) entries(e0);
         counts();
@@ -221,8 +227,7 @@ __global__ __launch_bounds__(kThreads) void kv_free_kernel(PageArgs a, const int
         for (int b = 0; b < kBatch; ++b)
             if (ref[b] == 0 || ref[b] < -(kMark / 2)) atomicMin(&a.refs[page[b]], e0 + b * kThreads + i - kMark);
     }
-    __threadfence();
-    __syncthreads();
+    counted();
     int pushed = 0;
     for (int e0 = 0; e0 < total; e0 += kRound) {
         if (total > kRound) entries(e0);
