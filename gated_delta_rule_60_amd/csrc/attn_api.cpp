@@ -24,6 +24,9 @@ kda_status hip_fail(hipError_t e, const char* what) {
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+// A launch counts its work items along x in 32 bits.
+constexpr int64_t kMaxItems = int64_t{1} << 32;
+
 bool supported_dim(int32_t d) { return d == 32 || d == 64 || d == 128; }
 
 // Head counts, head sizes and type, common to every entry point.
@@ -73,8 +76,8 @@ kda_status check_prefill(const void* q, const void* k, const void* v, const int3
         if (!aligned(p, 16)) return fail(KDA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
     if (!aligned(lse, 4) || !aligned(cu_seqlens, 4))
         return fail(KDA_ERR_INVALID_ARG, "lse and cu_seqlens must be 4-byte aligned");
-    // workgroups of the launches: one per (piece of at least 64 rows, head)
-    if ((T_tot / 64 + 1 + N) * H_q > INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "(T_tot / 64 + N) * H_q too large");
+    // workgroups of the launches: one of 256 work items per (piece of 128 rows, head)
+    if ((T_tot / 128 + N) * H_q * 256 >= kMaxItems) return fail(KDA_ERR_INVALID_ARG, "(T_tot / 128 + N) * H_q too large");
     return KDA_OK;
 }
 
@@ -153,10 +156,11 @@ kda_status check_cache(int32_t n_pages, int32_t page_size, int32_t max_pages) {
     return KDA_OK;
 }
 
-// Query rows, and row tiles times key blocks, must stay countable in 32 bits.
+// Query rows, row tiles times key blocks, and the work items of workgroups of up to 512, must stay
+// countable in 32 bits.
 bool tree_countable(const kda::TreePlan& p, int64_t T_q, int32_t max_pages, int32_t page_size, int32_t H_q, int32_t H_kv) {
     const int64_t blocks = static_cast<int64_t>(max_pages) * page_size / 128 + 1;
-    return T_q * (H_q / H_kv) <= (int64_t{1} << 30) && p.tiles <= INT32_MAX / blocks && (p.items + p.tiles) * H_kv <= INT32_MAX;
+    return T_q * (H_q / H_kv) <= (int64_t{1} << 30) && p.tiles <= INT32_MAX / blocks && (p.items + p.tiles) * H_kv * 512 < kMaxItems;
 }
 
 }  // namespace
@@ -299,7 +303,7 @@ kda_status kv_append(const void* k, const void* v, void* k_cache, void* v_cache,
     const void* ptrs[] = {block_table, lens, cu_new};
     kda_status s = check_pages(ptrs, 3, N, n_pages, page_size, max_pages);
     if (s != KDA_OK) return s;
-    if (T_new < 0 || T_new > (int64_t{1} << 24)) return fail(KDA_ERR_INVALID_ARG, "T_new must lie in [0, 2^24]");
+    if (T_new < 0 || T_new * 256 >= kMaxItems) return fail(KDA_ERR_INVALID_ARG, "T_new must lie in [0, 2^24)");
     kda::CacheArgs c{};
     if ((s = check_layers(k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, c)) != KDA_OK) return s;
     if (T_new > 0 && (!k || !v)) return fail(KDA_ERR_INVALID_ARG, "k and v must not be NULL when T_new > 0");
@@ -319,6 +323,7 @@ kda_status kv_compact(void* k_cache, void* v_cache, const int32_t* block_table, 
     const void* ptrs[] = {block_table, lens, cu_accepted, new_lens, accepted};
     kda_status s = check_pages(ptrs, A_tot > 0 ? 5 : 4, N, n_pages, page_size, max_pages);
     if (s != KDA_OK) return s;
+    if (static_cast<int64_t>(N) * 256 >= kMaxItems) return fail(KDA_ERR_INVALID_ARG, "N must be less than 2^24");
     if (A_tot < 0 || A_tot > (int64_t{1} << 24)) return fail(KDA_ERR_INVALID_ARG, "A_tot must lie in [0, 2^24]");
     if (new_lens == lens) return fail(KDA_ERR_INVALID_ARG, "new_lens must not be lens: every layer's work reads it");
     kda::CacheArgs c{};

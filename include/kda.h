@@ -416,7 +416,7 @@ kda_status kda_prefill_noalloc(const void* q, const void* k, const void* v,
  *   cu_seqlens device [N + 1]             int32   sequence offsets, as for
  *              kda_prefill; cu[N] may be less than T_tot.  Offsets outside
  *              [0, T_tot] are clamped to it.
- *   N, T_tot   >= 1, in [0, 2^30]
+ *   N, T_tot   >= 1, in [0, 2^30], with (T_tot / 128 + N) * H_q < 2^24
  *   H_q, H_kv  H_q a multiple of H_kv, at most 4096
  *   d_k, d_v   each one of 32, 64, 128
  *   q_stride, k_stride, v_stride   elements from one token to the next (the
@@ -501,7 +501,9 @@ size_t attn_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int32_t H_
  *   cu_q       device [N + 1] int32, as cu_seqlens of attn_prefill
  *   ctx_lens   device [N] int32, clamped to [0, max_pages * page_size]
  *   tree_mask  device [T_q] uint64, or NULL
- *   T_q        in [0, 2^24]
+ *   T_q        in [0, 2^24]; the row tiles (16 to 128 tokens x grouped heads
+ *              each, at most one more a sequence) of all key heads and their
+ *              chunks must together number less than 2^23
  *   o, lse     as for attn_prefill ([T_q, H_q, d_v], [T_q, H_q] or NULL);
  *              rows at or past cu_q[N] are not written
  *   workspace  at least attn_tree_decode_workspace_size bytes (NULL if 0),
@@ -584,8 +586,9 @@ kda_status kv_fork(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* 
  * packed by sequence (cu_new [N + 1]); token j of sequence n (row n of the
  * table) goes to position lens[n] + j.  lens stays as it is: drafted tokens
  * lie behind it until they are accepted.  Tokens at or past cu_new[N], and
- * positions without a page, are passed over.  A page that several rows share
- * is written all the same: kv_fork gives every row a last page of its own.
+ * positions without a page, are passed over.  T_new < 2^24.  A page that
+ * several rows share is written all the same: kv_fork gives every row a last
+ * page of its own.
  */
 kda_status kv_append(const void* k, const void* v, void* k_cache, void* v_cache,
                      const int32_t* block_table, const int32_t* lens, const int32_t* cu_new,
@@ -600,7 +603,7 @@ kda_status kv_append(const void* k, const void* v, void* k_cache, void* v_cache,
  * accepted to lens[n] + i, in every layer, and new_lens[n] = lens[n] + their
  * number.  The list of a sequence ends early at an entry that does not rise
  * or has no page.  new_lens [N] must not be lens itself.  Sequences may not
- * share the pages of their drafted positions.
+ * share the pages of their drafted positions.  N < 2^24.
  */
 kda_status kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
                       const int32_t* lens, const int32_t* accepted, const int32_t* cu_accepted,

@@ -67,6 +67,7 @@ COMMON = [
     (dict(k=FAKE + 8), BAD, "16-byte aligned"),
     (dict(lse=FAKE + 2), BAD, "4-byte aligned"),
     (dict(T_tot=1 << 30, H_q=2048, q_stride=2048 * 64), BAD, "too large"),
+    (dict(T_tot=1 << 24, N=1 << 23), BAD, "too large"),  # 2^32 work items and more
 ]
 
 
@@ -143,6 +144,7 @@ CACHE = [
     (dict(workspace=FAKE + 128), BAD, "256-byte aligned"),
     (dict(T_q=1 << 24, max_pages=1 << 26), BAD, "too many drafted tokens"),
     (dict(T_q=1 << 24, H_q=256, q_stride=256 * 64), BAD, "too many drafted tokens"),
+    (dict(T_q=1 << 24, N=1 << 24), BAD, "too many drafted tokens"),
     (dict(scale=3e38), BAD, "scale"),
 ])
 def test_tree_refuses(kw, status, needle):
@@ -202,6 +204,8 @@ _SOME_LAYERS = [(dict(n_layers=0), BAD, "n_layers"), (dict(n_layers=65536), BAD,
     ("kv_fork", dict(dst=None), BAD, "must not be NULL"),
     ("kv_append", dict(T_new=-1), BAD, "T_new"),
     ("kv_append", dict(T_new=(1 << 24) + 1), BAD, "T_new"),
+    ("kv_append", dict(T_new=1 << 24), BAD, "T_new"),
+    ("kv_compact", dict(N=1 << 24), BAD, "2^24"),
     ("kv_append", dict(N=0), BAD, "n_rows"),
     ("kv_append", dict(k=None), BAD, "must not be NULL"),
     ("kv_append", dict(v=FAKE + 8), BAD, "16-byte aligned"),
