@@ -144,7 +144,8 @@ def _prompt_args(q, k, v, cu_seqlens):
     Hkv, dv = k.shape[1], v.shape[2]
     code = _dtype_code(q)
     if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
+        # made on the device: nothing is copied from the host, so the call can be captured
+        cu_seqlens = torch.arange(0, 2 * T, T, dtype=torch.int32, device=dev) if T else torch.zeros(2, dtype=torch.int32, device=dev)
     N = cu_seqlens.shape[0] - 1
     dt = q.dtype
     strides = (_tokens(q, "q", (T, Hq, dk), dt, dev), _tokens(k, "k", (T, Hkv, dk), dt, dev),

@@ -248,6 +248,21 @@ def test_another_stream_and_graph_replays(dtype):
             assert torch.equal(x, y), f"replay {n}"
 
 
+def test_a_captured_call_without_offsets():
+    q, k, v, _, cu = _make([150], 4, 2, 64, 32, "bf16", 9)
+    kda.attn_prefill_t(q, k, v)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = kda.attn_prefill_t(q, k, v)
+    for n in range(3):
+        v.mul_(1.0 + n / 4)
+        o.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = kda.attn_prefill_t(q, k, v, cu)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), f"replay {n}"
+
+
 @pytest.mark.parametrize("lens", [[40, 9], [300] * 60])
 def test_the_row_statistics_may_be_left_out(lens):
     q, k, v, _, cu = _make(lens, 4, 2, 64, 32, "bf16", 6)
