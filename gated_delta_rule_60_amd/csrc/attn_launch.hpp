@@ -80,7 +80,8 @@ struct TreePlan {
     int32_t rows, target;
     int64_t tiles, items, part_rows;
     size_t bytes;
-    bool split;
+    bool split;   // sequences may have several chunks
+    bool chunky;  // they have many
 };
 
 TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus);

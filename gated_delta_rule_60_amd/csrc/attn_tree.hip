@@ -7,7 +7,11 @@
 // every committed position and the drafted ones its mask names.
 //
 // The step reads every visible key and value once per key head and does
-// little with them (2 H_q / H_kv products a value), so it is bound by HBM.
+// little with them (2 H_q / H_kv products a value), so it is bound by HBM
+// (256 sequences of 300 to 4000 positions, 32/8 heads of 128, bf16: 0.35 ms,
+// 4.4 TB/s of keys and values); at 128 rows a pass by the softmax's vector
+// work (329 drafted tokens of 12 trees over up to 32k positions: 0.18 ms and
+// 0.02 ms to join, against 0.13 ms for the loads alone).
 // The query rows of a key head (drafted tokens x grouped heads) are the
 // columns of 16x16 MFMAs, 16 to 128 of them per pass over the keys.  The keys
 // of a sequence are cut into chunks of equal work over the whole batch, a
@@ -15,9 +19,8 @@
 // its waves take 32-key tiles in turn, each with its own running maximum, sum
 // and output and its own two tiles in LDS, which the loads fill directly: a
 // wave always has a tile in flight and never waits for another.  With more
-// rows, two or four waves share a tile, and all of them load it.  (One wave
-// with 64 rows spilled: 0.69 ms for 329 drafted tokens of 12 trees over up to
-// 32k positions, 32/8 heads of 128, against 0.29 ms with 32 rows a pass.)
+// rows, four waves share a tile, and all waves load it.  (One wave with 64
+// rows spilled: 0.69 ms for the 12 trees, against 0.29 ms with 32 a pass.)
 // The waves' results are joined in LDS, the chunks' by a second launch, in a
 // fixed order.
 #include <hip/hip_runtime.h>
@@ -88,16 +91,25 @@ __device__ __forceinline__ SeqWork seq_work(const TreeArgs& a, int n, int rows) 
     return s;
 }
 
-// Keys a chunk: the whole batch's (row tile, key block) pairs over a.chunks_target chunks.
+// Blocks a chunk: the whole batch's (row tile, key block) pairs over a.chunks_target chunks.  Every row
+// tile's last chunk is cut short, which makes more chunks than that; with few sequences the chunks are
+// made larger until their number fits, so that no compute unit is left with one more than the others.
 __device__ __forceinline__ int chunk_blocks(const TreeArgs& a, int lane, int rows) {
-    int sum = 0;
+    int sum = 0, tiles = 0, blocks = 0;
     for (int n0 = 0; n0 < a.N; n0 += 64) {
         const SeqWork s = seq_work(a, n0 + lane, rows);
         sum += s.tiles * s.blocks;
+        tiles = s.tiles;
+        blocks = s.blocks;
     }
     sum = wave_sum(sum);
-    const int per = (sum + a.chunks_target - 1) / a.chunks_target;
-    return per < 1 ? 1 : per;
+    int per = sum / a.chunks_target + (sum % a.chunks_target != 0);
+    per = per < 1 ? 1 : per;
+    if (a.N <= 64 && 2 * static_cast<int64_t>(wave_sum(tiles)) <= a.chunks_target) {
+        // ends: at twice the size they fit
+        while (wave_sum(tiles * ((blocks + per - 1) / per)) > a.chunks_target) per += (per + 7) / 8;
+    }
+    return per;
 }
 
 // Row tile `p` of the batch (by_chunk: chunk p, counting every row tile's chunks).
@@ -447,7 +459,6 @@ __global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW), (TreeSh
     __syncthreads();
     if (lane == 0) sp[wave] = poisoned;
     if constexpr (KW > 1) {
-#pragma unroll
         for (int w = KW / 2; w >= 1; w /= 2) {
             if (w < KW / 2) __syncthreads();
             if (kw >= w && kw < 2 * w) {
@@ -535,62 +546,108 @@ __global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW), (TreeSh
     }
 }
 
-// Joins the chunks of a row tile: o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c, in the chunks'
-// order; a few rows a workgroup.
-template <bool BF16, int DV>
+// Joins the chunks of a row tile: o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c, with a running
+// maximum.  CG groups of threads share a row's chunks, and their sums are joined in the groups' order.
+// The chunks are a chain of loads, eight of each group in flight, bound by its latency where they are
+// many: one sequence of 32k positions and one key head, 16 rows in 250 chunks, 80 us in all with one
+// group and 23 with eight; eight are taken where a row tile has 16 chunks and more.
+template <bool BF16, int DV, int CG>
 __global__ __launch_bounds__(256) void attn_tree_join_kernel(TreeArgs a, int R) {
     using T = Elem<BF16>;
-    constexpr int TPR = DV / 4;  // threads a row
+    constexpr int TPR = DV / 4;             // threads of a row's group
+    constexpr int ROWS = 256 / TPR / CG;    // rows a workgroup
+    __shared__ __attribute__((aligned(16))) float s_o[CG][ROWS][DV];
+    __shared__ float s_ml[CG][ROWS][2];
     const int g = blockIdx.x % a.Hkv;
     const int group = a.Hq / a.Hkv;
     TreeItem it;
     if (!find_item(a, blockIdx.x / a.Hkv, R, false, it) || it.chunks == 1) return;
     if (it.item + it.chunks > a.items) return;  // offsets that overlap: no such partial results
-    const int rr = blockIdx.y * (256 / TPR) + threadIdx.x / TPR;
+    const int x = threadIdx.x / TPR, row = x % ROWS, cg = x / ROWS;
+    const int rr = blockIdx.y * ROWS + row;
     const int r = it.rt * R + rr, t = r / group, h = g * group + r % group;
-    if (rr >= R || t >= it.lq) return;
+    const bool live = rr < R && t < it.lq;
+    if (CG == 1 && !live) return;
     const int d = 4 * (threadIdx.x % TPR);
     const size_t step = static_cast<size_t>(a.Hkv) * R;
-    const size_t row0 = (static_cast<size_t>(it.item) * a.Hkv + g) * R + rr;
-    // four chunks' loads at a time; past the last, the last again with weight zero
-    constexpr int B = 4;
-    float m = -INFINITY;
-    for (int c = 0; c < it.chunks; c += B) {
-        float m2[B];
-#pragma unroll
-        for (int b = 0; b < B; ++b) m2[b] = a.part_ml[2 * (row0 + (c + b < it.chunks ? c + b : it.chunks - 1) * step)];
-#pragma unroll
-        for (int b = 0; b < B; ++b) m = fmaxf(m, m2[b]);
-    }
-    float l = 0.f;
+    const size_t row0 = (static_cast<size_t>(it.item) * a.Hkv + g) * R + (live ? rr : 0);
+    float m = -INFINITY, l = 0.f;
     f32x4_t o = {};
-    for (int c = 0; c < it.chunks; c += B) {
+    // a group's next B chunks of those there are; past the last, the last again without weight
+    auto add = [&](int c, auto Bc) __attribute__((always_inline)) {
+        constexpr int B = Bc;
         float m2[B], l2[B];
         f32x4_t y[B];
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-            const size_t row = row0 + (c + b < it.chunks ? c + b : it.chunks - 1) * step;
-            m2[b] = a.part_ml[2 * row];
-            l2[b] = a.part_ml[2 * row + 1];
-            y[b] = *reinterpret_cast<const f32x4_t*>(a.part_o + row * DV + d);
+            const int cb = c + b * CG;
+            const size_t at = row0 + (cb < it.chunks ? cb : it.chunks - 1) * step;
+            m2[b] = a.part_ml[2 * at];
+            l2[b] = a.part_ml[2 * at + 1];
+            y[b] = *reinterpret_cast<const f32x4_t*>(a.part_o + at * DV + d);
         }
+        float m1 = m;
+#pragma unroll
+        for (int b = 0; b < B; ++b) m1 = fmaxf(m1, m2[b]);
+        const float w0 = m == m1 ? 1.f : exp2f(m - m1);
+        m = m1;
+        l *= w0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= w0;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-            if (c + b >= it.chunks) break;
+            if (c + b * CG >= it.chunks) break;
             const float w = m2[b] == m ? 1.f : exp2f(m2[b] - m);
             l = fmaf(l2[b], w, l);
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = fmaf(y[b][e], w, o[e]);
         }
+    };
+    int c = cg;
+    for (; c + 4 * CG < it.chunks; c += 8 * CG) add(c, std::integral_constant<int, 8>{});
+    if (c < it.chunks) add(c, std::integral_constant<int, 4>{});
+    if constexpr (CG > 1) {
+        *reinterpret_cast<f32x4_t*>(&s_o[cg][row][d]) = o;
+        if (d == 0) {
+            s_ml[cg][row][0] = m;
+            s_ml[cg][row][1] = l;
+        }
+        __syncthreads();
+        if (cg > 0 || !live) return;
+        // a group without a chunk left -infinity and zeros
+        float m1 = m;
+#pragma unroll
+        for (int k = 1; k < CG; ++k) m1 = fmaxf(m1, s_ml[k][row][0]);
+        const float w0 = m == m1 ? 1.f : exp2f(m - m1);
+        m = m1;
+        l *= w0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= w0;
+#pragma unroll
+        for (int k = 1; k < CG; ++k) {
+            const float m2 = s_ml[k][row][0], w = m2 == m ? 1.f : exp2f(m2 - m);
+            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&s_o[k][row][d]);
+            l = fmaf(s_ml[k][row][1], w, l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(y[e], w, o[e]);
+        }
     }
-    const size_t row = static_cast<size_t>(it.tok0 + t) * a.Hq + h;
+    const size_t out = static_cast<size_t>(it.tok0 + t) * a.Hq + h;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
     const float y[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
-    T::store4(static_cast<typename T::G*>(a.o) + row * DV + d, y);
-    if (a.lse && d == 0) a.lse[row] = (m + log2f(l)) * kLn2;
+    T::store4(static_cast<typename T::G*>(a.o) + out * DV + d, y);
+    if (a.lse && d == 0) a.lse[out] = (m + log2f(l)) * kLn2;
 }
 
 namespace {
+
+template <bool BF16, int DV, int CG>
+hipError_t launch_join(const TreeArgs& a, const TreePlan& p) {
+    constexpr int rows = 256 / (DV / 4) / CG;  // of a workgroup
+    hipLaunchKernelGGL((attn_tree_join_kernel<BF16, DV, CG>), dim3(static_cast<unsigned>(p.tiles * a.Hkv), (p.rows + rows - 1) / rows),
+                       dim3(256), 0, static_cast<hipStream_t>(a.stream), a, p.rows);
+    return hipGetLastError();
+}
 
 template <bool BF16, int DK, int DV, int NQ, int RW>
 hipError_t launch(const TreeArgs& a, const TreePlan& p) {
@@ -600,10 +657,7 @@ hipError_t launch(const TreeArgs& a, const TreePlan& p) {
                        st, a, a.scale * kLog2e);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.split) return e;
-    constexpr int rows = 256 / (DV / 4);  // of a workgroup of the join
-    hipLaunchKernelGGL((attn_tree_join_kernel<BF16, DV>), dim3(static_cast<unsigned>(p.tiles * a.Hkv), (Sh::R + rows - 1) / rows),
-                       dim3(256), 0, st, a, Sh::R);
-    return hipGetLastError();
+    return p.chunky ? launch_join<BF16, DV, 8>(a, p) : launch_join<BF16, DV, 1>(a, p);
 }
 
 template <bool BF16, int DK, int DV>
@@ -637,8 +691,17 @@ hipError_t launch_dk(const TreeArgs& a, const TreePlan& p) {
 }  // namespace
 
 // Query rows a pass: the smallest of 16, 32, 64 and 128 that holds an average
-// sequence's rows.  Chunks: four workgroups a compute unit, so that uneven
-// sequences end together; never more than the cache's blocks.
+// sequence's rows (64 sequences of 2000 positions, 32/8 heads of 128: 16 rows
+// 125 us, 137 in passes of 32; 32 rows 147 us, 167 in passes of 16; 64 rows
+// 161 us, 298 in passes of 16; 96 rows 211 us, 222 in passes of 64).
+//
+// Chunks: as many as compute units where the row tiles are few, so that each
+// has one (one sequence of 32k positions: 36 us, 45 with two a unit, 65 with
+// four: every chunk writes and joins its rows' sums).  Else two a unit, which
+// evens out ragged sequences (32 of up to 8000 positions: 116 us, 133 with
+// one, 129 with four; 329 tokens of 12 trees: 171 us, 203 and 185); four where
+// the sequences alone are four a unit and more, and only the longest are cut
+// (256 decode rows: 348 us, 352 with two).  Never more than the blocks.
 TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus) {
     TreePlan p;
     const int64_t rows = T_q * (Hq / Hkv);
@@ -647,9 +710,12 @@ TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v,
     p.tiles = rows / p.rows + N;
     if (p.tiles > rows) p.tiles = rows;
     const int64_t blocks = (room + kBlock - 1) / kBlock;
-    int64_t target = 4 * static_cast<int64_t>(cus) / Hkv;
+    const int64_t least = N > rows / p.rows ? N : rows / p.rows;  // row tiles
+    const int64_t rounds = 4 * least * Hkv <= cus ? 1 : least * Hkv < 4 * static_cast<int64_t>(cus) ? 2 : 4;
+    int64_t target = rounds * cus / Hkv;
     if (target < 1) target = 1;
     p.target = static_cast<int32_t>(target);
+    p.chunky = target >= 16 * least && blocks >= 16;
     p.split = blocks > 1 && T_q > 0;
     p.items = p.split ? p.tiles + p.target : p.tiles;
     if (p.items > p.tiles * blocks) p.items = p.tiles * (blocks > 0 ? blocks : 1);

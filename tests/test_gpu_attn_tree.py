@@ -124,6 +124,18 @@ def test_long_contexts_are_cut_and_joined(dtype, draft):
     Case([9000, 20, 4100], draft, 4, 1, 64, 32, 64, dtype, seed=3).check()
 
 
+# chunks: one a compute unit (made larger until they fit), two, four; joined by one group of threads
+# a row or by eight
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ctx,hq,hkv", [
+    ([3000], 4, 1), ([2600, 3100], 2, 1), ([5000], 8, 4), ([700 + 611 * n for n in range(7)], 8, 8),
+    ([90 + 377 * n % 1500 for n in range(24)], 8, 8), ([64 * n for n in range(17)], 64, 64),
+])
+@pytest.mark.parametrize("dv", [32, 64, 128])
+def test_chunks_of_few_and_many_sequences(dtype, ctx, hq, hkv, dv):
+    Case(ctx, [1 + n % 3 for n in range(len(ctx))], hq, hkv, 32, dv, 16, dtype, seed=dv).check()
+
+
 def test_many_sequences():
     rng = random.Random(1)
     ctx = [rng.randrange(0, 700) for _ in range(150)]
