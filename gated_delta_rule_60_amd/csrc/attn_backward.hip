@@ -9,7 +9,11 @@
 // keys of a block of query rows (dq, and D_i on the way), the other the
 // query rows of a block of keys (dk, dv).  Scores are formed in both, 7
 // products instead of 5, and in return every sum has one owner and one
-// order: no atomics, the same bits every time.
+// order: no atomics, the same bits every time.  Both are laid out as the
+// forward kernel, and bound by what feeds the matrix cores (16k tokens in 4
+// sequences, 32/8 heads of 128, bf16: dq 1.0 ms for 3 products, 56 % busy;
+// dk/dv 1.7 ms for 4, 43 % busy: two accumulators leave two waves a SIMD and
+// no registers for a second tile's scores, so reads from LDS are waited for).
 //
 // D_i = do_i . o_i takes o as stored.  In bf16 its rounding matters where a
 // row has few keys (o is then as large as v, and ds is too): the first 128
@@ -165,7 +169,7 @@ __global__ __launch_bounds__(256, BF16 || DK + DV <= 128 ? 2 : 1) void attn_bwd_
     constexpr int BN = 32;
     // The values' fragments of bf16 are read from LDS each time: with both accumulators and the
     // keys' fragments in registers they would leave one wave a SIMD (128 + 128 channels, 16k packed
-    // tokens: 2.35 ms, against 1.91 ms with two).
+    // tokens: 2.35 ms, against 1.91 ms with two, either before the loads were written out).
     constexpr bool V_LDS = BF16;
     constexpr int QB = BN * QT::ROWB, OB = BN * OT::ROWB;
     constexpr int SB = 256;  // bytes of one statistic of a tile: a wave-wide load brings 64 floats
@@ -291,7 +295,9 @@ __global__ __launch_bounds__(256, BF16 || DK + DV <= 128 ? 2 : 1) void attn_bwd_
 
 // The same two for batches that leave compute units idle: 32 rows (or keys) a
 // workgroup, its four waves on every fourth 32-key (or 32-row) tile, their
-// sums joined at the end.
+// sums joined at the end.  Bound by the chain of the longest sequence (513
+// tokens of 924 in 5 sequences, 8/2 fp32 heads of 64: dq 25 us, dk/dv 34 us;
+// an fp32 MFMA of this shape takes 64 cycles and carries 2 channels).
 template <bool BF16, int DK, int DV>
 __global__ __launch_bounds__(256, 1) void attn_bwd_dq_split_kernel(AttnBwdArgs b, float c, Stats stats) {
     using Op = AttnOp<BF16>;
@@ -608,7 +614,7 @@ hipError_t launch_dk(const AttnBwdArgs& b) {
 
 // Where even the split blocks of the key heads leave compute units idle, the query heads of a key
 // head go to several workgroups and their sums are joined (5 ragged fp32 sequences of 924 tokens,
-// 8/2 heads of 64: dk/dv 107 us in one part).
+// 8/2 heads of 64: dk/dv 107 us in one part, 34 us and 7 to join in four).
 BwdPlan attn_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t d_k, int32_t d_v, bool bf16, int cus) {
     BwdPlan p;
     p.stats_bytes = (static_cast<size_t>(T_tot) * Hq * 2 * sizeof(float) + 255) / 256 * 256;

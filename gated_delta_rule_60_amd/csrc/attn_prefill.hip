@@ -6,6 +6,17 @@
 // One pass over the keys: with m the running maximum, l = sum exp(s - m) and
 // O = sum exp(s - m) v_j, a new tile adds to l and O, and both are rescaled
 // only when m rises.
+//
+// Long prompts are bound by the matrix cores: 2 (d_k + d_v) products a (row,
+// key) pair against bytes that grow with the rows only.  A workgroup has 128
+// rows of one head, 32 a wave, so that K and V tiles are read from LDS once
+// for 32 rows; S^T = K Q^T gives a lane one query row, whose statistics need
+// no shuffles, and P^T is the next product's operand as it stands.  The two
+// products of a step depend on each other through the exponentials; the next
+// tile's scores are formed in between (32k tokens in 8 prompts, 32/8 heads of
+// 128, bf16: 1.45 ms, 1030 TFLOP/s; one prompt of 16k, 16 heads: 1.0 ms, 1100
+// TFLOP/s, the matrix cores busy 61 % of the time at the 1.63 GHz that they
+// leave the chip).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -186,7 +197,9 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a, float 
 
 // The same for batches that leave compute units idle: 32 query rows a
 // workgroup, its four waves on every fourth 32-key tile, joined at the end.
-// Four times the workgroups and a quarter of the steps one after another.
+// Four times the workgroups and a quarter of the steps one after another:
+// what bounds it is that chain (256 tokens, 2 fp32 heads of 32: 8 us, of which
+// two steps of 16 dependent fp32 MFMAs and the join).
 template <bool BF16, int DK, int DV>
 __global__ __launch_bounds__(256, 1) void attn_prefill_split_kernel(AttnArgs a, float c) {
     using Op = AttnOp<BF16>;
