@@ -91,12 +91,32 @@ __device__ __forceinline__ SeqWork seq_work(const TreeArgs& a, int n, int rows) 
     return s;
 }
 
+// The work of the first 64 SETS sequences, kept: their loads are in flight together (one decode row:
+// 12.8 us, 13.4 with one load after another).  Not in the kernel of 64 and 128 rows, whose loop got slower
+// by it (329 tokens of 12 trees: 171 us without, 180 with).
+template <int SETS>
+struct FirstWork {
+    SeqWork s[SETS + 1];
+};
+
+template <int SETS>
+__device__ __forceinline__ FirstWork<SETS> first_work(const TreeArgs& a, int lane, int rows) {
+    FirstWork<SETS> f = {};
+#pragma unroll
+    for (int b = 0; b < SETS; ++b) f.s[b] = 64 * b < a.N ? seq_work(a, 64 * b + lane, rows) : SeqWork{};
+    return f;
+}
+
 // Blocks a chunk: the whole batch's (row tile, key block) pairs over a.chunks_target chunks.  Every row
 // tile's last chunk is cut short, which makes more chunks than that; with few sequences the chunks are
 // made larger until their number fits, so that no compute unit is left with one more than the others.
-__device__ __forceinline__ int chunk_blocks(const TreeArgs& a, int lane, int rows) {
-    int sum = 0, tiles = 0, blocks = 0;
-    for (int n0 = 0; n0 < a.N; n0 += 64) {
+template <int SETS>
+__device__ __forceinline__ int chunk_blocks(const TreeArgs& a, const FirstWork<SETS>& f, int lane, int rows) {
+    int sum = 0;
+#pragma unroll
+    for (int b = 0; b < SETS; ++b) sum += f.s[b].tiles * f.s[b].blocks;
+    int tiles = f.s[0].tiles, blocks = f.s[0].blocks;  // of 64 sequences, if there are no more
+    for (int n0 = 64 * SETS; n0 < a.N; n0 += 64) {
         const SeqWork s = seq_work(a, n0 + lane, rows);
         sum += s.tiles * s.blocks;
         tiles = s.tiles;
@@ -113,12 +133,15 @@ __device__ __forceinline__ int chunk_blocks(const TreeArgs& a, int lane, int row
 }
 
 // Row tile `p` of the batch (by_chunk: chunk p, counting every row tile's chunks).
+template <int SETS>
 __device__ __forceinline__ bool find_item(const TreeArgs& a, int p, int rows, bool by_chunk, TreeItem& t) {
     const int lane = threadIdx.x & 63;
-    const int per = chunk_blocks(a, lane, rows);
+    const FirstWork<SETS> f = first_work<SETS>(a, lane, rows);
+    const int per = chunk_blocks<SETS>(a, f, lane, rows);
     int base = 0;  // chunks before
-    for (int n0 = 0; n0 < a.N; n0 += 64) {
-        const SeqWork s = seq_work(a, n0 + lane, rows);
+    // whether it is among these 64 sequences, and then whether it is sound
+    bool sound = false;
+    auto among = [&](const SeqWork& s, int n0) __attribute__((always_inline)) {
         const int chunks = s.blocks > per ? (s.blocks + per - 1) / per : 1;
         const int all = s.tiles * chunks, mine = by_chunk ? all : s.tiles;
         const int upto = wave_scan(mine), upto_chunks = wave_scan(all);
@@ -126,7 +149,7 @@ __device__ __forceinline__ bool find_item(const TreeArgs& a, int p, int rows, bo
         if (p < total) {
             const int l = __builtin_ctzll(__ballot(upto > p));
             const int r = p - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l));
-            if (r < 0) return false;  // offsets that overlap so far that the counts wrap
+            if (r < 0) return true;  // offsets that overlap so far that the counts wrap
             t.chunks = __builtin_amdgcn_readlane(chunks, l);
             t.n = n0 + l;
             t.tok0 = __builtin_amdgcn_readlane(s.tok0, l);
@@ -139,11 +162,18 @@ __device__ __forceinline__ bool find_item(const TreeArgs& a, int p, int rows, bo
             // even chunks, in blocks
             t.k0 = static_cast<int>(static_cast<int64_t>(blocks) * c / t.chunks) * kBlock;
             t.k1 = static_cast<int>(static_cast<int64_t>(blocks) * (c + 1) / t.chunks) * kBlock;
+            sound = true;
             return true;
         }
         p -= total;
         base += __builtin_amdgcn_readlane(upto_chunks, 63);
-    }
+        return false;
+    };
+#pragma unroll
+    for (int b = 0; b < SETS; ++b)
+        if (64 * b < a.N && among(f.s[b], 64 * b)) return sound;
+    for (int n0 = 64 * SETS; n0 < a.N; n0 += 64)
+        if (among(seq_work(a, n0 + lane, rows), n0)) return sound;
     return false;
 }
 
@@ -192,7 +222,7 @@ __global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW), (TreeSh
     const int g = blockIdx.x % a.Hkv;
     const int group = a.Hq / a.Hkv;
     TreeItem it;
-    if (!find_item(a, blockIdx.x / a.Hkv, R, true, it)) return;
+    if (!find_item<RW == 1 ? 4 : 0>(a, blockIdx.x / a.Hkv, R, true, it)) return;
     const int wrow = it.rt * R + rw * 16 * NQ;  // the wave's first row
     const bool working = wrow < it.lq * group;
 
@@ -561,7 +591,7 @@ __global__ __launch_bounds__(256) void attn_tree_join_kernel(TreeArgs a, int R) 
     const int g = blockIdx.x % a.Hkv;
     const int group = a.Hq / a.Hkv;
     TreeItem it;
-    if (!find_item(a, blockIdx.x / a.Hkv, R, false, it) || it.chunks == 1) return;
+    if (!find_item<4>(a, blockIdx.x / a.Hkv, R, false, it) || it.chunks == 1) return;
     if (it.item + it.chunks > a.items) return;  // offsets that overlap: no such partial results
     const int x = threadIdx.x / TPR, row = x % ROWS, cg = x / ROWS;
     const int rr = blockIdx.y * ROWS + row;
