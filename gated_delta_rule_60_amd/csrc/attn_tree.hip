@@ -8,10 +8,10 @@
 //
 // The step reads every visible key and value once per key head and does
 // little with them (2 H_q / H_kv products a value), so it is bound by HBM
-// (256 sequences of 300 to 4000 positions, 32/8 heads of 128, bf16: 0.35 ms,
-// 4.4 TB/s of keys and values); at 128 rows a pass by the softmax's vector
-// work (329 drafted tokens of 12 trees over up to 32k positions: 0.18 ms and
-// 0.02 ms to join, against 0.13 ms for the loads alone).
+// (256 sequences of 300 to 4000 positions, 32/8 heads of 128, bf16: 0.34 ms,
+// 4.7 TB/s of keys and values, and 0.01 ms to join); at 128 rows a pass by the
+// softmax's vector work (329 drafted tokens of 12 trees over up to 32k
+// positions: 0.17 ms and 0.01 ms to join, the matrix cores busy 10 %).
 // The query rows of a key head (drafted tokens x grouped heads) are the
 // columns of 16x16 MFMAs, 16 to 128 of them per pass over the keys.  The keys
 // of a sequence are cut into chunks of equal work over the whole batch, a
