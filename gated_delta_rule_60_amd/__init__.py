@@ -7,6 +7,10 @@ chunk-parallel prefill and an in-place decode step (and the scalar-gate
 Gated DeltaNet case of the same recurrence), in hand-written HIP
 kernels behind the C ABI of include/kda.h (libkda.so).
 
+The full-attention layers of a hybrid model have ``attn_prefill_t`` (and its
+backward pass), and ``attn_tree_decode_t`` over a paged cache whose pages the
+``kv_*_t`` functions keep.
+
 ``import gated_delta_rule_60_amd`` does not load the library; the first call
 does, and raises if it has not been built.
 """
