@@ -77,7 +77,8 @@ kda_status check_prefill(const void* q, const void* k, const void* v, const int3
     if (!aligned(lse, 4) || !aligned(cu_seqlens, 4))
         return fail(KDA_ERR_INVALID_ARG, "lse and cu_seqlens must be 4-byte aligned");
     // workgroups of the launches: one of 256 work items per (piece of 128 rows, head)
-    if ((T_tot / 128 + N) * H_q * 256 >= kMaxItems) return fail(KDA_ERR_INVALID_ARG, "(T_tot / 128 + N) * H_q too large");
+    if (((T_tot + 127) / 128 + N) * H_q * 256 >= kMaxItems)
+        return fail(KDA_ERR_INVALID_ARG, "(ceil(T_tot / 128) + N) * H_q too large");
     return KDA_OK;
 }
 

@@ -416,7 +416,7 @@ kda_status kda_prefill_noalloc(const void* q, const void* k, const void* v,
  *   cu_seqlens device [N + 1]             int32   sequence offsets, as for
  *              kda_prefill; cu[N] may be less than T_tot.  Offsets outside
  *              [0, T_tot] are clamped to it.
- *   N, T_tot   >= 1, in [0, 2^30], with (T_tot / 128 + N) * H_q < 2^24
+ *   N, T_tot   >= 1, in [0, 2^30], with (ceil(T_tot / 128) + N) * H_q < 2^24
  *   H_q, H_kv  H_q a multiple of H_kv, at most 4096
  *   d_k, d_v   each one of 32, 64, 128
  *   q_stride, k_stride, v_stride   elements from one token to the next (the

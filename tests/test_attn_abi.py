@@ -91,6 +91,22 @@ def test_backward_refuses(kw, status, needle):
     assert needle in kda.kda_last_error()
 
 
+@pytest.mark.parametrize("N,T_tot,H_q", [
+    (4095, 1, 4096),             # the one token makes a piece of its own: 4096 pieces of 4096 heads
+    (4095, 127, 4096),
+    (4094, 129, 4096),
+    (4096, 0, 4096),
+    (1, 128 * 32766 + 1, 512),   # 32767 pieces and one a sequence
+])
+def test_the_last_short_piece_of_rows_counts(N, T_tot, H_q):
+    """2^32 work items: one more than a launch can count, refused before it."""
+    kw = dict(N=N, T_tot=T_tot, H_q=H_q, H_kv=1, q_stride=H_q * 64)
+    assert ((T_tot + 127) // 128 + N) * H_q * 256 == 1 << 32
+    for call in (_prefill, _backward):
+        assert call(**kw) == BAD
+        assert "too large" in kda.kda_last_error()
+
+
 def test_backward_workspace():
     size = kda.attn_prefill_backward_workspace_size
     big = size(8, 32677, 32, 8, 128, 128, BF16)  # the batch fills the device: two floats a row and head
