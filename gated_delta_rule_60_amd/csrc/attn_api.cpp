@@ -24,6 +24,12 @@ kda_status hip_fail(hipError_t e, const char* what) {
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+// Whether int32 arrays of na and nb entries share memory.
+bool overlap(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + 4 * static_cast<uintptr_t>(nb) && y < x + 4 * static_cast<uintptr_t>(na);
+}
+
 // A launch counts its work items along x in 32 bits.
 constexpr int64_t kMaxItems = int64_t{1} << 32;
 
@@ -292,6 +298,8 @@ kda_status kv_fork(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* 
     if (s != KDA_OK || (s = check_requests(n)) != KDA_OK) return s;
     kda::CacheArgs c{};
     if ((s = check_layers(k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, c)) != KDA_OK) return s;
+    if (overlap(status, n, src, n) || overlap(status, n, dst, n))
+        return fail(KDA_ERR_INVALID_ARG, "status must not lie in src or dst: the copies read them after it is written");
     (void)hipGetLastError();
     const hipError_t e = kda::launch_kv_fork({block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size,
                                               __builtin_ctz(page_size), max_pages, stream}, c, src, dst, n, status);
@@ -326,9 +334,12 @@ kda_status kv_compact(void* k_cache, void* v_cache, const int32_t* block_table, 
     if (s != KDA_OK) return s;
     if (static_cast<int64_t>(N) * 256 >= kMaxItems) return fail(KDA_ERR_INVALID_ARG, "N must be less than 2^24");
     if (A_tot < 0 || A_tot > (int64_t{1} << 24)) return fail(KDA_ERR_INVALID_ARG, "A_tot must lie in [0, 2^24]");
-    if (new_lens == lens) return fail(KDA_ERR_INVALID_ARG, "new_lens must not be lens: every layer's work reads it");
     kda::CacheArgs c{};
     if ((s = check_layers(k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, c)) != KDA_OK) return s;
+    if (overlap(new_lens, N, lens, N)) return fail(KDA_ERR_INVALID_ARG, "new_lens must not be lens: every layer's work reads it");
+    if (overlap(new_lens, N, accepted, A_tot) || overlap(new_lens, N, cu_accepted, static_cast<int64_t>(N) + 1) ||
+        overlap(new_lens, N, block_table, static_cast<int64_t>(N) * max_pages))
+        return fail(KDA_ERR_INVALID_ARG, "new_lens must not lie in block_table, accepted or cu_accepted: every layer's work reads them");
     (void)hipGetLastError();
     const hipError_t e = kda::launch_kv_compact({const_cast<int32_t*>(block_table), const_cast<int32_t*>(lens), nullptr, nullptr, nullptr,
                                                  nullptr, N, n_pages, page_size, __builtin_ctz(page_size), max_pages, stream},

@@ -572,7 +572,8 @@ kda_status kv_free(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* 
  * page of its own with a copy of the positions of the last, partly filled one
  * (in every layer; the rest of that page stays as it was).  Also refused
  * (status 2): a dst that holds pages, a src that is the dst of any request of
- * the call, a src that holds fewer pages than its positions need.
+ * the call, a src that holds fewer pages than its positions need.  status
+ * must share no memory with src or dst.
  */
 kda_status kv_fork(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* refs,
                    int32_t* free_list, int32_t* n_free, int32_t n_rows, int32_t n_pages,
@@ -602,8 +603,9 @@ kda_status kv_append(const void* k, const void* v, void* k_cache, void* v_cache,
  * (counted within the sequence, rising) goes from position lens[n] +
  * accepted to lens[n] + i, in every layer, and new_lens[n] = lens[n] + their
  * number.  The list of a sequence ends early at an entry that does not rise
- * or has no page.  new_lens [N] must not be lens itself.  Sequences may not
- * share the pages of their drafted positions.  N < 2^24.
+ * or has no page.  new_lens [N] must share no memory with lens, accepted,
+ * cu_accepted or block_table: the work of every layer reads them.  Sequences
+ * may not share the pages of their drafted positions.  N < 2^24.
  */
 kda_status kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
                       const int32_t* lens, const int32_t* accepted, const int32_t* cu_accepted,

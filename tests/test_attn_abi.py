@@ -234,6 +234,23 @@ def test_page_calls_refuse(call, kw, status, needle):
     assert needle in kda.kda_last_error()
 
 
+@pytest.mark.parametrize("call,kw,needle", [
+    # N = 4: lens and new_lens are four numbers each; A_tot = 9; the table 4 x 32
+    ("kv_compact", dict(lens=FAKE, new_lens=FAKE + 4), "must not be lens"),
+    ("kv_compact", dict(lens=FAKE + 12, new_lens=FAKE), "must not be lens"),
+    ("kv_compact", dict(accepted=FAKE + 4096, new_lens=FAKE + 4096 + 32), "accepted"),
+    ("kv_compact", dict(cu_accepted=FAKE + 4096, new_lens=FAKE + 4096 + 16), "accepted"),
+    ("kv_compact", dict(block_table=FAKE + 4096, new_lens=FAKE + 4096 + 4 * 127), "accepted"),
+    ("kv_fork", dict(src=FAKE + 64, status=FAKE + 64), "status"),
+    ("kv_fork", dict(dst=FAKE + 64, status=FAKE + 76), "status"),
+    ("kv_fork", dict(dst=FAKE + 76, status=FAKE + 64), "status"),
+])
+def test_an_output_over_what_is_still_read_is_refused(call, kw, needle):
+    """Other workgroups, or the call's second launch, read these lists while the output is written."""
+    assert getattr(kda, call)(**dict(_CALLS[call], **kw)) == BAD
+    assert needle in kda.kda_last_error()
+
+
 def test_nothing_to_do_is_done():
     assert _prefill(T_tot=0, q=None, k=None, v=None, o=None, lse=None) == kda.KDA_OK
     assert kda.kda_last_error() == ""
