@@ -39,21 +39,20 @@ __device__ __forceinline__ float half_sum(float x) {
 // 16 (4) bytes a lane from a buffer range to LDS at `lds` (the wave's base) + 16 (4) lane.  Written
 // out, because the compiler waits for every load into LDS it knows of before each column read
 // (ds_read_b64_tr_b16), the next tile's among them.  The load has no output register; whoever
-// reads the tile waits for it with lds_ready().  m0 holds the LDS base, one wait state ahead; the
-// kernels that use these have no other use of it.
+// reads the tile waits for it with lds_ready().  m0 holds the LDS base, one wait state ahead.
 __device__ __forceinline__ unsigned lds_offset(const char* p) {
     return __builtin_amdgcn_readfirstlane(static_cast<unsigned>(reinterpret_cast<uintptr_t>((KDA_LDS const char*)p)));
 }
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, char* lds, int voff, int soff) {
 #if defined(__HIP_DEVICE_COMPILE__)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(lds_offset(lds)), "v"(voff), "s"(r), "s"(soff) : "memory");
+                 :: "s"(lds_offset(lds)), "v"(voff), "s"(r), "s"(soff) : "memory", "m0");
 #endif
 }
 __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, char* lds, int voff, int soff) {
 #if defined(__HIP_DEVICE_COMPILE__)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :: "s"(lds_offset(lds)), "v"(voff), "s"(r), "s"(soff) : "memory");
+                 :: "s"(lds_offset(lds)), "v"(voff), "s"(r), "s"(soff) : "memory", "m0");
 #endif
 }
 
