@@ -34,6 +34,9 @@ constexpr int kBM = 32 * kWaves;  // query rows of a workgroup
 // exceed it by more than this many powers of two: p then stays below 2^8,
 // where bf16 and fp32 hold it as exactly as below 1.
 constexpr float kLazyLog2 = 8.f;
+// Where it starts: below every score but -infinity, which a product past the range of fp32 gives and
+// which weighs nothing (2^(-inf - kLowest) = 0, where -inf - -inf would be NaN for the whole row).
+constexpr float kLowest = -3.402823466e38f;
 
 }  // namespace
 
@@ -90,7 +93,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a, float 
     f32x16_t o[VT::ND];
 #pragma unroll
     for (int dt = 0; dt < VT::ND; ++dt) o[dt] = f32x16_t{};
-    float mc = -INFINITY;  // running maximum of c s
+    float mc = kLowest;  // running maximum of c s
     float l = 0.f;         // this half-wave's part of the row's sum
 
     auto scores = [&](int t, f32x16_t (&s)[NS]) __attribute__((always_inline)) {
@@ -243,7 +246,7 @@ __global__ __launch_bounds__(256, 1) void attn_prefill_split_kernel(AttnArgs a, 
     f32x16_t o[VT::ND];
 #pragma unroll
     for (int dt = 0; dt < VT::ND; ++dt) o[dt] = f32x16_t{};
-    float mc = -INFINITY, l = 0.f;
+    float mc = kLowest, l = 0.f;
 
     const int groups = (row0 + TG) / TG;  // row0 is a multiple of 32: up to the diagonal
     stage_group(0);

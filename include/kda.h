@@ -432,9 +432,11 @@ kda_status kda_prefill_noalloc(const void* q, const void* k, const void* v,
  *              NULL if not wanted.  The backward pass needs it.
  * Rows of o and lse at or past cu[N] are not written.  A non-finite value in
  * a token's k or v reaches the rows of that token and the later ones of its
- * sequence only.  Batches too small to fill the device split their keys over
- * the waves of a workgroup, which changes rounding only: a sequence gives the
- * same bits in any batch on the same side of that rule.
+ * sequence only.  A score below the range of fp32 (-infinity) weighs nothing
+ * (a row with no other: o NaN, lse -infinity).  Batches too small to fill the
+ * device split their keys over the waves of a workgroup, which changes
+ * rounding only: a sequence gives the same bits in any batch on the same side
+ * of that rule.
  */
 kda_status attn_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
                         int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k,

@@ -308,6 +308,31 @@ def test_offsets_past_32_bits():
         attn_ref.check(got[32800:], want[name], name)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("full", [False, True])
+def test_scores_below_the_range_weigh_nothing(dtype, full):
+    """Finite queries and keys whose products pass -2^128, for every key of the first tiles: -infinity in
+    32 bits, and a weight of e^-10^39 = 0 by the formula.  The later rows are those of the later keys alone."""
+    gone, n = 100, 300
+    q, k, v, d_o, cu = _make([n] + [64] * (150 if full else 0), 2, 1, 64, 64, dtype, 23)
+    q[:n, :, 0], k[:gone, :, 0], k[gone:n, :, 0] = 1e20, -1e20, 0.0
+    o, lse = kda.attn_prefill_t(q, k, v, cu)
+    grads = kda.attn_prefill_backward_t(q, k, v, o, lse, d_o, cu)
+    torch.cuda.synchronize()
+    q, k, v, d_o = (x[:n].cpu().double() for x in (q, k, v, d_o))
+    seen = torch.tril(torch.ones(n, n, dtype=torch.bool))[gone:]
+    seen[:, :gone] = False
+    parts = []
+    for h in range(2):
+        r = attn_ref.attend(q[gone:, h], k[:, 0], v[:, 0], seen, 1 / 8, DT[dtype], d_o[gone:, h])
+        for name, got in (("o", o), ("lse", lse), ("d_q", grads[0])):
+            attn_ref.check(got[gone:n, h], r[name], f"{name} head {h}")
+        parts.append(r)
+    for name, got in (("d_k", grads[1]), ("d_v", grads[2])):
+        value, bound = (sum(r[name][i][gone:] for r in parts) for i in range(2))
+        attn_ref.check(got[gone:n, 0], (value, bound), name)
+
+
 def test_torch_helper_refusals():
     q, k, v, d_o, cu = _make([20], 4, 2, 32, 32, "f32", 1)
     with pytest.raises(ValueError, match="shape"):

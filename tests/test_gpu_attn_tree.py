@@ -329,6 +329,19 @@ def test_offsets_past_32_bits():
     assert torch.isfinite(o).all() and (o != 0).any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("draft", DRAFTS)
+def test_scores_below_the_range_weigh_nothing(dtype, draft):
+    """Finite queries and keys whose products pass -2^128 in 32 bits: a weight of zero."""
+    c = Case([300, 20, 133], draft, 4, 2, 64, 64, 16, dtype, seed=7)
+    c.q[:, :, 0] = 1e20
+    c.k[..., 0] = 0.0
+    for p in range(140):
+        pg, rw = c.rows[0][p]
+        c.k[pg, rw, :, 0] = -1e20
+    c.check(gone=[(0, p) for p in range(140)])
+
+
 def test_torch_helper_refusals():
     c = Case([20], [2], 4, 2, 32, 32, 16, "f32")
     with pytest.raises(ValueError, match="one token per sequence"):
