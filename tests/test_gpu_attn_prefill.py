@@ -248,6 +248,35 @@ def test_another_stream_and_graph_replays(dtype):
             assert torch.equal(x, y), f"replay {n}"
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_tokens(dtype):
+    q, k, v, d_o, _ = _make([0], 4, 2, 64, 32, dtype, 1)
+    for cu in (None, torch.zeros(4, dtype=torch.int32).cuda()):
+        o, lse = kda.attn_prefill_t(q, k, v, cu)
+        assert o.shape == (0, 4, 32) and lse.shape == (0, 4)
+        grads = kda.attn_prefill_backward_t(q, k, v, o, lse, d_o, cu)
+        assert [tuple(x.shape) for x in grads] == [(0, 4, 64), (0, 2, 64), (0, 2, 32)]
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("full", [False, True])
+def test_rows_before_the_first_sequence_stay(dtype, full):
+    lens = [40, 100] + [64] * (150 if full else 0)
+    q, k, v, d_o, _ = _make([50] + lens, 2, 1, 64, 64, dtype, 19)
+    cu = torch.tensor([50, *(50 + torch.tensor(lens).cumsum(0)).tolist()], dtype=torch.int32).cuda()
+    for x in (q, k, v, d_o):
+        x[:50] = float("nan")
+    o = torch.full((q.shape[0], 2, 64), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((q.shape[0], 2), 7.0, device="cuda")
+    kda.attn_prefill_t(q, k, v, cu, o=o, lse=lse)
+    assert (o[:50] == 7).all() and (lse[:50] == 7).all()
+    grads = kda.attn_prefill_backward_t(q, k, v, o, lse, d_o, cu)
+    want = attn_ref.prefill(q[50:], k[50:], v[50:], lens, 1 / 8, d_o[50:])
+    for name, got in zip(("o", "lse", "d_q", "d_k", "d_v"), (o, lse, *grads)):
+        attn_ref.check(got[50:], want[name], name)
+
+
 def test_a_captured_call_without_offsets():
     q, k, v, _, cu = _make([150], 4, 2, 64, 32, "bf16", 9)
     kda.attn_prefill_t(q, k, v)

@@ -330,6 +330,64 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("draft", [[2, 1], [9, 5], [40, 30]])
+def test_clamped_lengths_are_those_of_the_table(dtype, draft):
+    """A length past the table is all its positions, with no drafted one behind them; a negative one is
+    zero, and the drafted tokens lie at positions 0, 1, ..."""
+    d, page = draft[0], 16
+    c = Case([3 * page - d % page, 16], draft, 2, 1, 32, 64, page, dtype, tree=None)
+    room = c.table.shape[1] * page
+    assert len(c.rows[0]) == room  # every position of the table has a key
+    pg, rw = (torch.tensor(x) for x in zip(*c.rows[0]))
+    k, v = c.k.cpu()[pg, rw, 0].double(), c.v.cpu()[pg, rw, 0].double()
+    for given, clamped in ((10 ** 9, room), (2 ** 31 - 1, room), (room + 1, room), (-5, 0), (-2 ** 31, 0)):
+        c.lens[0] = given
+        o, lse = c.call()
+        c.lens[0] = clamped
+        o2, lse2 = c.call()
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2), given
+        seen = torch.arange(room)[None] < (room if clamped else torch.arange(1, d + 1)[:, None])
+        for h in range(2):
+            r = attn_ref.attend(c.q[:d, h].cpu().double(), k, v, seen.expand(d, room), 1 / math.sqrt(32), DT[dtype])
+            attn_ref.check(o[:d, h], r["o"], f"length {given}")
+            attn_ref.check(lse[:d, h], r["lse"], f"length {given} lse")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [257, 600])
+def test_more_than_256_sequences(dtype, n):
+    """The look-up keeps the work of 256 sequences; the rest, long ones that are cut and joined among
+    them, come 64 at a time."""
+    rng = random.Random(n)
+    ctx = [rng.randrange(0, 100) for _ in range(n)]
+    ctx[3], ctx[256], ctx[n - 1] = 3000, 5000, 2000
+    draft = [rng.choice([0, 1, 1, 2]) for _ in range(n)]
+    draft[3] = draft[256] = draft[n - 1] = 1
+    Case(ctx, draft, 4, 2, 32, 32, 16, dtype, seed=n).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("few,most", [(17, 31), (40, 64)])  # 64 and 128 rows a pass
+def test_more_than_64_sequences_of_wide_drafts(dtype, few, most):
+    rng = random.Random(most)
+    n = 150
+    ctx = [rng.randrange(0, 60) for _ in range(n)]
+    ctx[0], ctx[64], ctx[n - 1] = 1500, 4000, 2500
+    draft = [rng.randrange(few, most + 1) for _ in range(n)]
+    draft[7], draft[70], draft[130] = 0, 1, 0
+    Case(ctx, draft, 2, 1, 32, 32, 16, dtype, seed=most).check()
+
+
+def test_one_wide_tree_among_many_decode_rows():
+    """The rows of a pass come from the batch's average: the tree takes several passes."""
+    rng = random.Random(3)
+    ctx = [rng.randrange(0, 300) for _ in range(100)]
+    ctx[40] = 1900
+    Case(ctx, [64 if n == 40 else 1 for n in range(100)], 8, 2, 64, 64, 32, "bf16", seed=4).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("draft", DRAFTS)
 def test_scores_below_the_range_weigh_nothing(dtype, draft):
     """Finite queries and keys whose products pass -2^128 in 32 bits: a weight of zero."""

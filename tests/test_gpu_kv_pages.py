@@ -255,6 +255,18 @@ def test_append(dtype, layers):
     m.check()
 
 
+def test_append_to_more_than_64_sequences():
+    m = filled(13, rows=200, used=190, n_pages=1600, layers=2)
+    counts = [m.rng.choice([0, 0, 1, 2, 7]) for _ in range(200)]
+    counts[63] = counts[64] = counts[127] = counts[128] = 3
+    t = sum(counts)
+    k, v = (torch.randint(-99, 99, (2, t + 2, 1, d)).bfloat16() for d in (32, 64))
+    cu = i32([0] + torch.tensor(counts).cumsum(0).tolist())
+    kda.kv_append_t(k.cuda(), v.cuda(), m.dk, m.dv, m.pages.table, m.pages.lens, cu)  # two tokens behind the last
+    m.append(k, v, counts)
+    m.check()
+
+
 def test_append_one_layer_and_one_token_each():
     m = filled(9, layers=3)
     k, v = torch.randint(-9, 9, (12, 1, 32)).bfloat16(), torch.randint(-9, 9, (12, 1, 64)).bfloat16()
@@ -332,6 +344,30 @@ def test_many_requests_and_pages():
     kda.kv_free_t(m.pages, i32(rows[::-1]))
     m.release(rows[::-1])
     m.check(data=False)
+
+
+@pytest.mark.parametrize("keep", [0, 5])
+def test_free_of_shared_pages_in_several_rounds(keep):
+    """More entries than a round of the kernel takes (8192), the same pages in all of them, rows with
+    pages of their own in between; with some continuations kept their pages stay."""
+    m = Model(320, 40, 700, 1, layers=1, dk=32, dv=32, seed=3)
+    m.reserve([0, 1, 2], [40, 39, 40])
+    m.lens[:3] = [40, 39, 40]
+    dst = list(range(3, 303))
+    assert m.fork([i % 3 for i in range(300)], dst) == [0] * 300
+    own = list(range(303, 317))
+    assert m.reserve(own, [30] * 14) == [0] * 14
+    m.upload()
+    rows = dst[keep:] + [0, 1, 2]
+    m.rng.shuffle(rows)
+    for i, r in enumerate(own):
+        rows.insert(22 * i + 3, r)
+    rows += rows[:4]  # twice
+    assert sum(m.held[r] for r in set(rows)) > 8192 + 3000
+    kda.kv_free_t(m.pages, i32(rows))
+    m.release(rows)
+    m.check(data=False)
+    assert m.n == 700 - (119 if keep else 0)
 
 
 def test_nothing_asked():
