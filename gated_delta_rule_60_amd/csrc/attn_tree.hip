@@ -726,16 +726,20 @@ hipError_t launch_dk(const TreeArgs& a, const TreePlan& p) {
 
 // Query rows a pass: the smallest of 16, 32, 64 and 128 that holds an average
 // sequence's rows (64 sequences of 2000 positions, 32/8 heads of 128: 16 rows
-// 125 us, 137 in passes of 32; 32 rows 147 us, 167 in passes of 16; 64 rows
-// 161 us, 298 in passes of 16; 96 rows 211 us, 222 in passes of 64).
+// 107 us, 112 in passes of 32; 32 rows 116 us, 161 in passes of 16, 119 of 64;
+// 64 rows 128 us, 196 in passes of 32, 151 of 128; 96 rows 159 us, 219 in
+// passes of 64).  One width for the batch: a sequence with more rows than the
+// average walks its positions once a pass (255 decode rows at 2000 positions
+// 402 us; a tree of 64 tokens beside them at 2000 too: 430, at 32000: 638,
+// which alone takes 80).
 //
 // Chunks: as many as compute units where the row tiles are few, so that each
-// has one (one sequence of 32k positions: 36 us, 45 with two a unit, 65 with
+// has one (one sequence of 32k positions: 31 us, 37 with two a unit, 48 with
 // four: every chunk writes and joins its rows' sums).  Else two a unit, which
-// evens out ragged sequences (32 of up to 8000 positions: 116 us, 133 with
-// one, 129 with four; 329 tokens of 12 trees: 171 us, 203 and 185); four where
+// evens out ragged sequences (32 of up to 8000 positions: 121 us, 137 with
+// one, 132 with four; 329 tokens of 12 trees: 169 us, 202 and 186); four where
 // the sequences alone are four a unit and more, and only the longest are cut
-// (256 decode rows: 348 us, 352 with two).  Never more than the blocks.
+// (256 decode rows: 349 us, 359 with two).  Never more than the blocks.
 TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus) {
     TreePlan p;
     const int64_t rows = T_q * (Hq / Hkv);

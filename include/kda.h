@@ -423,7 +423,9 @@ kda_status kda_prefill_noalloc(const void* q, const void* k, const void* v,
  *              heads of a token are contiguous): at least H * d, a multiple
  *              of 16 bytes, at most 2^22.  Slices of one fused projection
  *              need no copy.
- *   scale      positive, with scale log2(e) finite
+ *   scale      positive, with scale log2(e) finite; s_ij log2(e) must stay
+ *              below 2^128, the end of fp32 (a row with a score above it is
+ *              not defined)
  *   dtype      storage type of q, k, v and o.  Sums and softmax statistics
  *              are fp32; for bf16 the weights exp(s - max) are rounded to
  *              bf16 before they meet v.
@@ -437,6 +439,9 @@ kda_status kda_prefill_noalloc(const void* q, const void* k, const void* v,
  * device split their keys over the waves of a workgroup, which changes
  * rounding only: a sequence gives the same bits in any batch on the same side
  * of that rule.
+ * Past 64 sequences every workgroup looks its rows up among all of them, 64 at
+ * a time: small up to a few hundred, most of the time at thousands of short
+ * ones.
  */
 kda_status attn_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
                         int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k,
@@ -510,6 +515,12 @@ size_t attn_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int32_t H_
  *              rows at or past cu_q[N] are not written
  *   workspace  at least attn_tree_decode_workspace_size bytes (NULL if 0),
  *              256-byte aligned, used until the queued work ends
+ * The rows of a pass are chosen for the batch's average number of drafted
+ * tokens: a sequence with many more than the others reads its positions once
+ * for every 16 to 128 of its rows, and is better in a call of its own.  Every
+ * workgroup looks its sequence up among all N, 64 at a time: up to a few
+ * hundred sequences that is small beside the work, at thousands it is most of
+ * it.
  * No size on the host depends on ctx_lens: a captured call can be replayed
  * while the sequences grow.  Non-finite keys and values that a row does not
  * see do not reach it.
