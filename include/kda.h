@@ -403,6 +403,8 @@ kda_status kda_prefill_noalloc(const void* q, const void* k, const void* v,
  * attention attend to every earlier token; like the rest of the library
  * these entry points apply no position encoding.  Query heads come in groups
  * that share a key/value head: query head h reads key head h / (H_q / H_kv).
+ * Outputs must share no memory with inputs (a second launch, or another
+ * workgroup, may still read them).
  *
  * attn_prefill -- causal attention over a packed batch of whole prompts.
  * For row i of a sequence and query head h with key head g:
