@@ -37,6 +37,13 @@ from ._attn import (  # noqa: F401
     kv_reserve,
     kv_reserve_t,
 )
+from ._bounded import (  # noqa: F401
+    attn_window_prefill,
+    attn_window_prefill_backward,
+    attn_window_prefill_backward_t,
+    attn_window_prefill_backward_workspace_size,
+    attn_window_prefill_t,
+)
 from ._lib import (  # noqa: F401
     KDA_DTYPE_BF16,
     KDA_DTYPE_F32,

@@ -150,6 +150,85 @@ kda_status attn_prefill_backward(const void* q, const void* k, const void* v, co
 
 namespace {
 
+// Window and sinks, common to the windowed entry points.
+kda_status check_window(int32_t window, int32_t sinks) {
+    if (window < 1 || window > (1 << 30)) return fail(KDA_ERR_INVALID_ARG, "window must lie in [1, 2^30]");
+    if (sinks < 0 || sinks > kda::kMaxSinks) return fail(KDA_ERR_INVALID_ARG, "sinks must lie in [0, 256]");
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status attn_window_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int32_t N, int64_t T_tot,
+                               int32_t H_q, int32_t H_kv, int32_t d_k, int32_t d_v, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, int32_t window, int32_t sinks, float scale, kda_dtype dtype, void* o, float* lse,
+                               void* stream) {
+    kda_status s = check_prefill(q, k, v, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_stride, k_stride, v_stride, scale, dtype, o, lse);
+    if (s != KDA_OK || (s = check_window(window, sinks)) != KDA_OK) return s;
+    if (T_tot == 0) return KDA_OK;
+    const kda::AttnArgs a{q, k, v, cu_seqlens, N, static_cast<int32_t>(T_tot), H_q, H_kv, d_k, d_v,
+                          static_cast<int32_t>(q_stride), static_cast<int32_t>(k_stride), static_cast<int32_t>(v_stride),
+                          scale, dtype == KDA_DTYPE_BF16, o, lse, stream,
+                          kda::attn_split(N, T_tot, H_q, dtype == KDA_DTYPE_BF16, kda::device_cus_or_default())};
+    (void)hipGetLastError();  // report only this launch's status
+    const hipError_t e = kda::launch_attn_window({a, window, sinks});
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "windowed attention kernel launch");
+}
+
+size_t attn_window_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k, int32_t d_v,
+                                                   int32_t window, int32_t sinks, kda_dtype dtype) {
+    if (N < 1 || T_tot < 0 || T_tot > (int64_t{1} << 30) || H_kv < 1 || H_q < 1 || H_q > 4096 || H_q % H_kv != 0 ||
+        !supported_dim(d_k) || !supported_dim(d_v) || (dtype != KDA_DTYPE_BF16 && dtype != KDA_DTYPE_F32) || window < 1 ||
+        window > (1 << 30) || sinks < 0 || sinks > kda::kMaxSinks)
+        return 0;
+    return kda::attn_window_bwd_plan(N, T_tot, H_q, H_kv, d_k, d_v, window, sinks, dtype == KDA_DTYPE_BF16,
+                                     kda::device_cus_or_default()).bytes;
+}
+
+kda_status attn_window_prefill_backward(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                        const void* d_o, const int32_t* cu_seqlens, int32_t N, int64_t T_tot, int32_t H_q,
+                                        int32_t H_kv, int32_t d_k, int32_t d_v, int64_t q_stride, int64_t k_stride,
+                                        int64_t v_stride, int32_t window, int32_t sinks, float scale, kda_dtype dtype, void* d_q,
+                                        void* d_k_out, void* d_v_out, void* workspace, size_t workspace_bytes, void* stream) {
+    kda_status s = check_prefill(q, k, v, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_stride, k_stride, v_stride, scale, dtype, o, lse);
+    if (s != KDA_OK || (s = check_window(window, sinks)) != KDA_OK) return s;
+    if (T_tot > 0 && (!lse || !d_o || !d_q || !d_k_out || !d_v_out))
+        return fail(KDA_ERR_INVALID_ARG, "lse, d_o, d_q, d_k and d_v must not be NULL when T_tot > 0");
+    for (const void* p : {d_o, static_cast<const void*>(d_q), static_cast<const void*>(d_k_out), static_cast<const void*>(d_v_out)})
+        if (!aligned(p, 16)) return fail(KDA_ERR_INVALID_ARG, "gradient pointers must be 16-byte aligned");
+    const int cus = kda::device_cus_or_default();
+    const kda::WindowBwdPlan plan =
+        kda::attn_window_bwd_plan(N, T_tot, H_q, H_kv, d_k, d_v, window, sinks, dtype == KDA_DTYPE_BF16, cus);
+    // the sinks' sums: one workgroup of 256 per (sequence, 32 sinks, key head)
+    if (static_cast<int64_t>(N) * plan.blocks * H_kv * 256 >= kMaxItems)
+        return fail(KDA_ERR_INVALID_ARG, "N * ceil(sinks / 32) * H_kv too large");
+    if (workspace_bytes < plan.bytes)
+        return fail(KDA_ERR_INVALID_ARG, "workspace smaller than attn_window_prefill_backward_workspace_size");
+    if (T_tot > 0 && !workspace) return fail(KDA_ERR_INVALID_ARG, "workspace must not be NULL");
+    if (!aligned(workspace, 256)) return fail(KDA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (T_tot == 0) return KDA_OK;
+    const kda::AttnArgs a{q, k, v, cu_seqlens, N, static_cast<int32_t>(T_tot), H_q, H_kv, d_k, d_v,
+                          static_cast<int32_t>(q_stride), static_cast<int32_t>(k_stride), static_cast<int32_t>(v_stride),
+                          scale, dtype == KDA_DTYPE_BF16, const_cast<void*>(o), const_cast<float*>(lse), stream,
+                          kda::attn_split(N, T_tot, H_q, dtype == KDA_DTYPE_BF16, cus)};
+    char* const at = static_cast<char*>(workspace) + plan.stats_bytes;
+    float* const sink_parts = reinterpret_cast<float*>(at);
+    float* const band_parts = reinterpret_cast<float*>(at + plan.parts_bytes);
+    float* const parts = reinterpret_cast<float*>(at + plan.parts_bytes + plan.band_bytes);
+    (void)hipGetLastError();  // report only this launch's status
+    const hipError_t e = kda::launch_attn_window_bwd({{a, d_o, d_q, d_k_out, d_v_out, workspace, parts, plan.head_parts},
+                                                      static_cast<int32_t>(window < T_tot ? window : T_tot), sinks, plan.rows,
+                                                      plan.blocks, static_cast<int32_t>(plan.pieces), sink_parts, band_parts},
+                                                     plan);
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "windowed attention backward kernel launch");
+}
+
+}  // extern "C"
+
+namespace {
+
 bool pow2(int32_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
 // The cache's shape, common to every entry point that reads or writes it.

@@ -98,7 +98,7 @@ __device__ __forceinline__ int wave_scan(int x) {
 // [beg, beg + len).
 // ---------------------------------------------------------------------------
 struct SeqTile {
-    int beg, len, tile;
+    int beg, len, tile, n;  // n: the sequence
 };
 
 __device__ __forceinline__ int2 seq_bounds(const int32_t* cu, int n, int T_tot) {
@@ -140,6 +140,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, int N, int T_tot, i
         s.beg = __builtin_amdgcn_readlane(bl.x, n);
         s.len = __builtin_amdgcn_readlane(bl.y, n);
         s.tile = from_end ? (s.len + BM - 1) / BM - 1 - lo : lo;
+        s.n = n;
         return true;
     }
     for (int n0 = 0; n0 < N; n0 += 64) {
@@ -153,6 +154,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, int N, int T_tot, i
             s.beg = __builtin_amdgcn_readlane(bl.x, n);
             s.len = __builtin_amdgcn_readlane(bl.y, n);
             s.tile = p - (__builtin_amdgcn_readlane(incl, n) - __builtin_amdgcn_readlane(nt, n));
+            s.n = n0 + n;
             return true;
         }
         p -= total;

@@ -49,6 +49,36 @@ struct BwdPlan {
 };
 BwdPlan attn_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t d_k, int32_t d_v, bool bf16, int cus);
 
+// The same with a sliding window and sinks: row i sees key j <= i if i - j < window or j < sinks.
+struct WindowArgs {
+    AttnArgs f;
+    int32_t window;  // in [1, 2^30]
+    int32_t sinks;   // in [0, kMaxSinks]
+};
+constexpr int32_t kMaxSinks = 256;
+
+// Its backward pass.  The rows past the window of the sinks' keys go to pieces of `rows` rows, each
+// with a sum of its own for those keys.
+struct WindowBwdArgs {
+    AttnBwdArgs b;
+    int32_t window;     // at most T_tot
+    int32_t sinks;
+    int32_t rows;
+    int32_t blocks;     // of 32 keys that hold the sinks; 0: no row is past their window
+    int32_t pieces;     // at most
+    float* sink_parts;  // [pieces][32 blocks][Hkv][d_k + d_v]
+    float* band_parts;  // [N][32 blocks][Hkv][d_k + d_v]: what the window gives those keys (whole blocks only)
+};
+
+struct WindowBwdPlan {
+    size_t stats_bytes, parts_bytes, band_bytes, bytes;
+    int32_t head_parts;  // as BwdPlan's
+    int32_t rows, blocks;
+    int64_t pieces;
+};
+WindowBwdPlan attn_window_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t d_k, int32_t d_v, int32_t window,
+                                   int32_t sinks, bool bf16, int cus);
+
 // Attention of drafted tokens over a paged cache.
 struct TreeArgs {
     const void* q;        // [T_q, Hq, d_k], q_stride elements between tokens
@@ -120,5 +150,7 @@ hipError_t launch_kv_compact(const PageArgs& a, const CacheArgs& c, const int32_
 
 hipError_t launch_attn_prefill(const AttnArgs& a);
 hipError_t launch_attn_bwd(const AttnBwdArgs& a);
+hipError_t launch_attn_window(const WindowArgs& a);
+hipError_t launch_attn_window_bwd(const WindowBwdArgs& a, const WindowBwdPlan& p);
 
 }  // namespace kda

@@ -1,0 +1,51 @@
+// attn_window.hpp -- which keys a row of windowed attention sees, by row, by
+// tile and by block of rows; shared by the forward and the backward kernels.
+#pragma once
+
+#include "attn_device.hpp"
+#include "attn_launch.hpp"
+
+namespace kda {
+
+__device__ __forceinline__ bool window_sees(const WindowArgs& w, int row, int key) {
+    return key <= row && (row - key < w.window || key < w.sinks);
+}
+
+// The tiles of BN keys that a block of rows [row0, end) walks: those of the
+// sinks that lie before the first row's window, then from that window to the
+// diagonal.
+template <int BN>
+struct WindowTiles {
+    int head;   // tiles of the sinks before the window's
+    int skip;   // tiles between them and the window's
+    int count;
+    __device__ __forceinline__ WindowTiles(const WindowArgs& w, int row0, int end) {
+        const int lo = row0 - w.window + 1;
+        const int first = lo > 0 ? lo / BN : 0;
+        const int sinks = (w.sinks + BN - 1) / BN;
+        head = sinks < first ? sinks : first;
+        skip = first - head;
+        count = (end + BN - 1) / BN - skip;
+    }
+    // tile number u of the list, and the number of a tile at or past the window's first
+    __device__ __forceinline__ int tile(int u) const { return u < head ? u : u + skip; }
+    __device__ __forceinline__ int number(int t) const { return t - skip; }
+};
+
+// Rows [row0, row0 + n) against tiles of BN keys at or before their diagonal.
+template <int BN>
+struct WindowRows {
+    int lo;     // the first row's first key in its window
+    int all_lo; // the last row's
+    int row0, sinks;
+    __device__ __forceinline__ WindowRows(const WindowArgs& w, int row0_, int n)
+        : lo(row0_ - w.window + 1), all_lo(row0_ + n - w.window), row0(row0_), sinks(w.sinks) {}
+    // some row may see some key of tile t (which begins at or before the last row)
+    __device__ __forceinline__ bool sees(int t) const { return (t + 1) * BN > lo || t * BN < sinks; }
+    // every row sees every key of it
+    __device__ __forceinline__ bool sees_all(int t) const {
+        return (t + 1) * BN - 1 <= row0 && (t * BN >= all_lo || (t + 1) * BN <= sinks);
+    }
+};
+
+}  // namespace kda

@@ -484,6 +484,47 @@ size_t attn_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int32_t H_
                                             int32_t d_k, int32_t d_v, kda_dtype dtype);
 
 /*
+ * attn_window_prefill -- attn_prefill with a sliding window and sinks: row i
+ * sees key j <= i if i - j < window (the last `window` positions, its own
+ * among them) or j < sinks (the first positions of its sequence).  Everything
+ * else is as for attn_prefill, lse too.
+ *
+ *   window     in [1, 2^30]; at or past a sequence's length: plain attention
+ *   sinks      in [0, 256]
+ * Keys and values that a row does not see do not reach it, non-finite ones
+ * neither.  The work grows with T_tot * (window + sinks).
+ */
+kda_status attn_window_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
+                               int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k,
+                               int32_t d_v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                               int32_t window, int32_t sinks, float scale, kda_dtype dtype, void* o,
+                               float* lse, void* stream);
+
+/*
+ * attn_window_prefill_backward -- its gradients with respect to q, k and v:
+ * attn_prefill_backward's formulas over the pairs that are seen, from the
+ * forward's o and lse of the same window and sinks.  Sums and roundings as
+ * there; N * ceil(sinks / 32) * H_kv < 2^24.
+ *   workspace  at least attn_window_prefill_backward_workspace_size bytes,
+ *   256-byte aligned, used until the queued work ends.
+ */
+kda_status attn_window_prefill_backward(const void* q, const void* k, const void* v, const void* o,
+                                        const float* lse, const void* d_o, const int32_t* cu_seqlens,
+                                        int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k,
+                                        int32_t d_v, int64_t q_stride, int64_t k_stride,
+                                        int64_t v_stride, int32_t window, int32_t sinks, float scale,
+                                        kda_dtype dtype, void* d_q, void* d_k_out, void* d_v_out,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_window_prefill_backward needs on the current device (0
+ * for unsupported sizes): two floats per row and query head, for small batches
+ * the parts of d_k and d_v that different query heads give, and what pieces of
+ * the rows past the window give the sinks. */
+size_t attn_window_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv,
+                                                   int32_t d_k, int32_t d_v, int32_t window,
+                                                   int32_t sinks, kda_dtype dtype);
+
+/*
  * A paged cache holds the keys and values of many sequences of growing
  * length in pages of page_size positions:
  *
