@@ -38,6 +38,12 @@ from ._attn import (  # noqa: F401
     kv_reserve_t,
 )
 from ._bounded import (  # noqa: F401
+    attn_weighed_decode,
+    attn_weighed_decode_t,
+    attn_weighed_decode_workspace_size,
+    attn_window_decode,
+    attn_window_decode_t,
+    attn_window_decode_workspace_size,
     attn_window_prefill,
     attn_window_prefill_backward,
     attn_window_prefill_backward_t,

@@ -1,14 +1,15 @@
 """Attention over a bounded part of the past (a sliding window and the first
 positions of a sequence), what keeps a cache bounded, and their gradients: the
-binding of the ``attn_window_*`` entry points of libkda.so (include/kda.h).
+binding of the ``attn_window_*`` and ``attn_weighed_*`` entry points of
+libkda.so (include/kda.h).
 
 As in ``_attn``: the functions named like the C symbols take raw device
 pointers and a stream handle; the ``*_t`` functions take torch tensors.
 """
 from __future__ import annotations
 
-from ._attn import _gpu, _need, _on_stream, _prompt_args, _scale, _workspace
-from ._lib import _check, load
+from ._attn import _cache_shape, _gpu, _need, _on_stream, _prompt_args, _scale, _tokens, _workspace
+from ._lib import _check, _dtype_code, load
 
 
 # ---------------------------------------------------------------------------
@@ -30,6 +31,27 @@ def attn_window_prefill_backward(q, k, v, o, lse, d_o, cu_seqlens, N, T_tot, H_q
 
 def attn_window_prefill_backward_workspace_size(N, T_tot, H_q, H_kv, d_k, d_v, window, sinks, dtype) -> int:
     return int(load().attn_window_prefill_backward_workspace_size(N, T_tot, H_q, H_kv, d_k, d_v, window, sinks, dtype))
+
+
+def attn_window_decode(q, k_cache, v_cache, block_table, ctx_lens, cu_q, N, T_q, H_q, H_kv, d_k, d_v, n_pages, page_size,
+                       max_pages, q_stride, window, sinks, scale, dtype, o, lse, workspace, workspace_bytes, stream) -> int:
+    return load().attn_window_decode(q, k_cache, v_cache, block_table, ctx_lens, cu_q, N, T_q, H_q, H_kv, d_k, d_v, n_pages,
+                                     page_size, max_pages, q_stride, window, sinks, scale, dtype, o, lse, workspace,
+                                     workspace_bytes, stream)
+
+
+def attn_window_decode_workspace_size(N, T_q, H_q, H_kv, d_v, page_size, max_pages, window, sinks) -> int:
+    return int(load().attn_window_decode_workspace_size(N, T_q, H_q, H_kv, d_v, page_size, max_pages, window, sinks))
+
+
+def attn_weighed_decode(q, k_cache, v_cache, block_table, ctx_lens, N, H_q, H_kv, d_k, d_v, n_pages, page_size, max_pages,
+                        q_stride, scale, dtype, o, lse, weights, workspace, workspace_bytes, stream) -> int:
+    return load().attn_weighed_decode(q, k_cache, v_cache, block_table, ctx_lens, N, H_q, H_kv, d_k, d_v, n_pages, page_size,
+                                      max_pages, q_stride, scale, dtype, o, lse, weights, workspace, workspace_bytes, stream)
+
+
+def attn_weighed_decode_workspace_size(N, H_q, H_kv, d_v, page_size, max_pages) -> int:
+    return int(load().attn_weighed_decode_workspace_size(N, H_q, H_kv, d_v, page_size, max_pages))
 
 
 # ---------------------------------------------------------------------------
@@ -87,3 +109,82 @@ def _window_backward_on(q, k, v, o, lse, d_o, cu_seqlens, window, sinks, scale, 
                                         sinks, _scale(scale, dk), code, d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(),
                                         ws.data_ptr(), ws.numel(), stream))
     return d_q, d_k, d_v
+
+
+def attn_window_decode_t(q, k_cache, v_cache, block_table, ctx_lens, cu_q=None, *, window, sinks=0, scale=None, o=None,
+                         lse=None, workspace=None, stream=None):
+    """Attention of new tokens with a sliding window and sinks over a paged
+    cache; returns (o, lse).
+
+    Token j of sequence n stands at position ctx_lens[n] + j and sees the last
+    ``window`` positions (itself among them) and the first ``sinks`` ones.
+    Tensors as for ``attn_tree_decode_t``.  ``workspace``: optional uint8
+    device tensor of ``attn_window_decode_workspace_size`` bytes."""
+    return _on_stream(stream, _gpu(q, "q"), _window_decode_on, q, k_cache, v_cache, block_table, ctx_lens, cu_q, window,
+                      sinks, scale, o, lse, workspace)
+
+
+def _decode_args(q, k_cache, v_cache, block_table, ctx_lens, o, lse):
+    """Checks of a step over a paged cache; returns (device, N, T, H_q, H_kv, d_k, d_v, pages, page size, pages a row,
+    stride of q, dtype code, o, lse)."""
+    import torch
+    dev = q.device
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [tokens, heads, size] and block_table [N, max_pages]")
+    T, Hq, dk = q.shape
+    code = _dtype_code(q)
+    P, ps, Hkv, dk_cache, dv = _cache_shape(k_cache, v_cache, q.dtype, dev)
+    if dk_cache != dk:
+        raise ValueError(f"k_cache holds keys of {dk_cache}, q has {dk}")
+    N, MP = ctx_lens.shape[0], block_table.shape[1]
+    qs = _tokens(q, "q", (T, Hq, dk), q.dtype, dev)
+    _need(block_table, "block_table", (N, MP), torch.int32, dev)
+    _need(ctx_lens, "ctx_lens", (N,), torch.int32, dev)
+    if o is None:
+        o = torch.empty((T, Hq, dv), dtype=q.dtype, device=dev)
+    else:
+        _need(o, "o", (T, Hq, dv), q.dtype, dev)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", (T, Hq), torch.float32, dev)
+    return dev, N, T, Hq, Hkv, dk, dv, P, ps, MP, qs, code, o, lse
+
+
+def _window_decode_on(q, k_cache, v_cache, block_table, ctx_lens, cu_q, window, sinks, scale, o, lse, workspace, stream):
+    import torch
+    dev, N, T, Hq, Hkv, dk, dv, P, ps, MP, qs, code, o, lse = _decode_args(q, k_cache, v_cache, block_table, ctx_lens, o, lse)
+    if cu_q is None:
+        if T != N:
+            raise ValueError(f"without cu_q there is one token per sequence: {T} tokens, {N} sequences")
+        cu_q = torch.arange(N + 1, dtype=torch.int32, device=dev)
+    _need(cu_q, "cu_q", (N + 1,), torch.int32, dev)
+    ws = _workspace(workspace, attn_window_decode_workspace_size(N, T, Hq, Hkv, dv, ps, MP, window, sinks), dev)
+    _check(attn_window_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                              ctx_lens.data_ptr(), cu_q.data_ptr(), N, T, Hq, Hkv, dk, dv, P, ps, MP, qs, window, sinks,
+                              _scale(scale, dk), code, o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), stream))
+    return o, lse
+
+
+def attn_weighed_decode_t(q, k_cache, v_cache, block_table, ctx_lens, weights, *, scale=None, o=None, lse=None,
+                          workspace=None, stream=None):
+    """One token per sequence over a paged cache, as ``attn_tree_decode_t``;
+    its attention weights, summed over the query heads of a key head, are added
+    to ``weights`` (fp32 [N, H_kv, max_pages * page_size]; a position's is at
+    its number).  Returns (o, lse).  ``workspace``: optional uint8 device
+    tensor of ``attn_weighed_decode_workspace_size`` bytes."""
+    return _on_stream(stream, _gpu(q, "q"), _weighed_decode_on, q, k_cache, v_cache, block_table, ctx_lens, weights, scale,
+                      o, lse, workspace)
+
+
+def _weighed_decode_on(q, k_cache, v_cache, block_table, ctx_lens, weights, scale, o, lse, workspace, stream):
+    import torch
+    dev, N, T, Hq, Hkv, dk, dv, P, ps, MP, qs, code, o, lse = _decode_args(q, k_cache, v_cache, block_table, ctx_lens, o, lse)
+    if T != N:
+        raise ValueError(f"there is one token per sequence: {T} tokens, {N} sequences")
+    _need(weights, "weights", (N, Hkv, MP * ps), torch.float32, dev)
+    ws = _workspace(workspace, attn_weighed_decode_workspace_size(N, Hq, Hkv, dv, ps, MP), dev)
+    _check(attn_weighed_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                               ctx_lens.data_ptr(), N, Hq, Hkv, dk, dv, P, ps, MP, qs, _scale(scale, dk), code,
+                               o.data_ptr(), lse.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel(), stream))
+    return o, lse

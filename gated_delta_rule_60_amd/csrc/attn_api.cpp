@@ -244,9 +244,72 @@ kda_status check_cache(int32_t n_pages, int32_t page_size, int32_t max_pages) {
 
 // Query rows, row tiles times key blocks, and the work items of workgroups of up to 512, must stay
 // countable in 32 bits.
-bool tree_countable(const kda::TreePlan& p, int64_t T_q, int32_t max_pages, int32_t page_size, int32_t H_q, int32_t H_kv) {
-    const int64_t blocks = static_cast<int64_t>(max_pages) * page_size / 128 + 1;
+bool tree_countable(const kda::TreePlan& p, int64_t T_q, int64_t room, int32_t H_q, int32_t H_kv) {
+    const int64_t blocks = room / 128 + 1;
     return T_q * (H_q / H_kv) <= (int64_t{1} << 30) && p.tiles <= INT32_MAX / blocks && (p.items + p.tiles) * H_kv * 512 < kMaxItems;
+}
+
+// Sizes that the workspace functions answer for.
+bool decode_sizes(int32_t N, int64_t T_q, int32_t H_q, int32_t H_kv, int32_t d_v, int32_t page_size, int32_t max_pages) {
+    return N >= 1 && T_q >= 0 && T_q <= (int64_t{1} << 24) && H_kv >= 1 && H_q >= 1 && H_q <= 4096 && H_q % H_kv == 0 &&
+           supported_dim(d_v) && pow2(page_size) && page_size <= 4096 && max_pages >= 1 &&
+           static_cast<int64_t>(max_pages) * page_size <= (int64_t{1} << 30);
+}
+
+// What the entry points over a paged cache have in common; sets page_shift.  `lists` is the last of the
+// required lists, `names` what to say of them.
+kda_status check_decode(kda::TreeArgs& a, int64_t T_q, int64_t q_stride, kda_dtype dtype, const char* names, const int32_t* lists) {
+    kda::set_last_error("");
+    if (a.N < 1 || T_q < 0 || T_q > (int64_t{1} << 24)) return fail(KDA_ERR_INVALID_ARG, "need N >= 1 and T_q in [0, 2^24]");
+    kda_status s = check_heads(a.Hq, a.Hkv, a.d_k, a.d_v, dtype);
+    if (s != KDA_OK) return s;
+    if ((s = check_cache(a.n_pages, a.page_size, a.max_pages)) != KDA_OK) return s;
+    if ((s = check_scale(a.scale)) != KDA_OK) return s;
+    if ((s = check_stride(q_stride, static_cast<int64_t>(a.Hq) * a.d_k, dtype, "q_stride")) != KDA_OK) return s;
+    if (!a.block_table || !a.ctx_lens || !lists) return fail(KDA_ERR_INVALID_ARG, names);
+    if (T_q > 0 && (!a.q || !a.k_cache || !a.v_cache || !a.o))
+        return fail(KDA_ERR_INVALID_ARG, "q, k_cache, v_cache and o must not be NULL when T_q > 0");
+    for (const void* p : {a.q, a.k_cache, a.v_cache, static_cast<const void*>(a.o)})
+        if (!aligned(p, 16)) return fail(KDA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+    if (!aligned(a.lse, 4) || !aligned(a.block_table, 4) || !aligned(a.ctx_lens, 4) || !aligned(lists, 4))
+        return fail(KDA_ERR_INVALID_ARG, "lse, block_table, ctx_lens and cu_q must be 4-byte aligned");
+    a.page_shift = __builtin_ctz(a.page_size);
+    return KDA_OK;
+}
+
+// The launch shape over at most `room` positions a row tile.
+kda_status check_tree_plan(const kda::TreeArgs& a, int64_t room, kda::TreePlan& plan) {
+    plan = kda::tree_plan(a.N, a.T_q, a.Hq, a.Hkv, a.d_v, room, kda::device_cus_or_default());
+    if (!tree_countable(plan, a.T_q, room, a.Hq, a.Hkv))
+        return fail(KDA_ERR_INVALID_ARG, "too many drafted tokens for sequences this long");
+    return KDA_OK;
+}
+
+kda_status check_tree_workspace(const kda::TreeArgs& a, size_t need, size_t have, const char* size) {
+    if (have < need) return fail(KDA_ERR_INVALID_ARG, std::string("workspace smaller than ") + size);
+    if (need > 0 && !a.workspace) return fail(KDA_ERR_INVALID_ARG, "workspace must not be NULL");
+    if (!aligned(a.workspace, 256)) return fail(KDA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    return KDA_OK;
+}
+
+// Positions a row tile of up to 128 tokens walks at most.
+int64_t window_room(int32_t page_size, int32_t max_pages, int32_t window, int32_t sinks) {
+    const int64_t room = static_cast<int64_t>(max_pages) * page_size, most = static_cast<int64_t>(window) + sinks + 128;
+    return room < most ? room : most;
+}
+
+// A weighed step's workspace: the partial results, the scores, and lse if the caller wants none.
+struct WeighedBytes {
+    size_t scores, lse, all;
+    int32_t pitch;
+};
+WeighedBytes weighed_bytes(int32_t N, int32_t H_q, int64_t room, const kda::TreePlan& plan) {
+    WeighedBytes w;
+    w.pitch = static_cast<int32_t>((room + 31) / 32 * 32);
+    w.scores = (plan.bytes + 255) / 256 * 256;
+    w.lse = w.scores + static_cast<size_t>(N) * H_q * w.pitch * sizeof(float);
+    w.all = w.lse + static_cast<size_t>(N) * H_q * sizeof(float);
+    return w;
 }
 
 }  // namespace
@@ -255,10 +318,7 @@ extern "C" {
 
 size_t attn_tree_decode_workspace_size(int32_t N, int64_t T_q, int32_t H_q, int32_t H_kv, int32_t d_v, int32_t page_size,
                                        int32_t max_pages) {
-    if (N < 1 || T_q < 0 || T_q > (int64_t{1} << 24) || H_kv < 1 || H_q < 1 || H_q > 4096 || H_q % H_kv != 0 ||
-        !supported_dim(d_v) || !pow2(page_size) || page_size > 4096 || max_pages < 1 ||
-        static_cast<int64_t>(max_pages) * page_size > (int64_t{1} << 30))
-        return 0;
+    if (!decode_sizes(N, T_q, H_q, H_kv, d_v, page_size, max_pages)) return 0;
     return kda::tree_plan(N, T_q, H_q, H_kv, d_v, static_cast<int64_t>(max_pages) * page_size, kda::device_cus_or_default()).bytes;
 }
 
@@ -267,35 +327,84 @@ kda_status attn_tree_decode(const void* q, const void* k_cache, const void* v_ca
                             int32_t H_q, int32_t H_kv, int32_t d_k, int32_t d_v, int32_t n_pages, int32_t page_size,
                             int32_t max_pages, int64_t q_stride, float scale, kda_dtype dtype, void* o, float* lse,
                             void* workspace, size_t workspace_bytes, void* stream) {
-    kda::set_last_error("");
-    if (N < 1 || T_q < 0 || T_q > (int64_t{1} << 24)) return fail(KDA_ERR_INVALID_ARG, "need N >= 1 and T_q in [0, 2^24]");
-    kda_status s = check_heads(H_q, H_kv, d_k, d_v, dtype);
-    if (s != KDA_OK) return s;
-    if ((s = check_cache(n_pages, page_size, max_pages)) != KDA_OK) return s;
-    if ((s = check_scale(scale)) != KDA_OK) return s;
-    if ((s = check_stride(q_stride, static_cast<int64_t>(H_q) * d_k, dtype, "q_stride")) != KDA_OK) return s;
-    if (!block_table || !ctx_lens || !cu_q) return fail(KDA_ERR_INVALID_ARG, "block_table, ctx_lens and cu_q must not be NULL");
-    if (T_q > 0 && (!q || !k_cache || !v_cache || !o))
-        return fail(KDA_ERR_INVALID_ARG, "q, k_cache, v_cache and o must not be NULL when T_q > 0");
-    for (const void* p : {q, k_cache, v_cache, static_cast<const void*>(o)})
-        if (!aligned(p, 16)) return fail(KDA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
-    if (!aligned(tree_mask, 8)) return fail(KDA_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
-    if (!aligned(lse, 4) || !aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(cu_q, 4))
-        return fail(KDA_ERR_INVALID_ARG, "lse, block_table, ctx_lens and cu_q must be 4-byte aligned");
-    const kda::TreePlan plan = kda::tree_plan(N, T_q, H_q, H_kv, d_v, static_cast<int64_t>(max_pages) * page_size,
-                                              kda::device_cus_or_default());
-    if (!tree_countable(plan, T_q, max_pages, page_size, H_q, H_kv))
-        return fail(KDA_ERR_INVALID_ARG, "too many drafted tokens for sequences this long");
-    if (workspace_bytes < plan.bytes) return fail(KDA_ERR_INVALID_ARG, "workspace smaller than attn_tree_decode_workspace_size");
-    if (plan.bytes > 0 && !workspace) return fail(KDA_ERR_INVALID_ARG, "workspace must not be NULL");
-    if (!aligned(workspace, 256)) return fail(KDA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-    if (T_q == 0) return KDA_OK;
     kda::TreeArgs a{q, k_cache, v_cache, block_table, ctx_lens, cu_q, reinterpret_cast<const unsigned long long*>(tree_mask),
-                    N, static_cast<int32_t>(T_q), H_q, H_kv, d_k, d_v, n_pages, page_size, __builtin_ctz(page_size), max_pages,
+                    N, static_cast<int32_t>(T_q), H_q, H_kv, d_k, d_v, n_pages, page_size, 0, max_pages,
                     static_cast<int32_t>(q_stride), scale, dtype == KDA_DTYPE_BF16, o, lse, workspace, stream};
+    kda_status s = check_decode(a, T_q, q_stride, dtype, "block_table, ctx_lens and cu_q must not be NULL", cu_q);
+    if (s != KDA_OK) return s;
+    if (!aligned(tree_mask, 8)) return fail(KDA_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
+    kda::TreePlan plan;
+    if ((s = check_tree_plan(a, static_cast<int64_t>(max_pages) * page_size, plan)) != KDA_OK) return s;
+    if ((s = check_tree_workspace(a, plan.bytes, workspace_bytes, "attn_tree_decode_workspace_size")) != KDA_OK) return s;
+    if (T_q == 0) return KDA_OK;
     (void)hipGetLastError();  // report only this launch's status
     const hipError_t e = kda::launch_attn_tree(a, plan);
     return e == hipSuccess ? KDA_OK : hip_fail(e, "tree attention kernel launch");
+}
+
+size_t attn_window_decode_workspace_size(int32_t N, int64_t T_q, int32_t H_q, int32_t H_kv, int32_t d_v, int32_t page_size,
+                                         int32_t max_pages, int32_t window, int32_t sinks) {
+    if (!decode_sizes(N, T_q, H_q, H_kv, d_v, page_size, max_pages) || window < 1 || window > (1 << 30) || sinks < 0 ||
+        sinks > kda::kMaxSinks)
+        return 0;
+    return kda::tree_plan(N, T_q, H_q, H_kv, d_v, window_room(page_size, max_pages, window, sinks), kda::device_cus_or_default()).bytes;
+}
+
+kda_status attn_window_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                              const int32_t* ctx_lens, const int32_t* cu_q, int32_t N, int64_t T_q, int32_t H_q, int32_t H_kv,
+                              int32_t d_k, int32_t d_v, int32_t n_pages, int32_t page_size, int32_t max_pages, int64_t q_stride,
+                              int32_t window, int32_t sinks, float scale, kda_dtype dtype, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    kda::TreeArgs a{q, k_cache, v_cache, block_table, ctx_lens, cu_q, nullptr,
+                    N, static_cast<int32_t>(T_q), H_q, H_kv, d_k, d_v, n_pages, page_size, 0, max_pages,
+                    static_cast<int32_t>(q_stride), scale, dtype == KDA_DTYPE_BF16, o, lse, workspace, stream};
+    a.window = window;
+    a.sinks = sinks;
+    kda_status s = check_decode(a, T_q, q_stride, dtype, "block_table, ctx_lens and cu_q must not be NULL", cu_q);
+    if (s != KDA_OK || (s = check_window(window, sinks)) != KDA_OK) return s;
+    kda::TreePlan plan;
+    if ((s = check_tree_plan(a, window_room(page_size, max_pages, window, sinks), plan)) != KDA_OK) return s;
+    if ((s = check_tree_workspace(a, plan.bytes, workspace_bytes, "attn_window_decode_workspace_size")) != KDA_OK) return s;
+    if (T_q == 0) return KDA_OK;
+    (void)hipGetLastError();  // report only this launch's status
+    const hipError_t e = kda::launch_attn_window_decode(a, plan);
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "windowed decode kernel launch");
+}
+
+size_t attn_weighed_decode_workspace_size(int32_t N, int32_t H_q, int32_t H_kv, int32_t d_v, int32_t page_size, int32_t max_pages) {
+    if (!decode_sizes(N, N, H_q, H_kv, d_v, page_size, max_pages)) return 0;
+    return weighed_bytes(N, H_q, static_cast<int64_t>(max_pages) * page_size,
+                         kda::tree_plan(N, N, H_q, H_kv, d_v, static_cast<int64_t>(max_pages) * page_size,
+                                        kda::device_cus_or_default())).all;
+}
+
+kda_status attn_weighed_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                               const int32_t* ctx_lens, int32_t N, int32_t H_q, int32_t H_kv, int32_t d_k, int32_t d_v,
+                               int32_t n_pages, int32_t page_size, int32_t max_pages, int64_t q_stride, float scale,
+                               kda_dtype dtype, void* o, float* lse, float* weights, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    kda::TreeArgs a{q, k_cache, v_cache, block_table, ctx_lens, nullptr, nullptr,
+                    N, N, H_q, H_kv, d_k, d_v, n_pages, page_size, 0, max_pages,
+                    static_cast<int32_t>(q_stride), scale, dtype == KDA_DTYPE_BF16, o, lse, workspace, stream};
+    kda_status s = check_decode(a, N, q_stride, dtype, "block_table and ctx_lens must not be NULL", ctx_lens);
+    if (s != KDA_OK) return s;
+    if (!weights || !aligned(weights, 4)) return fail(KDA_ERR_INVALID_ARG, "weights must not be NULL, and 4-byte aligned");
+    const int64_t room = static_cast<int64_t>(max_pages) * page_size;
+    kda::TreePlan plan;
+    if ((s = check_tree_plan(a, room, plan)) != KDA_OK) return s;
+    // the weights: workgroups of 256, at most 4096 turns of 1024 positions each
+    const int64_t turns = (room + 1023) / 1024 < 4096 ? (room + 1023) / 1024 : 4096;
+    if (static_cast<int64_t>(N) * H_kv * turns * 256 >= kMaxItems)
+        return fail(KDA_ERR_INVALID_ARG, "N * H_kv too large for sequences this long");
+    const WeighedBytes bytes = weighed_bytes(N, H_q, room, plan);
+    if ((s = check_tree_workspace(a, bytes.all, workspace_bytes, "attn_weighed_decode_workspace_size")) != KDA_OK) return s;
+    a.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + bytes.scores);
+    a.score_pitch = bytes.pitch;
+    a.weights = weights;
+    if (!a.lse) a.lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + bytes.lse);
+    (void)hipGetLastError();  // report only this launch's status
+    const hipError_t e = kda::launch_attn_weighed(a, plan);
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "weighed decode kernel launch");
 }
 
 }  // extern "C"

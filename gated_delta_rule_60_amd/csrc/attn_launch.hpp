@@ -102,6 +102,12 @@ struct TreeArgs {
     int32_t items = 0;
     float* part_o = nullptr;
     float* part_ml = nullptr;
+    // of a window
+    int32_t window = 0, sinks = 0;
+    // of a weighed step
+    float* scores = nullptr;    // [N, Hq, score_pitch]: q . k of every position
+    int32_t score_pitch = 0;    // at least the sequence's room, a multiple of 32
+    float* weights = nullptr;   // [N, Hkv, room], added to
 };
 
 // Launch shape: query rows a pass, row tiles and chunk items at most, and the
@@ -115,7 +121,9 @@ struct TreePlan {
 };
 
 TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus);
-hipError_t launch_attn_tree(TreeArgs a, const TreePlan& p);
+hipError_t launch_attn_tree(const TreeArgs& a, const TreePlan& p);
+hipError_t launch_attn_window_decode(const TreeArgs& a, const TreePlan& p);
+hipError_t launch_attn_weighed(const TreeArgs& a, const TreePlan& p);
 
 // The pages of a cache: block table rows and what is kept about them.  Calls
 // that only read the table and the lengths leave the rest null.

@@ -1,0 +1,61 @@
+// attn_weighed.hip -- a decode step over a paged cache that adds its attention
+// weights to what every position has drawn so far, gfx950.
+//
+// For the one token of sequence n, key head g and position j:
+//     w[n, g, j] += sum_{h of g} exp(s_hj - lse_h).
+// The pass over the keys is attn_tree.hip's.  A weight needs the row's lse,
+// which is known only when all chunks of the sequence are joined, so the pass
+// also leaves its scores (4 bytes a query head and position, beside the
+// 2 d 2 bytes of keys and values a key head that it reads in bf16), and a last
+// launch turns them into weights: one read of the scores, one of w and one
+// write, against a second pass over the keys.
+#include "attn_tree.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int kKeys = 1024;  // positions of a workgroup's turn
+
+}  // namespace
+
+__global__ __launch_bounds__(256) void attn_weigh_kernel(TreeArgs a, float c) {
+    const int g = blockIdx.x % a.Hkv, n = blockIdx.x / a.Hkv, group = a.Hq / a.Hkv;
+    const int room = a.max_pages * a.page_size;
+    int ctx = a.ctx_lens[n];
+    ctx = ctx < 0 ? 0 : (ctx > room ? room : ctx);
+    const int total = ctx < room ? ctx + 1 : room;
+    const float* lse = a.lse + static_cast<size_t>(n) * a.Hq + static_cast<size_t>(g) * group;
+    const float* s = a.scores + (static_cast<size_t>(n) * a.Hkv + g) * group * a.score_pitch;
+    float* w = a.weights + (static_cast<size_t>(n) * a.Hkv + g) * room;
+    for (int k0 = blockIdx.y * kKeys; k0 < total; k0 += gridDim.y * kKeys) {
+        float sum[kKeys / 256] = {};
+        for (int r = 0; r < group; ++r) {
+            const float l2 = lse[r] * kLog2e;
+            const float* row = s + static_cast<size_t>(r) * a.score_pitch;
+#pragma unroll
+            for (int i = 0; i < kKeys / 256; ++i) {
+                const int j = k0 + i * 256 + threadIdx.x;
+                const float x = j < total ? row[j] : -INFINITY;
+                // a position without a page is seen by no row, and lse is -infinity where there is none else
+                sum[i] += x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(fmaf(x, c, -l2));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kKeys / 256; ++i) {
+            const int j = k0 + i * 256 + threadIdx.x;
+            if (j < total) w[j] += sum[i];
+        }
+    }
+}
+
+hipError_t launch_attn_weighed(const TreeArgs& a, const TreePlan& p) {
+    const hipError_t e = launch_tree<TreeMode::kWeighed>(a, p);
+    if (e != hipSuccess) return e;
+    const int64_t turns = (static_cast<int64_t>(a.max_pages) * a.page_size + kKeys - 1) / kKeys;
+    hipLaunchKernelGGL(attn_weigh_kernel, dim3(static_cast<unsigned>(a.N) * a.Hkv, static_cast<unsigned>(turns < 4096 ? turns : 4096)),
+                       dim3(256), 0, static_cast<hipStream_t>(a.stream), a, a.scale * kLog2e);
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -582,6 +582,69 @@ size_t attn_tree_decode_workspace_size(int32_t N, int64_t T_q, int32_t H_q, int3
                                        int32_t d_v, int32_t page_size, int32_t max_pages);
 
 /*
+ * attn_window_decode -- attention of new tokens with a sliding window and
+ * sinks over such a cache.  Token j of sequence n stands at position
+ * ctx_lens[n] + j, where kv_append has put its key and value, and sees
+ * position x up to its own if it is among the last `window` (its own one of
+ * them) or x < sinks.  One token per sequence: the decode step of a layer of
+ * attn_window_prefill.  Arguments are attn_tree_decode's; window and sinks as
+ * for attn_window_prefill.  Only the positions of the windows and the sinks
+ * are read: pages that hold none of them may be missing.
+ *   workspace  at least attn_window_decode_workspace_size bytes (NULL if 0),
+ *              256-byte aligned, used until the queued work ends
+ * Captured calls, many sequences and uneven numbers of tokens: as for
+ * attn_tree_decode.  Non-finite keys and values that a row does not see do
+ * not reach it.
+ */
+kda_status attn_window_decode(const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_table, const int32_t* ctx_lens,
+                              const int32_t* cu_q, int32_t N, int64_t T_q, int32_t H_q, int32_t H_kv,
+                              int32_t d_k, int32_t d_v, int32_t n_pages, int32_t page_size,
+                              int32_t max_pages, int64_t q_stride, int32_t window, int32_t sinks,
+                              float scale, kda_dtype dtype, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_window_decode needs on the current device (0 for
+ * unsupported sizes): as for attn_tree_decode, for sequences of the window,
+ * the sinks and 128 positions at most. */
+size_t attn_window_decode_workspace_size(int32_t N, int64_t T_q, int32_t H_q, int32_t H_kv, int32_t d_v,
+                                         int32_t page_size, int32_t max_pages, int32_t window,
+                                         int32_t sinks);
+
+/*
+ * attn_weighed_decode -- the plain decode step (one token per sequence,
+ * attn_tree_decode without a mask) that also adds up how much attention each
+ * position draws:
+ *
+ *     weights[n, g, x] += sum_h exp(s_hx - lse_h)   (query heads h of key head
+ *                          g; x up to the token's own position, ctx_lens[n])
+ *
+ *   q          device [N, H_q, d_k] dtype, q_stride elements between tokens
+ *   weights    device [N, H_kv, max_pages * page_size] float32, read and
+ *              written up to the token's own position (later ones stay); zero
+ *              for positions that have not been weighed yet.  The weight of a
+ *              position without a page is zero.
+ *   lse        may be NULL
+ *   workspace  at least attn_weighed_decode_workspace_size bytes, 256-byte
+ *              aligned, used until the queued work ends
+ * Everything else as for attn_tree_decode with cu_q = 0, 1, ..., N.  The
+ * result is the same bits every time.  attn_prefill_weights starts a prompt's
+ * weights, kv_evict uses them.
+ */
+kda_status attn_weighed_decode(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, const int32_t* ctx_lens, int32_t N,
+                               int32_t H_q, int32_t H_kv, int32_t d_k, int32_t d_v, int32_t n_pages,
+                               int32_t page_size, int32_t max_pages, int64_t q_stride, float scale,
+                               kda_dtype dtype, void* o, float* lse, float* weights, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attn_weighed_decode needs on the current device (0 for
+ * unsupported sizes): those of attn_tree_decode, a float for every query head
+ * and position that a sequence has room for, and one for every query head. */
+size_t attn_weighed_decode_workspace_size(int32_t N, int32_t H_q, int32_t H_kv, int32_t d_v,
+                                          int32_t page_size, int32_t max_pages);
+
+/*
  * The pages of such a cache are kept in six int32 arrays on the device, owned
  * by the caller and shared by every layer:
  *

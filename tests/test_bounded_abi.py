@@ -3,7 +3,7 @@ before any HIP call (no kernel is launched here)."""
 import pytest
 
 import gated_delta_rule_60_amd as kda
-from test_attn_abi import BAD, BF16, COMMON, F32, FAKE
+from test_attn_abi import BAD, BF16, COMMON, F32, FAKE, NOT
 
 
 def _prefill(**kw):
@@ -62,3 +62,81 @@ def test_window_backward_workspace():
                (1, 10, 1, 1, 48, 64, 5, 1, BF16), (1, 10, 1, 1, 64, 64, 0, 1, BF16), (1, 10, 1, 1, 64, 64, 5, 300, BF16),
                (1, 10, 1, 1, 64, 64, 5, 1, 7)):
         assert size(*kw) == 0
+
+
+def _window_decode(**kw):
+    a = dict(q=FAKE, k_cache=FAKE, v_cache=FAKE, block_table=FAKE, ctx_lens=FAKE, cu_q=FAKE, N=2, T_q=3, H_q=4, H_kv=2, d_k=64,
+             d_v=32, n_pages=100, page_size=16, max_pages=50, q_stride=256, window=64, sinks=4, scale=0.125, dtype=BF16, o=FAKE,
+             lse=FAKE, workspace=FAKE, workspace_bytes=1 << 40, stream=None)
+    a.update(kw)
+    return kda.attn_window_decode(**a)
+
+
+def _weighed(**kw):
+    a = dict(q=FAKE, k_cache=FAKE, v_cache=FAKE, block_table=FAKE, ctx_lens=FAKE, N=2, H_q=4, H_kv=2, d_k=64, d_v=32, n_pages=100,
+             page_size=16, max_pages=50, q_stride=256, scale=0.125, dtype=BF16, o=FAKE, lse=FAKE, weights=FAKE, workspace=FAKE,
+             workspace_bytes=1 << 40, stream=None)
+    a.update(kw)
+    return kda.attn_weighed_decode(**a)
+
+
+DECODE = [
+    (dict(N=0), BAD, "N >= 1"),
+    (dict(H_q=3), BAD, "multiple of H_kv"),
+    (dict(d_k=48), NOT, "d_k and d_v"),
+    (dict(dtype=2), NOT, "dtype"),
+    (dict(page_size=24), BAD, "page_size"),
+    (dict(page_size=8192), BAD, "page_size"),
+    (dict(n_pages=0), BAD, "n_pages"),
+    (dict(n_pages=1 << 28), BAD, "2^31"),
+    (dict(max_pages=0), BAD, "max_pages"),
+    (dict(max_pages=1 << 27), BAD, "2^30"),
+    (dict(q_stride=248), BAD, "q_stride"),
+    (dict(scale=0.0), BAD, "scale"),
+    (dict(q=None), BAD, "must not be NULL"),
+    (dict(v_cache=None), BAD, "must not be NULL"),
+    (dict(o=None), BAD, "must not be NULL"),
+    (dict(block_table=None), BAD, "must not be NULL"),
+    (dict(ctx_lens=None), BAD, "must not be NULL"),
+    (dict(k_cache=FAKE + 8), BAD, "16-byte aligned"),
+    (dict(ctx_lens=FAKE + 2), BAD, "4-byte aligned"),
+    (dict(workspace=None), BAD, "workspace must not be NULL"),
+    (dict(workspace=FAKE + 16), BAD, "256-byte aligned"),
+    (dict(workspace_bytes=64), BAD, "workspace smaller"),
+]
+
+
+@pytest.mark.parametrize("kw,status,needle", DECODE + WINDOW + [
+    (dict(T_q=-1), BAD, "T_q"),
+    (dict(T_q=(1 << 24) + 1), BAD, "T_q"),
+    (dict(cu_q=None), BAD, "cu_q"),
+    (dict(cu_q=FAKE + 2), BAD, "4-byte aligned"),
+])
+def test_window_decode_refuses(kw, status, needle):
+    assert _window_decode(**kw) == status
+    assert needle in kda.kda_last_error()
+
+
+@pytest.mark.parametrize("kw,status,needle", DECODE + [
+    (dict(weights=None), BAD, "weights"),
+    (dict(weights=FAKE + 2), BAD, "weights"),
+    (dict(N=(1 << 24) + 1), BAD, "2^24"),
+    (dict(N=1 << 20, page_size=4096, max_pages=1 << 10), BAD, "for sequences this long"),
+])
+def test_weighed_decode_refuses(kw, status, needle):
+    assert _weighed(**kw) == status
+    assert needle in kda.kda_last_error()
+
+
+def test_decode_workspaces():
+    size = kda.attn_window_decode_workspace_size
+    assert 0 < size(1, 1, 32, 8, 128, 16, 8192, 1000, 4) <= kda.attn_tree_decode_workspace_size(1, 1, 32, 8, 128, 16, 8192)
+    assert size(1, 1, 32, 8, 128, 16, 8192, 1 << 30, 4) == kda.attn_tree_decode_workspace_size(1, 1, 32, 8, 128, 16, 8192)
+    weighed = kda.attn_weighed_decode_workspace_size(3, 8, 2, 64, 16, 10)
+    assert weighed >= kda.attn_tree_decode_workspace_size(3, 3, 8, 2, 64, 16, 10) + 3 * 8 * (160 + 1) * 4
+    for kw in ((0, 1, 1, 1, 64, 16, 10, 5, 1), (1, -1, 1, 1, 64, 16, 10, 5, 1), (1, 1, 3, 2, 64, 16, 10, 5, 1),
+               (1, 1, 1, 1, 48, 16, 10, 5, 1), (1, 1, 1, 1, 64, 15, 10, 5, 1), (1, 1, 1, 1, 64, 16, 0, 5, 1),
+               (1, 1, 1, 1, 64, 16, 10, 0, 1), (1, 1, 1, 1, 64, 16, 10, 5, 257)):
+        assert size(*kw) == 0
+    for kw in ((0, 1, 1, 64, 16, 10), (1, 3, 2, 64, 16, 10), (1, 1, 1, 48, 16, 10), (1, 1, 1, 64, 15, 10), (1, 1, 1, 64, 16, 0)):
+        assert kda.attn_weighed_decode_workspace_size(*kw) == 0
