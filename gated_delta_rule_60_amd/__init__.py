@@ -38,6 +38,8 @@ from ._attn import (  # noqa: F401
     kv_reserve_t,
 )
 from ._bounded import (  # noqa: F401
+    attn_prefill_weights,
+    attn_prefill_weights_t,
     attn_weighed_decode,
     attn_weighed_decode_t,
     attn_weighed_decode_workspace_size,
@@ -49,6 +51,8 @@ from ._bounded import (  # noqa: F401
     attn_window_prefill_backward_t,
     attn_window_prefill_backward_workspace_size,
     attn_window_prefill_t,
+    kv_evict,
+    kv_evict_t,
 )
 from ._lib import (  # noqa: F401
     KDA_DTYPE_BF16,

@@ -1,14 +1,16 @@
 """Attention over a bounded part of the past (a sliding window and the first
 positions of a sequence), what keeps a cache bounded, and their gradients: the
-binding of the ``attn_window_*`` and ``attn_weighed_*`` entry points of
-libkda.so (include/kda.h).
+binding of the ``attn_window_*`` entry points of libkda.so, of
+``attn_prefill_weights``, ``attn_weighed_decode`` and ``kv_evict``
+(include/kda.h).
 
 As in ``_attn``: the functions named like the C symbols take raw device
 pointers and a stream handle; the ``*_t`` functions take torch tensors.
 """
 from __future__ import annotations
 
-from ._attn import _cache_shape, _gpu, _need, _on_stream, _prompt_args, _scale, _tokens, _workspace
+from ._attn import (KVPages, _cache_shape, _gpu, _layers, _need, _on_stream, _pages_args, _prompt_args, _requests,
+                    _scale, _tokens, _workspace)
 from ._lib import _check, _dtype_code, load
 
 
@@ -52,6 +54,18 @@ def attn_weighed_decode(q, k_cache, v_cache, block_table, ctx_lens, N, H_q, H_kv
 
 def attn_weighed_decode_workspace_size(N, H_q, H_kv, d_v, page_size, max_pages) -> int:
     return int(load().attn_weighed_decode_workspace_size(N, H_q, H_kv, d_v, page_size, max_pages))
+
+
+def attn_prefill_weights(q, k, lse, cu_seqlens, N, T_tot, H_q, H_kv, d_k, q_stride, k_stride, rows, scale, dtype, weights,
+                         width, stream) -> int:
+    return load().attn_prefill_weights(q, k, lse, cu_seqlens, N, T_tot, H_q, H_kv, d_k, q_stride, k_stride, rows, scale,
+                                       dtype, weights, width, stream)
+
+
+def kv_evict(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages, rows, n, k_cache,
+             v_cache, n_layers, H_kv, d_k, d_v, dtype, weights, budget, recent, sinks, status, stream) -> int:
+    return load().kv_evict(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages, rows, n,
+                           k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, weights, budget, recent, sinks, status, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -188,3 +202,54 @@ def _weighed_decode_on(q, k_cache, v_cache, block_table, ctx_lens, weights, scal
                                ctx_lens.data_ptr(), N, Hq, Hkv, dk, dv, P, ps, MP, qs, _scale(scale, dk), code,
                                o.data_ptr(), lse.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel(), stream))
     return o, lse
+
+
+def attn_prefill_weights_t(q, k, lse, cu_seqlens=None, *, weights, rows=None, scale=None, stream=None):
+    """How much attention each position of the packed prompts has drawn from
+    the last ``rows`` rows of its sequence (None: all), summed over the query
+    heads of a key head, into ``weights`` (fp32 [N, H_kv, width], written in
+    full, zero behind a sequence).  q, k, cu_seqlens, scale as for
+    ``attn_prefill_t``, and its lse.  Returns ``weights``."""
+    return _on_stream(stream, _gpu(q, "q"), _prefill_weights_on, q, k, lse, cu_seqlens, weights, rows, scale)
+
+
+def _prefill_weights_on(q, k, lse, cu_seqlens, weights, rows, scale, stream):
+    import torch
+    dev = q.device
+    if weights.dim() != 3:
+        raise ValueError("weights must be [N, H_kv, width]")
+    cu_seqlens, N, T, Hq, Hkv, dk, _, strides, code = _prompt_args(q, k, k, cu_seqlens)
+    _need(lse, "lse", (T, Hq), torch.float32, dev)
+    width = weights.shape[2]
+    _need(weights, "weights", (N, Hkv, width), torch.float32, dev)
+    rows = max(T, 1) if rows is None else rows
+    _check(attn_prefill_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(), N, T, Hq, Hkv, dk,
+                                strides[0], strides[1], rows, _scale(scale, dk), code, weights.data_ptr(), width, stream))
+    return weights
+
+
+def kv_evict_t(pages: KVPages, rows, k_cache, v_cache, weights=None, *, budget, recent, sinks=0, stream=None):
+    """Rows ``rows`` (int32 [n]) with more than ``budget`` positions keep the
+    first ``sinks``, the last ``recent`` and, by layer and key head, those
+    between with the largest ``weights`` (fp32 [n_layers, rows, H_kv,
+    max_pages * page_size]; None if budget = sinks + recent).  What is kept
+    moves together in the caches and the weights; pages behind the budget go
+    back.  Returns status int32 [n]: 0 done, 2 refused (a row that shares a
+    page among them)."""
+    return _on_stream(stream, _gpu(pages.table, "table"), _kv_evict_on, pages, rows, k_cache, v_cache, weights, budget,
+                      recent, sinks)
+
+
+def _kv_evict_on(pages, rows, k_cache, v_cache, weights, budget, recent, sinks, stream):
+    import torch
+    dev, args = _pages_args(pages)
+    n = _requests(dev, rows=rows)
+    code, L, P, ps, Hkv, dk, dv = _layers(k_cache, v_cache, dev)
+    if (P, ps) != (args[7], args[8]):
+        raise ValueError(f"the caches have {P} pages of {ps} positions, the bookkeeping {args[7]} of {args[8]}")
+    if weights is not None:
+        _need(weights, "weights", (L,) * (k_cache.dim() == 5) + (args[6], Hkv, args[9] * ps), torch.float32, dev)
+    status = torch.empty(n, dtype=torch.int32, device=dev)
+    _check(kv_evict(*args, rows.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(), L, Hkv, dk, dv, code,
+                    weights.data_ptr() if weights is not None else None, budget, recent, sinks, status.data_ptr(), stream))
+    return status

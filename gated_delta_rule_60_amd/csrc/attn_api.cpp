@@ -227,6 +227,32 @@ kda_status attn_window_prefill_backward(const void* q, const void* k, const void
 
 }  // extern "C"
 
+extern "C" {
+
+kda_status attn_prefill_weights(const void* q, const void* k, const float* lse, const int32_t* cu_seqlens, int32_t N,
+                                int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k, int64_t q_stride, int64_t k_stride,
+                                int32_t rows, float scale, kda_dtype dtype, float* weights, int32_t width, void* stream) {
+    // the checks of attn_prefill, with the keys in the place of values and the queries in that of outputs
+    const kda_status s = check_prefill(q, k, k, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_k, q_stride, k_stride, k_stride, scale,
+                                       dtype, q, lse);
+    if (s != KDA_OK) return s;
+    if (T_tot > 0 && !lse) return fail(KDA_ERR_INVALID_ARG, "lse must not be NULL when T_tot > 0");
+    if (rows < 1) return fail(KDA_ERR_INVALID_ARG, "rows must be at least 1");
+    if (width < 1 || width > (1 << 30)) return fail(KDA_ERR_INVALID_ARG, "width must lie in [1, 2^30]");
+    if (!weights || !aligned(weights, 4)) return fail(KDA_ERR_INVALID_ARG, "weights must not be NULL, and 4-byte aligned");
+    // one workgroup of 256 per (256 positions, sequence, key head)
+    if ((static_cast<int64_t>(width) + 255) / 256 * N * H_kv * 256 >= kMaxItems)
+        return fail(KDA_ERR_INVALID_ARG, "ceil(width / 256) * N * H_kv too large");
+    const kda::AttnArgs a{q, k, nullptr, cu_seqlens, N, static_cast<int32_t>(T_tot), H_q, H_kv, d_k, d_k,
+                          static_cast<int32_t>(q_stride), static_cast<int32_t>(k_stride), 0, scale, dtype == KDA_DTYPE_BF16,
+                          nullptr, const_cast<float*>(lse), stream, false};
+    (void)hipGetLastError();  // report only this launch's status
+    const hipError_t e = kda::launch_attn_weights({a, rows, width, weights});
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "attention weights kernel launch");
+}
+
+}  // extern "C"
+
 namespace {
 
 bool pow2(int32_t x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -532,6 +558,32 @@ kda_status kv_compact(void* k_cache, void* v_cache, const int32_t* block_table, 
     const hipError_t e = kda::launch_kv_compact({const_cast<int32_t*>(block_table), const_cast<int32_t*>(lens), nullptr, nullptr, nullptr,
                                                  nullptr, N, n_pages, page_size, __builtin_ctz(page_size), max_pages, stream},
                                                 c, accepted, cu_accepted, N, static_cast<int32_t>(A_tot), new_lens);
+    return e == hipSuccess ? KDA_OK : hip_fail(e, "page kernel launch");
+}
+
+kda_status kv_evict(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* refs, int32_t* free_list, int32_t* n_free,
+                    int32_t n_rows, int32_t n_pages, int32_t page_size, int32_t max_pages, const int32_t* rows, int32_t n,
+                    void* k_cache, void* v_cache, int32_t n_layers, int32_t H_kv, int32_t d_k, int32_t d_v, kda_dtype dtype,
+                    float* weights, int32_t budget, int32_t recent, int32_t sinks, int32_t* status, void* stream) {
+    const void* ptrs[] = {block_table, lens, held, refs, free_list, n_free, rows, status};
+    kda_status s = check_pages(ptrs, n > 0 ? 8 : 6, n_rows, n_pages, page_size, max_pages);
+    if (s != KDA_OK || (s = check_requests(n)) != KDA_OK) return s;
+    kda::CacheArgs c{};
+    if ((s = check_layers(k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, c)) != KDA_OK) return s;
+    if (budget < 1 || budget > (1 << 30) || recent < 0 || sinks < 0 || static_cast<int64_t>(recent) + sinks > budget)
+        return fail(KDA_ERR_INVALID_ARG, "need budget in [1, 2^30], recent >= 0, sinks >= 0 and recent + sinks <= budget");
+    if (!weights && recent + sinks != budget)
+        return fail(KDA_ERR_INVALID_ARG, "without weights the budget must be recent + sinks: there is nothing to choose by");
+    if (!aligned(weights, 4)) return fail(KDA_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+    if (static_cast<int64_t>(n) * n_layers * H_kv * 1024 >= kMaxItems)
+        return fail(KDA_ERR_INVALID_ARG, "n * n_layers * H_kv too large");
+    if (overlap(status, n, rows, n) || overlap(status, n, lens, n_rows) || overlap(status, n, held, n_rows) ||
+        overlap(status, n, refs, n_pages) || overlap(status, n, block_table, static_cast<int64_t>(n_rows) * max_pages))
+        return fail(KDA_ERR_INVALID_ARG, "status must not lie in rows or the bookkeeping: other workgroups read them");
+    (void)hipGetLastError();
+    const hipError_t e = kda::launch_kv_evict({block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size,
+                                               __builtin_ctz(page_size), max_pages, stream}, c,
+                                              {weights, H_kv, budget, recent, sinks}, rows, n, status);
     return e == hipSuccess ? KDA_OK : hip_fail(e, "page kernel launch");
 }
 

@@ -149,6 +149,23 @@ struct CacheArgs {
     int64_t k_row, v_row;
 };
 
+// What kv_evict keeps, and by which weights.
+struct EvictArgs {
+    float* weights;  // [n_layers, n_rows, Hkv, max_pages page_size], or null: no position between sinks and recent ones is kept
+    int32_t Hkv, budget, recent, sinks;
+};
+
+// How much attention the positions of prompts have drawn from their last `rows` rows (o and v are not used, lse is read).
+struct WeightsArgs {
+    AttnArgs f;
+    int32_t rows;
+    int32_t width;
+    float* weights;  // [N, Hkv, width]
+};
+
+hipError_t launch_attn_weights(const WeightsArgs& w);
+
+hipError_t launch_kv_evict(const PageArgs& a, const CacheArgs& c, const EvictArgs& e, const int32_t* rows, int n, int32_t* status);
 hipError_t launch_kv_reserve(const PageArgs& a, const int32_t* rows, const int32_t* n_tokens, int n, int32_t* status);
 hipError_t launch_kv_free(const PageArgs& a, const int32_t* rows, int n);
 hipError_t launch_kv_fork(const PageArgs& a, const CacheArgs& c, const int32_t* src, const int32_t* dst, int n, int32_t* status);

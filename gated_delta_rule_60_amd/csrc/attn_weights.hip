@@ -1,0 +1,171 @@
+// attn_weights.hip -- how much attention the positions of a prompt have drawn
+// from its (last) rows, gfx950.
+//
+// For sequence n, key head g and position j, over the last `rows` rows i:
+//     w[n, g, j] = sum_{h of g} sum_{i >= j} exp(s_ij - lse_i).
+//
+// The scores of the forward pass once more, with the keys kept and the rows
+// walked: a wave has 64 keys of a key head in registers, the tiles of 32 query
+// rows of its heads come through LDS, and S = Q K^T in 32x32 MFMAs leaves a
+// lane the scores of 16 rows against one key, whose weights it adds into one
+// number.  So there is one product a pair and no second one to feed; 64 keys
+// a wave and not 32, because a row read from LDS then serves two products (at
+// one product a read LDS bounds it).  Each sum is one lane's, in one order,
+// joined with the other half-wave's at the end.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "attn_device.hpp"
+#include "attn_launch.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kKeys = 64;             // of a wave
+constexpr int kBK = kKeys * kWaves;   // of a workgroup
+
+}  // namespace
+
+template <bool BF16, int DK>
+__global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, float c /* scale log2(e) */) {
+    using Op = AttnOp<BF16>;
+    using QT = AttnTile<BF16, DK>;
+    using G = typename Op::G;
+    constexpr int BN = 32;                 // query rows of a tile
+    constexpr int QB = BN * QT::ROWB, SLOT = QB + 1024;
+    constexpr int NK = kKeys / 32;
+    __shared__ __attribute__((aligned(1024))) char lds[2][SLOT];
+
+    const AttnArgs& a = wa.f;
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = a.Hq / a.Hkv;
+    // the first keys have the most rows: their workgroups come first, over all sequences
+    const int g = blockIdx.x % a.Hkv, n = blockIdx.x / a.Hkv % a.N;
+    const int key0 = static_cast<int>(blockIdx.x / a.Hkv / a.N) * kBK, wkey = key0 + kKeys * wave;
+    const int2 bl = seq_bounds(a.cu_seqlens, n, a.T_tot);
+    const int beg = bl.x, len = bl.y;
+    float* out = wa.weights + (static_cast<size_t>(n) * a.Hkv + g) * wa.width;
+
+    // A tile's weights are summed by themselves and added with what the sum before has lost to rounding
+    // (compensated): one number takes thousands of rows of every head.
+    float sum[NK] = {}, lost[NK] = {};
+    if (key0 < len) {
+        typename Op::Row k[NK][QT::NF];
+#pragma unroll
+        for (int x = 0; x < NK; ++x) {
+            const int kj = wkey + 32 * x + (lane & 31);
+            const size_t tok = static_cast<size_t>(beg) + (kj < len ? kj : 0);
+            load_row_frags<BF16, DK>(k[x], static_cast<const G*>(a.k) + tok * a.k_stride + static_cast<size_t>(g) * DK, half, kj < len);
+        }
+        const int qs = a.q_stride * Op::ES;
+        const auto qsrc = QT::template src<kWaves>(wave, lane, qs);
+        const int qat = QT::row_at(lane);
+        // row tiles t0 .. t1 - 1 of every head of the group, one after another
+        const int first = len > wa.rows ? len - wa.rows : 0;  // the first row that counts
+        const int t0 = (first > key0 ? first : key0) / BN, t1 = (len + BN - 1) / BN;
+        auto stage_tile = [&](int slot, int hh, int t) __attribute__((always_inline)) {
+            const int h = g * group + hh, left = len - t * BN;
+            const size_t r = static_cast<size_t>(beg) + static_cast<size_t>(t) * BN;
+            QT::template stage<kWaves, BN>(lds[slot], static_cast<const char*>(a.q) + (r * a.q_stride + static_cast<size_t>(h) * DK) * Op::ES,
+                                           left, qs, qsrc, wave);
+            if (wave == 0) {  // the rows' statistics; lanes past the tile's last row read past the range: zero
+                const int there = left < BN ? left : BN;
+                load_lds4(buffer_rsrc(a.lse + r * a.Hq + h, ((there - 1) * a.Hq + 1) * 4), lds[slot] + QB, lane * a.Hq * 4, 0);
+            }
+        };
+        int hh = 0, t = t0, slot = 0;
+        stage_tile(0, 0, t0);
+        loads_done();
+        while (hh < group) {
+            int nh = hh, nt = t + 1;
+            if (nt == t1) {
+                nt = t0;
+                ++nh;
+            }
+            lds_ready();
+            if (nh < group) stage_tile(slot ^ 1, nh, nt);
+            if (t * BN + BN > wkey && wkey < len) {
+                const char* qt = lds[slot];
+                const float* sl = reinterpret_cast<const float*>(qt + QB);
+                f32x16_t s[NK];
+#pragma unroll
+                for (int x = 0; x < NK; ++x) s[x] = f32x16_t{};
+#pragma unroll
+                for (int kk = 0; kk < QT::NF; ++kk) {
+                    const typename Op::Row q = QT::row(qt, qat, 0, kk);
+#pragma unroll
+                    for (int x = 0; x < NK; ++x) s[x] = Op::mma(q, k[x][kk], s[x]);
+                }
+                f32x4_t l2[4];
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4) {
+                    l2[i4] = *reinterpret_cast<const f32x4_t*>(sl + 8 * i4 + 4 * half);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) l2[i4][e] *= kLog2e;
+                }
+                auto add = [&](auto MASKED) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int x = 0; x < NK; ++x) {
+                        float p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int row = t * BN + 8 * (i >> 2) + 4 * half + (i & 3);
+                            p[i] = __builtin_amdgcn_exp2f(fmaf(s[x][i], c, -l2[i >> 2][i & 3]));
+                            if (MASKED && !(row >= wkey + 32 * x + (lane & 31) && row >= first && row < len)) p[i] = 0.f;
+                        }
+#pragma unroll
+                        for (int d = 8; d >= 1; d /= 2)
+#pragma unroll
+                            for (int i = 0; i < d; ++i) p[i] += p[i + d];
+                        const float y = p[0] - lost[x], z = sum[x] + y;
+                        lost[x] = (z - sum[x]) - y;
+                        sum[x] = z;
+                    }
+                };
+                if (t * BN < wkey + kKeys - 1 || t * BN < first || t * BN + BN > len)
+                    add(std::true_type{});
+                else
+                    add(std::false_type{});
+            }
+            hh = nh;
+            t = nt;
+            slot ^= 1;
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < NK; ++x) {
+        const int kj = wkey + 32 * x + (lane & 31);
+        const float y = half_sum(sum[x]);
+        if (half == 0 && kj < wa.width) out[kj] = kj < len ? y : 0.f;
+    }
+}
+
+namespace {
+
+template <bool BF16, int DK>
+hipError_t launch(const WeightsArgs& w) {
+    const AttnArgs& a = w.f;
+    const unsigned blocks = static_cast<unsigned>((w.width + kBK - 1) / kBK) * a.N * a.Hkv;
+    hipLaunchKernelGGL((attn_weights_kernel<BF16, DK>), dim3(blocks), dim3(64 * kWaves), 0, static_cast<hipStream_t>(a.stream), w,
+                       a.scale * kLog2e);
+    return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t launch_dk(const WeightsArgs& w) {
+    switch (w.f.d_k) {
+        case 32: return launch<BF16, 32>(w);
+        case 64: return launch<BF16, 64>(w);
+        default: return launch<BF16, 128>(w);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_attn_weights(const WeightsArgs& w) { return w.f.bf16 ? launch_dk<true>(w) : launch_dk<false>(w); }
+
+}  // namespace kda

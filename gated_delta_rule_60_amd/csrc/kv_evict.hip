@@ -1,0 +1,312 @@
+// kv_evict.hip -- sequences that outgrew their budget of a paged key/value
+// cache keep the first `sinks` positions, the last `recent` ones and, of the
+// others, those with the most accumulated weight, gfx950.
+//
+// The choice is each layer's and key head's own: without position encodings a
+// cache is a set, so the heads of a page need not hold the same positions, only
+// as many.  What is moved is little: with front = budget - recent,
+//   - a chosen position before `front` stays where it is;
+//   - one behind it goes to the place of a position before `front` that is
+//     given up, both in rising order;
+//   - the last `recent` positions move together to [front, budget), in order,
+//     so that they are still the last ones.
+// Against moving all survivors up in order that reads and writes only what
+// must change places (a sequence one page over its budget: the page's worth of
+// choices and the recent positions, not the whole budget).
+//
+// One workgroup does all of it for a request, layer and key head: it finds the
+// weight that parts the chosen from the others digit by digit (three histograms
+// of 2048 bins; the positions with exactly that weight are taken from the
+// lowest on), lists both kinds of place, copies 16 bytes a lane, and clears the
+// weights behind the budget.  A second launch, one workgroup, gives the pages
+// behind the budget back.
+#include <hip/hip_runtime.h>
+
+#include "attn_device.hpp"
+#include "attn_launch.hpp"
+#include "kv_device.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int kBins = 2048;
+constexpr int kPer = 4;                  // candidates a thread looks at in a turn
+constexpr int kTurn = kPer * kThreads;
+constexpr int kList = 2 * kTurn;         // places listed at a time: turns until one is full
+constexpr int kMoves = 8;                // 16-byte units of a thread in flight
+
+// Weights in rising order as unsigned numbers: -0 is 0, and NaN lies below everything.
+__device__ __forceinline__ unsigned order_of(float w) {
+    const unsigned u = __float_as_uint(w + 0.f);
+    return w != w ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+}  // namespace
+
+// Request i, the same for every thread: its row's length, 0 if nothing is to be done; `good` false if it
+// is refused.  A row counts once, and holds its positions in pages that it shares with no other.
+__device__ __forceinline__ int evict_request(const PageArgs& a, const int32_t* rows, int i, int& row, bool& good) {
+    row = rows[i];
+    int bad = 0;
+    for (int j = threadIdx.x; j < i; j += kThreads) bad |= rows[j] == row;
+    good = row >= 0 && row < a.n_rows;
+    int len = 0, held = 0;
+    if (good) {
+        len = a.lens[row];
+        held = a.held[row];
+        good = len >= 0 && held >= 0 && held <= a.max_pages && len <= static_cast<int64_t>(held) << a.page_shift;
+    }
+    if (good)
+        for (int p = threadIdx.x; p < held; p += kThreads) {
+            const int page = a.table[static_cast<int64_t>(row) * a.max_pages + p];
+            bad |= page < 0 || page >= a.n_pages || a.refs[page] != 1;
+        }
+    good = !__syncthreads_or(bad) && good;
+    return good ? len : 0;
+}
+
+__global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArgs c, EvictArgs e, const int32_t* rows, int32_t* status) {
+    __shared__ int s_hist[kBins], s_wave[kThreads / 64], s_pick[2];
+    __shared__ int s_src[kList], s_dst[kList];  // the listed positions, from where to where
+    const int tid = threadIdx.x;
+    const int g = blockIdx.x % e.Hkv, layer = blockIdx.x / e.Hkv % c.n_layers, i = blockIdx.x / e.Hkv / c.n_layers;
+    int row;
+    bool good;
+    const int len = evict_request(a, rows, i, row, good);
+    if (g == 0 && layer == 0 && tid == 0) status[i] = good ? 0 : 2;
+    if (len <= e.budget) return;
+
+    const int32_t* table = a.table + static_cast<int64_t>(row) * a.max_pages;
+    auto token = [&](int pos) __attribute__((always_inline)) {
+        return (static_cast<int64_t>(table[pos >> a.page_shift]) << a.page_shift) + (pos & (a.page_size - 1));
+    };
+    float* w = e.weights ? e.weights + ((static_cast<int64_t>(layer) * a.n_rows + row) * e.Hkv + g) * (static_cast<int64_t>(a.max_pages) << a.page_shift)
+                         : nullptr;
+    const int front = e.budget - e.recent, choose = front - e.sinks;
+    const int from = e.sinks, to = len - e.recent;  // the ones to choose from
+
+    // this layer's and head's units of 16 bytes: of a token, and between tokens
+    const int64_t positions = static_cast<int64_t>(a.n_pages) << a.page_shift;
+    const int ku = static_cast<int>(c.k_row / e.Hkv), vu = static_cast<int>(c.v_row / e.Hkv);
+    u32x4_t* const kc = static_cast<u32x4_t*>(c.k_cache) + layer * positions * c.k_row + g * ku;
+    u32x4_t* const vc = static_cast<u32x4_t*>(c.v_cache) + layer * positions * c.v_row + g * vu;
+
+    if (choose > 0) {
+        // the weight `least` that the choose-th heaviest has, and how many of exactly that are chosen
+        unsigned least = 0, known = 0;  // digits found so far, and their bits
+        int ties = choose;
+        for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
+            const unsigned bins = shift == 0 ? 1024 : kBins;
+            for (int b = tid; b < kBins; b += kThreads) s_hist[b] = 0;
+            __syncthreads();
+            for (int p = from + tid; p < to; p += kThreads) {
+                const unsigned x = order_of(w[p]);
+                if ((x & known) == least) atomicAdd(&s_hist[(x >> shift) & (bins - 1)], 1);
+            }
+            __syncthreads();
+            // thread t has bins 2 t' and 2 t' + 1 from the top: the bin in which the count passes `ties`
+            const int top = kBins - 1 - 2 * tid;
+            const int n0 = s_hist[top], n1 = s_hist[top - 1];
+            int total;
+            const int upto = block_scan(n0 + n1, s_wave, total);
+            const int before = upto - n0 - n1;
+            if (before < ties && before + n0 >= ties) {
+                s_pick[0] = top;
+                s_pick[1] = ties - before;
+            } else if (before + n0 < ties && upto >= ties) {
+                s_pick[0] = top - 1;
+                s_pick[1] = ties - before - n0;
+            }
+            __syncthreads();
+            least |= static_cast<unsigned>(s_pick[0]) << shift;
+            known |= (bins - 1) << shift;
+            ties = s_pick[1];
+        }
+
+        // chosen ones before `front`
+        int over = 0, equal = 0;
+        for (int p = from + tid; p < front; p += kThreads) {
+            const unsigned x = order_of(w[p]);
+            over += x > least;
+            equal += x == least;
+        }
+        int over_front, equal_front;
+        block_scan(over, s_wave, over_front);
+        block_scan(equal, s_wave, equal_front);
+        const int moves = choose - over_front - (equal_front < ties ? equal_front : ties);
+
+        // Two streams of places, each in rising order: given up before `front`, chosen behind it.  A turn is
+        // looked at once: a place that has been filled has another weight.
+        struct Stream {
+            int pos, equal;  // where it goes on, and equal weights before
+            int n;           // listed
+        };
+        Stream gone{from, 0, 0}, come{front, equal_front, 0};
+        auto list = [&](Stream& s, int end, bool want, int* out) __attribute__((always_inline)) {
+            while (s.pos < end && s.n <= kList - kTurn) {
+                bool over[kPer], same[kPer];
+                int eq = 0;
+#pragma unroll
+                for (int x = 0; x < kPer; ++x) {
+                    const int p = s.pos + kPer * tid + x;
+                    const unsigned y = p < end ? order_of(w[p]) : 0u;
+                    over[x] = p < end && y > least;
+                    same[x] = p < end && y == least;
+                    eq += same[x];
+                }
+                int all_equal, all_found;
+                int rank_equal = s.equal + block_scan(eq, s_wave, all_equal) - eq;
+                bool found[kPer];
+                int n = 0;
+#pragma unroll
+                for (int x = 0; x < kPer; ++x) {
+                    const bool kept = over[x] || (same[x] && rank_equal < ties);
+                    rank_equal += same[x];
+                    found[x] = kept == want && s.pos + kPer * tid + x < end;
+                    n += found[x];
+                }
+                int at = s.n + block_scan(n, s_wave, all_found) - n;
+#pragma unroll
+                for (int x = 0; x < kPer; ++x)
+                    if (found[x]) out[at++] = s.pos + kPer * tid + x;
+                s.pos += kTurn;
+                s.equal += all_equal;
+                s.n += all_found;
+            }
+        };
+        // the first n of a list are done: the others move up
+        auto used = [&](Stream& s, int n, int* out) __attribute__((always_inline)) {
+            int rest[kList / kThreads];
+#pragma unroll
+            for (int x = 0; x < kList / kThreads; ++x) {
+                const int at = x * kThreads + tid;
+                rest[x] = at < s.n - n ? out[n + at] : 0;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < kList / kThreads; ++x) {
+                const int at = x * kThreads + tid;
+                if (at < s.n - n) out[at] = rest[x];
+            }
+            s.n -= n;
+        };
+        for (int done = 0; done < moves;) {
+            list(gone, front, false, s_dst);
+            list(come, to, true, s_src);
+            __syncthreads();
+            const int n = gone.n < come.n ? gone.n : come.n;  // at least one: each is listed until it is long or all there
+            auto copy = [&](u32x4_t* cache, int units, int64_t step) __attribute__((always_inline)) {
+                const int lg = __builtin_ctz(units), all = n << lg;
+                for (int x0 = tid; x0 < all; x0 += kThreads * kMoves) {
+                    u32x4_t y[kMoves];
+                    int64_t at[kMoves];
+#pragma unroll
+                    for (int b = 0; b < kMoves; ++b) {
+                        const int x = x0 + b * kThreads, m = x >> lg, u = x & (units - 1);
+                        at[b] = -1;
+                        if (x >= all) continue;
+                        y[b] = cache[token(s_src[m]) * step + u];
+                        at[b] = token(s_dst[m]) * step + u;
+                    }
+#pragma unroll
+                    for (int b = 0; b < kMoves; ++b)
+                        if (at[b] >= 0) cache[at[b]] = y[b];
+                }
+            };
+            copy(kc, ku, c.k_row);
+            copy(vc, vu, c.v_row);
+            for (int m = tid; m < n; m += kThreads) w[s_dst[m]] = w[s_src[m]];
+            done += n;
+            __syncthreads();
+            if (done < moves) {
+                used(gone, n, s_dst);
+                used(come, n, s_src);
+                __syncthreads();
+            }
+        }
+    }
+
+    // The last ones: block by block, all of a block read before any of it is written.  A block's writes lie
+    // before every later block's reads.
+    const int back = len - e.budget;
+    auto shift = [&](u32x4_t* cache, int units, int64_t step) __attribute__((always_inline)) {
+        const int lg = __builtin_ctz(units);
+        const int64_t all = static_cast<int64_t>(e.recent) << lg;
+        for (int64_t x0 = 0; x0 < all; x0 += kThreads * kMoves) {
+            u32x4_t y[kMoves];
+            int64_t at[kMoves];
+#pragma unroll
+            for (int b = 0; b < kMoves; ++b) {
+                const int64_t x = x0 + b * kThreads + tid;
+                at[b] = -1;
+                if (x >= all) continue;
+                const int m = front + static_cast<int>(x >> lg), u = static_cast<int>(x & (units - 1));
+                y[b] = cache[token(m + back) * step + u];
+                at[b] = token(m) * step + u;
+            }
+            loads_done();
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < kMoves; ++b)
+                if (at[b] >= 0) cache[at[b]] = y[b];
+        }
+    };
+    __syncthreads();  // what goes to places in front has been read
+    shift(kc, ku, c.k_row);
+    shift(vc, vu, c.v_row);
+    if (!w) return;
+    for (int m0 = 0; m0 < e.recent; m0 += kThreads) {
+        const int m = m0 + tid;
+        const float x = m < e.recent ? w[front + m + back] : 0.f;
+        loads_done();
+        __syncthreads();
+        if (m < e.recent) w[front + m] = x;
+    }
+    __syncthreads();  // written before cleared, read before cleared
+    for (int p = e.budget + tid; p < len; p += kThreads) w[p] = 0.f;
+}
+
+// The pages behind the budget go back, in the order of the requests and of the rows' pages.
+__global__ __launch_bounds__(kThreads) void kv_evict_pages_kernel(PageArgs a, int budget, const int32_t* rows, int n, const int32_t* status) {
+    __shared__ int s_row[kThreads], s_need[kThreads];
+    __shared__ int64_t s_upto[kThreads], s_wave[kThreads / 64];
+    const int i = threadIdx.x;
+    int row = -1, give = 0;
+    const int need = (budget + a.page_size - 1) >> a.page_shift;
+    if (i < n && status[i] == 0) {
+        row = rows[i];
+        if (a.lens[row] > budget) {
+            a.lens[row] = budget;
+            give = a.held[row] - need;
+            a.held[row] = need;
+        }
+    }
+    s_row[i] = row;
+    int64_t total;
+    s_upto[i] = block_scan(static_cast<int64_t>(give), s_wave, total);
+    const int have = free_pages(a);
+    __syncthreads();
+    for (int64_t e = i; e < total; e += kThreads) {
+        const int r = request_of(s_upto, n, e);
+        const int64_t at = static_cast<int64_t>(s_row[r]) * a.max_pages + need + (e - (r ? s_upto[r - 1] : 0));
+        const int page = a.table[at];
+        a.table[at] = -1;
+        if (page < 0 || page >= a.n_pages) continue;
+        a.refs[page] = 0;
+        if (have + e < a.n_pages) a.free[have + e] = page;
+    }
+    if (i == 0 && total > 0) *a.n_free = static_cast<int>(have + total < a.n_pages ? have + total : a.n_pages);
+}
+
+hipError_t launch_kv_evict(const PageArgs& a, const CacheArgs& c, const EvictArgs& e, const int32_t* rows, int n, int32_t* status) {
+    if (n == 0) return hipSuccess;
+    const hipStream_t st = static_cast<hipStream_t>(a.stream);
+    hipLaunchKernelGGL(kv_evict_kernel, dim3(static_cast<unsigned>(n) * c.n_layers * e.Hkv), dim3(kThreads), 0, st, a, c, e, rows, status);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL(kv_evict_pages_kernel, dim3(1), dim3(kThreads), 0, st, a, e.budget, rows, n, status);
+    return hipGetLastError();
+}
+
+}  // namespace kda

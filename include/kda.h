@@ -525,6 +525,30 @@ size_t attn_window_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int
                                                    int32_t sinks, kda_dtype dtype);
 
 /*
+ * attn_prefill_weights -- how much attention each position of a prompt has
+ * drawn from the last `rows` rows of its sequence, from attn_prefill's lse:
+ *
+ *     weights[n, g, j] = sum_h sum_i exp(s_ij - lse_i)   (query heads h of key
+ *                        head g; rows i >= j among the last `rows` ones)
+ *
+ *   q, k, cu_seqlens, N, T_tot, H_q, H_kv, d_k, strides, scale, dtype   as for
+ *              attn_prefill
+ *   lse        device [T_tot, H_q] float32
+ *   rows       at least 1 (T_tot or more: all rows)
+ *   weights    device [N, H_kv, width] float32, written in full: zero at and
+ *              past a sequence's length; positions at or past width are left
+ *              out.  With width = max_pages * page_size, what kv_evict and
+ *              attn_weighed_decode take for one layer.
+ *   width      in [1, 2^30], with ceil(width / 256) * N * H_kv < 2^24
+ * Sums are fp32, in one order: the same inputs give the same bits.
+ */
+kda_status attn_prefill_weights(const void* q, const void* k, const float* lse,
+                                const int32_t* cu_seqlens, int32_t N, int64_t T_tot, int32_t H_q,
+                                int32_t H_kv, int32_t d_k, int64_t q_stride, int64_t k_stride,
+                                int32_t rows, float scale, kda_dtype dtype, float* weights,
+                                int32_t width, void* stream);
+
+/*
  * A paged cache holds the keys and values of many sequences of growing
  * length in pages of page_size positions:
  *
@@ -731,6 +755,43 @@ kda_status kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
                       int32_t N, int64_t A_tot, int32_t n_layers, int32_t H_kv, int32_t d_k,
                       int32_t d_v, int32_t n_pages, int32_t page_size, int32_t max_pages,
                       kda_dtype dtype, int32_t* new_lens, void* stream);
+
+/*
+ * kv_evict -- row rows[i], where it holds more than `budget` positions, keeps
+ * `budget` of them: the first `sinks`, the last `recent`, and of those between
+ * the budget - sinks - recent with the largest weights (the lower position
+ * where weights are equal; NaN counts as less than any number), by layer and
+ * key head.  Rows within the budget stay as they are.
+ *
+ * Afterwards the row has `budget` positions.  With front = budget - recent:
+ * kept positions before front stay in their places, the kept ones between
+ * front and the last `recent` fill the places before front that were given up
+ * (both in rising order), and the last `recent` ones stand at front, front + 1,
+ * ... in their order.  Their weights move with them, and the weights of the
+ * positions from budget to the row's old length become zero.  The order within a cache means
+ * nothing to attn_tree_decode and attn_weighed_decode; attn_window_decode's
+ * window and sinks keep their meaning as long as window <= recent and its
+ * sinks are no more than these.  Pages behind the budget are given back, in
+ * the order of the requests and of the row's pages.  Positions behind the
+ * row's length (drafted tokens) are lost.
+ *
+ *   weights    device [n_layers, n_rows, H_kv, max_pages * page_size] float32,
+ *              or NULL if budget = sinks + recent (nothing is chosen)
+ *   budget, recent, sinks   budget in [1, 2^30], recent + sinks <= budget
+ *   n          at most 1024, n * n_layers * H_kv < 2^22
+ *   status     [n]: 0 done (also where nothing was to be done), 2 refused: a
+ *              row outside the table, a repeated one (the first counts), one
+ *              that holds fewer pages than its positions need, or one that
+ *              shares a page with another (refs other than 1: what it moves
+ *              would change under the other).  Must share no memory with rows
+ *              or the bookkeeping.
+ */
+kda_status kv_evict(int32_t* block_table, int32_t* lens, int32_t* held, int32_t* refs,
+                    int32_t* free_list, int32_t* n_free, int32_t n_rows, int32_t n_pages,
+                    int32_t page_size, int32_t max_pages, const int32_t* rows, int32_t n,
+                    void* k_cache, void* v_cache, int32_t n_layers, int32_t H_kv, int32_t d_k,
+                    int32_t d_v, kda_dtype dtype, float* weights, int32_t budget, int32_t recent,
+                    int32_t sinks, int32_t* status, void* stream);
 
 /* Static text for a status code. */
 const char* kda_status_string(kda_status status);

@@ -140,3 +140,68 @@ def test_decode_workspaces():
         assert size(*kw) == 0
     for kw in ((0, 1, 1, 64, 16, 10), (1, 3, 2, 64, 16, 10), (1, 1, 1, 48, 16, 10), (1, 1, 1, 64, 15, 10), (1, 1, 1, 64, 16, 0)):
         assert kda.attn_weighed_decode_workspace_size(*kw) == 0
+
+
+def _weights(**kw):
+    a = dict(q=FAKE, k=FAKE, lse=FAKE, cu_seqlens=FAKE, N=1, T_tot=64, H_q=4, H_kv=2, d_k=64, q_stride=256, k_stride=128, rows=32,
+             scale=0.125, dtype=BF16, weights=FAKE, width=64, stream=None)
+    a.update(kw)
+    return kda.attn_prefill_weights(**a)
+
+
+@pytest.mark.parametrize("kw,status,needle", [c for c in COMMON if not {"v", "o", "d_v", "v_stride"} & set(c[0])] + [
+    (dict(lse=None), BAD, "lse"),
+    (dict(rows=0), BAD, "rows"),
+    (dict(rows=-1), BAD, "rows"),
+    (dict(width=0), BAD, "width"),
+    (dict(width=(1 << 30) + 1), BAD, "width"),
+    (dict(weights=None), BAD, "weights"),
+    (dict(weights=FAKE + 2), BAD, "weights"),
+    (dict(width=1 << 30, N=2, H_q=4, H_kv=2), BAD, "ceil(width / 256)"),
+])
+def test_prefill_weights_refuses(kw, status, needle):
+    assert _weights(**kw) == status
+    assert needle in kda.kda_last_error()
+
+
+def _evict(**kw):
+    a = dict(block_table=FAKE, lens=FAKE + (1 << 20), held=FAKE + (2 << 20), refs=FAKE + (3 << 20), free_list=FAKE, n_free=FAKE,
+             n_rows=8, n_pages=100, page_size=16, max_pages=50, rows=FAKE + (4 << 20), n=4, k_cache=FAKE, v_cache=FAKE, n_layers=2,
+             H_kv=2, d_k=64, d_v=32, dtype=BF16, weights=FAKE, budget=64, recent=16, sinks=4, status=FAKE + (5 << 20), stream=None)
+    a.update(kw)
+    return kda.kv_evict(**a)
+
+
+@pytest.mark.parametrize("kw,status,needle", [
+    (dict(n_rows=0), BAD, "n_rows"),
+    (dict(page_size=24), BAD, "page_size"),
+    (dict(n_pages=0), BAD, "n_pages"),
+    (dict(max_pages=0), BAD, "max_pages"),
+    (dict(n=-1), BAD, "1024"),
+    (dict(n=1025), BAD, "1024"),
+    (dict(rows=None), BAD, "must not be NULL"),
+    (dict(status=None), BAD, "must not be NULL"),
+    (dict(refs=None), BAD, "must not be NULL"),
+    (dict(rows=FAKE + 2), BAD, "4-byte aligned"),
+    (dict(k_cache=None), BAD, "must not be NULL"),
+    (dict(v_cache=FAKE + 8), BAD, "16-byte aligned"),
+    (dict(n_layers=0), BAD, "n_layers"),
+    (dict(H_kv=0), BAD, "H_kv"),
+    (dict(d_k=48), NOT, "d_k and d_v"),
+    (dict(dtype=3), NOT, "dtype"),
+    (dict(weights=FAKE + 2), BAD, "weights"),
+    (dict(weights=None), BAD, "without weights"),
+    (dict(budget=0, recent=0, sinks=0), BAD, "budget"),
+    (dict(budget=(1 << 30) + 1), BAD, "budget"),
+    (dict(recent=-1), BAD, "recent"),
+    (dict(sinks=-1), BAD, "sinks"),
+    (dict(recent=61), BAD, "recent + sinks"),
+    (dict(recent=2 ** 31 - 1, sinks=2 ** 31 - 1), BAD, "recent + sinks"),
+    (dict(n=1024, n_layers=64, H_kv=64), BAD, "n * n_layers * H_kv"),
+    (dict(status=FAKE + (4 << 20) + 12), BAD, "status"),
+    (dict(status=FAKE + (1 << 20) + 28), BAD, "status"),
+    (dict(status=FAKE + 396), BAD, "status"),
+])
+def test_evict_refuses(kw, status, needle):
+    assert _evict(**kw) == status
+    assert needle in kda.kda_last_error()

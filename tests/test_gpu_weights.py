@@ -171,3 +171,182 @@ def test_decode_refusals():
         kda.attn_weighed_decode_t(torch.cat([c.q, c.q]), c.k, c.v, c.table, c.lens, c.weights)
     with pytest.raises(kda.KDAError, match="workspace smaller"):
         c.call(workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+# ---------------------------------------------------------------------------
+# prompts
+# ---------------------------------------------------------------------------
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _prompt(lens, hq, hkv, dk, dtype, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    t = sum(lens)
+    q, k = ((spread * torch.randn(t, h, dk, generator=g)).to(DT[dtype]).cuda() for h in (hq, hkv))
+    cu = torch.tensor([0, *torch.tensor(lens).cumsum(0).tolist()], dtype=torch.int32).cuda()
+    # the row statistics, rounded from 64 bits
+    lse = torch.zeros(t, hq, dtype=torch.float64)
+    a = 0
+    for n in lens:
+        for h in range(hq if n else 0):
+            s = q[a:a + n, h].cpu().double() @ k[a:a + n, h // (hq // hkv)].cpu().double().T / math.sqrt(dk)
+            lse[a:a + n, h] = torch.logsumexp(torch.where(torch.ones(n, n).tril() > 0, s, -math.inf), -1)
+        a += n
+    return q, k, lse.float().cuda(), cu
+
+
+def _check_prompt(lens, hq, hkv, dk, dtype, rows=None, width=None, seed=0, spread=1.0):
+    q, k, lse, cu = _prompt(lens, hq, hkv, dk, dtype, seed, spread)
+    width = max(lens) + 3 if width is None else width
+    weights = torch.full((len(lens), hkv, width), float("nan"), device="cuda")
+    assert kda.attn_prefill_weights_t(q, k, lse, cu, weights=weights, rows=rows) is weights
+    torch.cuda.synchronize()
+    value, bound = (torch.zeros(len(lens), hkv, width, dtype=torch.float64) for _ in range(2))
+    a = 0
+    for n, length in enumerate(lens):
+        first = 0 if rows is None else max(0, length - rows)
+        seen = torch.ones(length, length, dtype=torch.bool).tril()[first:]
+        for h in range(hq if length else 0):
+            g = h // (hq // hkv)
+            v, b = weights_of(q[a + first:a + length, h].cpu().double(), k[a:a + length, g].cpu().double(), seen,
+                              1 / math.sqrt(dk), lse[a + first:a + length, h].cpu().double())
+            m = min(length, width)
+            value[n, g, :m] += v[:m]
+            bound[n, g, :m] += b[:m]
+        # the heads of a group are summed on
+        bound[n] += (hq // hkv) * E24 * value[n]
+        a += length
+    attn_ref.check(weights, (value, bound), f"{dtype} weights")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk", [32, 64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 2), (5, 1), (9, 3)])
+def test_prompt_head_sizes_and_groups(dtype, dk, hq, hkv):
+    _check_prompt([70, 331], hq, hkv, dk, dtype, seed=dk + hq)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[1], [2], [31, 32, 33], [63, 64, 65], [127, 128, 129], [1, 0, 0, 5, 1], [0, 300, 0],
+                                  [255, 256, 257, 513], [1] * 70, [3, 130] * 40])
+@pytest.mark.parametrize("rows", [1, 17, 32, 64, 100, None])
+def test_prompt_lengths_and_rows(dtype, lens, rows):
+    _check_prompt(lens, 2, 1, 64, dtype, rows=rows, seed=len(lens))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", [1, 100, 256, 257, 1024, 5000])
+def test_prompt_widths(dtype, width):
+    """Narrower than a sequence: what lies past it is left out."""
+    _check_prompt([300, 1, 700], 2, 2, 32, dtype, width=width, seed=width)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_longer_sequences(dtype):
+    _check_prompt([2100, 777], 4, 2, 128, dtype, seed=5)
+    _check_prompt([2100, 777], 8, 1, 128, dtype, rows=64, seed=6)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_peaked_rows(dtype):
+    _check_prompt([200, 33], 2, 2, 64, dtype, seed=11, spread=3.0)
+
+
+def test_prompt_every_row_gives_one():
+    """All rows: a row's weights sum to one, so the positions' sum to the rows times heads of the group."""
+    q, k, lse, cu = _prompt([400], 6, 2, 64, "f32", 3)
+    w = kda.attn_prefill_weights_t(q, k, lse, cu, weights=torch.empty(1, 2, 400, device="cuda"))
+    assert ((w.double().sum(-1) - 3 * 400).abs() < 1200 * (400 + 400 + 64) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_from_the_passes_own_statistics(dtype):
+    lens = [200, 61]
+    q, k, lse, cu = _prompt(lens, 4, 2, 64, dtype, 8)
+    _, own = kda.attn_prefill_t(q, k, k, cu)
+    a, b = (kda.attn_prefill_weights_t(q, k, x, cu, weights=torch.empty(2, 2, 200, device="cuda")) for x in (lse, own))
+    torch.cuda.synchronize()
+    # either lse is within 64 + 200 + 8 roundings of exact, twice
+    assert ((a - b).abs() <= 2 * (64 + 200 + 8 + 40) * 2.0 ** -24 * 2 * (a + 1e-30)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_padding_neighbours_and_later_tokens(dtype):
+    q, k, lse, cu = _prompt([170, 50, 190], 2, 1, 64, dtype, 13)
+    call = lambda: kda.attn_prefill_weights_t(q, k, lse, cu, weights=torch.full((3, 1, 256), 7.0, device="cuda"))  # noqa: E731
+    want = call()
+    q[170:220], k[170:220], lse[170:220] = float("nan"), float("inf"), float("nan")
+    got = call()
+    assert torch.equal(got[[0, 2]], want[[0, 2]]) and (got[1, :, 50:] == 0).all()
+    # a key that is not finite: the others of its sequence keep theirs
+    k[100, 0, 3] = float("nan")
+    got = call()
+    keep = [j for j in range(256) if j != 100]
+    assert torch.equal(got[0][:, keep], want[0][:, keep]) and torch.isnan(got[0][:, 100]).all()
+    # rows past the last sequence do not count, whatever they hold
+    cu2 = torch.tensor([0, 170], dtype=torch.int32).cuda()
+    lse[170:], q[170:] = float("nan"), float("inf")
+    k[100, 0, 3] = 0.5
+    w1 = kda.attn_prefill_weights_t(q, k, lse, cu2, weights=torch.empty(1, 1, 256, device="cuda"))
+    w2 = kda.attn_prefill_weights_t(q[:170], k[:170], lse[:170], weights=torch.empty(1, 1, 256, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(w1, w2)
+
+
+def test_prompt_streams_graph_replays_slices_and_the_same_bits():
+    fused = torch.randn(500, 8 * 64, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    q, k = fused[:, :256].view(500, 4, 64), fused[:, 256:384].view(500, 2, 64)
+    cu = torch.tensor([0, 330, 500], dtype=torch.int32).cuda()
+    _, lse = kda.attn_prefill_t(q, k, k, cu)
+    call = lambda **kw: kda.attn_prefill_weights_t(q, k, lse, cu, weights=torch.empty(2, 2, 400, device="cuda"), **kw)  # noqa: E731
+    want = call()
+    assert torch.equal(want, kda.attn_prefill_weights_t(q.contiguous(), k.contiguous(), lse, cu, weights=torch.empty(2, 2, 400, device="cuda")))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = call(stream=side)
+    side.synchronize()
+    assert torch.equal(want, other)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = call(rows=50)
+    for n in range(3):
+        lse.add_(0.5 * n)
+        kept.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kept, call(rows=50)), f"replay {n}"
+
+
+def test_prompt_no_tokens():
+    q, k = (torch.empty(0, h, 64, device="cuda") for h in (4, 2))
+    w = kda.attn_prefill_weights_t(q, k, torch.empty(0, 4, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda"),
+                                   weights=torch.full((2, 2, 300), 7.0, device="cuda"))
+    torch.cuda.synchronize()
+    assert (w == 0).all()
+
+
+def test_prompt_offsets_past_32_bits():
+    stride, t = 1 << 16, 33000
+    fused = torch.zeros(t, stride, dtype=torch.bfloat16, device="cuda")
+    fused[:, :384] = torch.randn(t, 384, generator=torch.Generator(device="cuda").manual_seed(5), device="cuda")
+    q, k = fused[:, :256].view(t, 2, 128), fused[:, 256:384].view(t, 1, 128)
+    lse = torch.full((t, 2), 5.0, device="cuda")
+    cu = torch.tensor([0, 32800, 33000], dtype=torch.int32).cuda()
+    w = kda.attn_prefill_weights_t(q, k, lse, cu, weights=torch.empty(2, 1, 256, device="cuda"))
+    alone = kda.attn_prefill_weights_t(q[32800:].contiguous(), k[32800:].contiguous(), lse[32800:].contiguous(),
+                                       weights=torch.empty(1, 1, 256, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(w[1], alone[0])
+
+
+def test_prompt_refusals():
+    q, k, lse, cu = _prompt([20], 4, 2, 32, "f32", 1)
+    w = torch.empty(1, 2, 32, device="cuda")
+    with pytest.raises(ValueError, match="lse must have shape"):
+        kda.attn_prefill_weights_t(q, k, lse[:10], cu, weights=w)
+    with pytest.raises(ValueError, match="weights must have shape"):
+        kda.attn_prefill_weights_t(q, k, lse, cu, weights=torch.empty(2, 2, 32, device="cuda"))
+    with pytest.raises(ValueError, match="contiguous"):
+        kda.attn_prefill_weights_t(q, k, lse, cu, weights=w[..., :20])
+    with pytest.raises(kda.KDAError, match="rows"):
+        kda.attn_prefill_weights_t(q, k, lse, cu, weights=w, rows=0)
