@@ -40,6 +40,7 @@ from ._attn import (  # noqa: F401
 from ._bounded import (  # noqa: F401
     attn_prefill_weights,
     attn_prefill_weights_t,
+    attn_prefill_weights_workspace_size,
     attn_weighed_decode,
     attn_weighed_decode_t,
     attn_weighed_decode_workspace_size,

@@ -57,9 +57,13 @@ def attn_weighed_decode_workspace_size(N, H_q, H_kv, d_v, page_size, max_pages) 
 
 
 def attn_prefill_weights(q, k, lse, cu_seqlens, N, T_tot, H_q, H_kv, d_k, q_stride, k_stride, rows, scale, dtype, weights,
-                         width, stream) -> int:
+                         width, workspace, workspace_bytes, stream) -> int:
     return load().attn_prefill_weights(q, k, lse, cu_seqlens, N, T_tot, H_q, H_kv, d_k, q_stride, k_stride, rows, scale,
-                                       dtype, weights, width, stream)
+                                       dtype, weights, width, workspace, workspace_bytes, stream)
+
+
+def attn_prefill_weights_workspace_size(N, T_tot, H_q, H_kv, rows) -> int:
+    return int(load().attn_prefill_weights_workspace_size(N, T_tot, H_q, H_kv, rows))
 
 
 def kv_evict(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages, rows, n, k_cache,
@@ -204,16 +208,18 @@ def _weighed_decode_on(q, k_cache, v_cache, block_table, ctx_lens, weights, scal
     return o, lse
 
 
-def attn_prefill_weights_t(q, k, lse, cu_seqlens=None, *, weights, rows=None, scale=None, stream=None):
+def attn_prefill_weights_t(q, k, lse, cu_seqlens=None, *, weights, rows=None, scale=None, workspace=None, stream=None):
     """How much attention each position of the packed prompts has drawn from
     the last ``rows`` rows of its sequence (None: all), summed over the query
     heads of a key head, into ``weights`` (fp32 [N, H_kv, width], written in
     full, zero behind a sequence).  q, k, cu_seqlens, scale as for
-    ``attn_prefill_t``, and its lse.  Returns ``weights``."""
-    return _on_stream(stream, _gpu(q, "q"), _prefill_weights_on, q, k, lse, cu_seqlens, weights, rows, scale)
+    ``attn_prefill_t``, and its lse.  Returns ``weights``.  ``workspace``:
+    optional uint8 device tensor of ``attn_prefill_weights_workspace_size``
+    bytes."""
+    return _on_stream(stream, _gpu(q, "q"), _prefill_weights_on, q, k, lse, cu_seqlens, weights, rows, scale, workspace)
 
 
-def _prefill_weights_on(q, k, lse, cu_seqlens, weights, rows, scale, stream):
+def _prefill_weights_on(q, k, lse, cu_seqlens, weights, rows, scale, workspace, stream):
     import torch
     dev = q.device
     if weights.dim() != 3:
@@ -223,8 +229,10 @@ def _prefill_weights_on(q, k, lse, cu_seqlens, weights, rows, scale, stream):
     width = weights.shape[2]
     _need(weights, "weights", (N, Hkv, width), torch.float32, dev)
     rows = max(T, 1) if rows is None else rows
+    ws = _workspace(workspace, attn_prefill_weights_workspace_size(N, T, Hq, Hkv, rows), dev)
     _check(attn_prefill_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(), N, T, Hq, Hkv, dk,
-                                strides[0], strides[1], rows, _scale(scale, dk), code, weights.data_ptr(), width, stream))
+                                strides[0], strides[1], rows, _scale(scale, dk), code, weights.data_ptr(), width, ws.data_ptr(),
+                                ws.numel(), stream))
     return weights
 
 

@@ -86,7 +86,8 @@ SIGNATURES = {
                                            ctypes.c_float, ctypes.c_int, _vp, _fp, _fp, _vp, _sz, _vp]),
     "attn_weighed_decode_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
     "attn_prefill_weights": (ctypes.c_int, [_vp, _vp, _fp, _ip, _i32, _i64, _i32, _i32, _i32, _i64, _i64, _i32,
-                                            ctypes.c_float, ctypes.c_int, _fp, _i32, _vp]),
+                                            ctypes.c_float, ctypes.c_int, _fp, _i32, _vp, _sz, _vp]),
+    "attn_prefill_weights_workspace_size": (_sz, [_i32, _i64, _i32, _i32, _i32]),
     "kv_evict": (ctypes.c_int, [_ip] * 6 + [_i32] * 4 + [_ip, _i32, _vp, _vp, _i32, _i32, _i32, _i32, ctypes.c_int, _fp,
                                                          _i32, _i32, _i32, _ip, _vp]),
     "kv_reserve": (ctypes.c_int, [_ip] * 6 + [_i32] * 4 + [_ip, _ip, _i32, _ip, _vp]),

@@ -229,9 +229,17 @@ kda_status attn_window_prefill_backward(const void* q, const void* k, const void
 
 extern "C" {
 
+size_t attn_prefill_weights_workspace_size(int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t rows) {
+    if (N < 1 || T_tot < 0 || T_tot > (int64_t{1} << 30) || H_kv < 1 || H_q < 1 || H_q > 4096 || H_q % H_kv != 0 || rows < 1)
+        return 0;
+    const int32_t parts = kda::attn_weights_parts(N, T_tot, H_q, H_kv, rows, kda::device_cus_or_default());
+    return parts > 1 ? static_cast<size_t>(parts) * H_kv * T_tot * sizeof(float) : 0;
+}
+
 kda_status attn_prefill_weights(const void* q, const void* k, const float* lse, const int32_t* cu_seqlens, int32_t N,
                                 int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t d_k, int64_t q_stride, int64_t k_stride,
-                                int32_t rows, float scale, kda_dtype dtype, float* weights, int32_t width, void* stream) {
+                                int32_t rows, float scale, kda_dtype dtype, float* weights, int32_t width, void* workspace,
+                                size_t workspace_bytes, void* stream) {
     // the checks of attn_prefill, with the keys in the place of values and the queries in that of outputs
     const kda_status s = check_prefill(q, k, k, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_k, q_stride, k_stride, k_stride, scale,
                                        dtype, q, lse);
@@ -243,11 +251,17 @@ kda_status attn_prefill_weights(const void* q, const void* k, const float* lse, 
     // one workgroup of 256 per (256 positions, sequence, key head)
     if ((static_cast<int64_t>(width) + 255) / 256 * N * H_kv * 256 >= kMaxItems)
         return fail(KDA_ERR_INVALID_ARG, "ceil(width / 256) * N * H_kv too large");
+    const size_t need = attn_prefill_weights_workspace_size(N, T_tot, H_q, H_kv, rows);
+    if (workspace_bytes < need) return fail(KDA_ERR_INVALID_ARG, "workspace smaller than attn_prefill_weights_workspace_size");
+    if (need > 0 && !workspace) return fail(KDA_ERR_INVALID_ARG, "workspace must not be NULL");
+    if (!aligned(workspace, 256)) return fail(KDA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     const kda::AttnArgs a{q, k, nullptr, cu_seqlens, N, static_cast<int32_t>(T_tot), H_q, H_kv, d_k, d_k,
                           static_cast<int32_t>(q_stride), static_cast<int32_t>(k_stride), 0, scale, dtype == KDA_DTYPE_BF16,
                           nullptr, const_cast<float*>(lse), stream, false};
     (void)hipGetLastError();  // report only this launch's status
-    const hipError_t e = kda::launch_attn_weights({a, rows, width, weights});
+    const hipError_t e = kda::launch_attn_weights({a, rows, width, weights,
+                                                   kda::attn_weights_parts(N, T_tot, H_q, H_kv, rows, kda::device_cus_or_default()),
+                                                   static_cast<float*>(workspace)});
     return e == hipSuccess ? KDA_OK : hip_fail(e, "attention weights kernel launch");
 }
 

@@ -161,7 +161,11 @@ struct WeightsArgs {
     int32_t rows;
     int32_t width;
     float* weights;  // [N, Hkv, width]
+    int32_t parts;   // attn_weights_parts
+    float* part;     // [parts, Hkv, T_tot], if parts > 1
 };
+
+int32_t attn_weights_parts(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t rows, int cus);
 
 hipError_t launch_attn_weights(const WeightsArgs& w);
 

@@ -34,7 +34,7 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
     using Op = AttnOp<BF16>;
     using QT = AttnTile<BF16, DK>;
     using G = typename Op::G;
-    constexpr int BN = 32;                 // query rows of a tile
+    constexpr int BN = 64;                 // query rows of a tile
     constexpr int QB = BN * QT::ROWB, SLOT = QB + 1024;
     constexpr int NK = kKeys / 32;
     __shared__ __attribute__((aligned(1024))) char lds[2][SLOT];
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
     const int key0 = static_cast<int>(blockIdx.x / a.Hkv / a.N) * kBK, wkey = key0 + kKeys * wave;
     const int2 bl = seq_bounds(a.cu_seqlens, n, a.T_tot);
     const int beg = bl.x, len = bl.y;
-    float* out = wa.weights + (static_cast<size_t>(n) * a.Hkv + g) * wa.width;
+    if (wa.parts > 1 && key0 >= len) return;
 
     // A tile's weights are summed by themselves and added with what the sum before has lost to rounding
     // (compensated): one number takes thousands of rows of every head.
@@ -77,43 +77,47 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
                 load_lds4(buffer_rsrc(a.lse + r * a.Hq + h, ((there - 1) * a.Hq + 1) * 4), lds[slot] + QB, lane * a.Hq * 4, 0);
             }
         };
-        int hh = 0, t = t0, slot = 0;
-        stage_tile(0, 0, t0);
+        // this workgroup's part of them
+        const int64_t all = static_cast<int64_t>(group) * (t1 - t0);
+        const int begin = static_cast<int>(all * blockIdx.y / wa.parts), end = static_cast<int>(all * (blockIdx.y + 1) / wa.parts);
+        int hh = begin / (t1 - t0), t = t0 + begin % (t1 - t0), slot = 0;
+        if (begin < end) stage_tile(0, hh, t);
         loads_done();
-        while (hh < group) {
+        for (int step = begin; step < end; ++step) {
             int nh = hh, nt = t + 1;
             if (nt == t1) {
                 nt = t0;
                 ++nh;
             }
             lds_ready();
-            if (nh < group) stage_tile(slot ^ 1, nh, nt);
+            if (step + 1 < end) stage_tile(slot ^ 1, nh, nt);
             if (t * BN + BN > wkey && wkey < len) {
                 const char* qt = lds[slot];
                 const float* sl = reinterpret_cast<const float*>(qt + QB);
-                f32x16_t s[NK];
+                auto scores = [&](int r0, f32x16_t (&s)[NK]) __attribute__((always_inline)) {
 #pragma unroll
-                for (int x = 0; x < NK; ++x) s[x] = f32x16_t{};
+                    for (int x = 0; x < NK; ++x) s[x] = f32x16_t{};
 #pragma unroll
-                for (int kk = 0; kk < QT::NF; ++kk) {
-                    const typename Op::Row q = QT::row(qt, qat, 0, kk);
+                    for (int kk = 0; kk < QT::NF; ++kk) {
+                        const typename Op::Row q = QT::row(qt, qat, r0, kk);
 #pragma unroll
-                    for (int x = 0; x < NK; ++x) s[x] = Op::mma(q, k[x][kk], s[x]);
-                }
-                f32x4_t l2[4];
+                        for (int x = 0; x < NK; ++x) s[x] = Op::mma(q, k[x][kk], s[x]);
+                    }
+                };
+                auto add = [&](int r0, const f32x16_t (&s)[NK], auto MASKED) __attribute__((always_inline)) {
+                    f32x4_t l2[4];
 #pragma unroll
-                for (int i4 = 0; i4 < 4; ++i4) {
-                    l2[i4] = *reinterpret_cast<const f32x4_t*>(sl + 8 * i4 + 4 * half);
+                    for (int i4 = 0; i4 < 4; ++i4) {
+                        l2[i4] = *reinterpret_cast<const f32x4_t*>(sl + r0 + 8 * i4 + 4 * half);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) l2[i4][e] *= kLog2e;
-                }
-                auto add = [&](auto MASKED) __attribute__((always_inline)) {
+                        for (int e = 0; e < 4; ++e) l2[i4][e] *= kLog2e;
+                    }
 #pragma unroll
                     for (int x = 0; x < NK; ++x) {
                         float p[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const int row = t * BN + 8 * (i >> 2) + 4 * half + (i & 3);
+                            const int row = t * BN + r0 + 8 * (i >> 2) + 4 * half + (i & 3);
                             p[i] = __builtin_amdgcn_exp2f(fmaf(s[x][i], c, -l2[i >> 2][i & 3]));
                             if (MASKED && !(row >= wkey + 32 * x + (lane & 31) && row >= first && row < len)) p[i] = 0.f;
                         }
@@ -126,10 +130,20 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
                         sum[x] = z;
                     }
                 };
-                if (t * BN < wkey + kKeys - 1 || t * BN < first || t * BN + BN > len)
-                    add(std::true_type{});
-                else
-                    add(std::false_type{});
+                if (t * BN < wkey + kKeys - 1 || t * BN < first || t * BN + BN > len) {
+#pragma unroll 1
+                    for (int r0 = 0; r0 < BN; r0 += 32) {
+                        f32x16_t s[NK];
+                        scores(r0, s);
+                        add(r0, s, std::true_type{});
+                    }
+                } else {
+                    f32x16_t s0[NK], s1[NK];
+                    scores(0, s0);
+                    scores(32, s1);
+                    add(0, s0, std::false_type{});
+                    add(32, s1, std::false_type{});
+                }
             }
             hh = nh;
             t = nt;
@@ -140,8 +154,30 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
     for (int x = 0; x < NK; ++x) {
         const int kj = wkey + 32 * x + (lane & 31);
         const float y = half_sum(sum[x]);
-        if (half == 0 && kj < wa.width) out[kj] = kj < len ? y : 0.f;
+        if (half != 0) continue;
+        if (wa.parts > 1) {
+            if (kj < len) wa.part[(static_cast<size_t>(blockIdx.y) * a.Hkv + g) * a.T_tot + beg + kj] = y;
+        } else if (kj < wa.width) {
+            wa.weights[(static_cast<size_t>(n) * a.Hkv + g) * wa.width + kj] = kj < len ? y : 0.f;
+        }
     }
+}
+
+// The parts' sums, in their order; zero behind a sequence.
+__global__ __launch_bounds__(256) void attn_weights_join_kernel(WeightsArgs wa) {
+    const AttnArgs& a = wa.f;
+    const int g = blockIdx.x % a.Hkv, n = blockIdx.x / a.Hkv % a.N;
+    const int j = static_cast<int>(blockIdx.x / a.Hkv / a.N) * kBK + threadIdx.x;
+    if (j >= wa.width) return;
+    const int2 bl = seq_bounds(a.cu_seqlens, n, a.T_tot);
+    float y = 0.f;
+    if (j < bl.y) {
+        const float* p = wa.part + static_cast<size_t>(g) * a.T_tot + bl.x + j;
+        const size_t step = static_cast<size_t>(a.Hkv) * a.T_tot;
+#pragma unroll 4
+        for (int x = 0; x < wa.parts; ++x) y += p[x * step];
+    }
+    wa.weights[(static_cast<size_t>(n) * a.Hkv + g) * wa.width + j] = y;
 }
 
 namespace {
@@ -150,8 +186,11 @@ template <bool BF16, int DK>
 hipError_t launch(const WeightsArgs& w) {
     const AttnArgs& a = w.f;
     const unsigned blocks = static_cast<unsigned>((w.width + kBK - 1) / kBK) * a.N * a.Hkv;
-    hipLaunchKernelGGL((attn_weights_kernel<BF16, DK>), dim3(blocks), dim3(64 * kWaves), 0, static_cast<hipStream_t>(a.stream), w,
-                       a.scale * kLog2e);
+    const hipStream_t st = static_cast<hipStream_t>(a.stream);
+    hipLaunchKernelGGL((attn_weights_kernel<BF16, DK>), dim3(blocks, w.parts), dim3(64 * kWaves), 0, st, w, a.scale * kLog2e);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || w.parts == 1) return e;
+    hipLaunchKernelGGL(attn_weights_join_kernel, dim3(blocks), dim3(256), 0, st, w);
     return hipGetLastError();
 }
 
@@ -165,6 +204,17 @@ hipError_t launch_dk(const WeightsArgs& w) {
 }
 
 }  // namespace
+
+// Parts that the rows of a block of keys go to.  The first keys of a long sequence have all its rows: one
+// workgroup's chain of them is longer than the whole launch should take, and few blocks leave compute
+// units idle.
+int32_t attn_weights_parts(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t rows, int cus) {
+    const int64_t blocks = (T_tot / kBK + N) * Hkv;
+    const int64_t steps = (Hq / Hkv) * (((rows < T_tot ? rows : T_tot) + 63) / 64);  // of the longest chain, at most
+    int64_t parts = (24 * static_cast<int64_t>(cus) + blocks - 1) / blocks;
+    if (parts > steps / 8) parts = steps / 8;
+    return static_cast<int32_t>(parts < 1 ? 1 : parts > 64 ? 64 : parts);
+}
 
 hipError_t launch_attn_weights(const WeightsArgs& w) { return w.f.bf16 ? launch_dk<true>(w) : launch_dk<false>(w); }
 

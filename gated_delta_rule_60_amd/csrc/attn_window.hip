@@ -46,7 +46,7 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
     const int group = a.Hq / a.Hkv;
     const int g = hp % a.Hkv, h = g * group + hp / a.Hkv;
     SeqTile st;
-    if (!find_tile<kBM>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hq, false, st)) return;
+    if (!find_window_tile<kBM>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hq, st)) return;
 
     const int row0 = st.tile * kBM;
     const int wrow = row0 + 32 * wave;   // the wave's first row
@@ -81,31 +81,39 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
     };
 
     f32x16_t o[VT::ND];
-#pragma unroll
-    for (int dt = 0; dt < VT::ND; ++dt) o[dt] = f32x16_t{};
-    float mc = kLowest;  // running maximum of c s
-    float l = 0.f;       // this half-wave's part of the row's sum
+    float mc, l;  // running maximum of c s, and this half-wave's part of the row's sum
 
     auto scores = [&](int u, f32x16_t (&s)[NS]) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = 0; n < NS; ++n) s[n] = KT::rows_times(f32x16_t{}, lds[u & 1], kat, 32 * n, q);
     };
-    // One tile's scores into the row's statistics and O.  MASKED: some row may not see some key of the
-    // tile; otherwise the next tile's scores go to `s1`, between the two dependent halves of the step.
-    auto step = [&](int u, f32x16_t (&s)[NS], f32x16_t (&s1)[NS], auto MASKED) __attribute__((always_inline)) {
+    // One tile's scores into the row's statistics and O.  kPlain: every row sees every key of it, and the
+    // next tile's scores go to `s1`, between the two dependent halves of the step.  kCareful: values
+    // behind the mask may be infinite or NaN, which a weight of zero does not keep out.
+    enum { kPlain, kMasked, kCareful };
+    auto step = [&](int u, f32x16_t (&s)[NS], f32x16_t (&s1)[NS], auto kind) __attribute__((always_inline)) {
         const char* vt = lds[u & 1] + KB;
         const int key0 = list.tile(u) * BN;
         auto cols = vat;
-        if constexpr (MASKED) {
+        if constexpr (kind != kPlain) {
             // what is worked out from them stays in here: kept over the loop it would be spilled
             asm volatile("" : "+v"(cols.v[0]), "+v"(cols.v[1]));
+            const int at = key0 + 4 * half;  // of the lane's first score
+            if (key0 + BN - 1 > wrow) {
 #pragma unroll
-            for (int n = 0; n < NS; ++n)
+                for (int n = 0; n < NS; ++n)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = key0 + 32 * n + 8 * (i >> 2) + 4 * half + (i & 3);
-                    s[n][i] = window_sees(w, qi, key) ? s[n][i] : -INFINITY;
-                }
+                    for (int i = 0; i < 16; ++i) s[n][i] = 32 * n + 8 * (i >> 2) + (i & 3) <= qi - at ? s[n][i] : -INFINITY;
+            }
+            if (key0 < rows.all_lo) {
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int x = 32 * n + 8 * (i >> 2) + (i & 3);
+                        s[n][i] = x > qi - w.window - at || x < w.sinks - at ? s[n][i] : -INFINITY;
+                    }
+            }
         }
         float mx = s[0][0];
 #pragma unroll
@@ -123,7 +131,7 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[dt][i] *= r;
         }
-        if constexpr (!MASKED) scores(u + 1, s1);
+        if constexpr (kind == kPlain) scores(u + 1, s1);
         ColOp<BF16> p[NS];
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
@@ -134,8 +142,7 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
             }
             p[n].set(s[n]);
         }
-        // a weight of zero does not keep out an infinity or NaN behind the mask
-        if (MASKED && VT::template any_nonfinite<BN>(vt, lane)) {
+        if (kind == kCareful && VT::template any_nonfinite<BN>(vt, lane)) {
 #pragma unroll
             for (int dt = 0; dt < VT::ND; ++dt)
 #pragma unroll
@@ -160,30 +167,48 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
     };
     // a tile that all rows see all of, before another that the wave works on
     auto plain = [&](int u) __attribute__((always_inline)) { return active(u) && rows.sees_all(list.tile(u)) && active(u + 1); };
-    stage_k(0);
-    stage_v(0);
-    loads_done();
-    lds_ready();
-    if (1 < tiles) stage_k(1);
     f32x16_t sa[NS], sb[NS];
-    if (active(0)) scores(0, sa);
-    // sa holds the scores of tile u, if the wave works on it.  Masked tiles, a few a row at either end,
-    // are taken one by one, with their scores not ahead; the run of plain ones between them in pairs.
-    // In loops of their own: what the masked ones need would take registers from the pairs.
-    auto alone = [&](int u) __attribute__((always_inline)) {
-        next(u);
-        if (active(u)) step(u, sa, sb, std::true_type{});
-        if (active(u + 1)) scores(u + 1, sa);
+    // The walk over the tiles.  sa holds the scores of tile u, if the wave works on it.  Masked tiles, a
+    // few a row at either end, are taken one by one, with their scores not ahead; the run of plain ones
+    // between them in pairs.  In loops of their own: what the masked ones need would take registers from
+    // the pairs.
+    auto walk = [&](auto careful) __attribute__((always_inline)) {
+#pragma unroll
+        for (int dt = 0; dt < VT::ND; ++dt) o[dt] = f32x16_t{};
+        mc = kLowest;
+        l = 0.f;
+        auto alone = [&](int u) __attribute__((always_inline)) {
+            next(u);
+            if (active(u)) step(u, sa, sb, std::integral_constant<int, careful ? kCareful : kMasked>{});
+            if (active(u + 1)) scores(u + 1, sa);
+        };
+        stage_k(0);
+        stage_v(0);
+        loads_done();
+        lds_ready();
+        if (1 < tiles) stage_k(1);
+        if (active(0)) scores(0, sa);
+        int u = 0;
+        if constexpr (!careful) {
+            for (; u < tiles && !(plain(u) && plain(u + 1) && u >= list.head); ++u) alone(u);
+            for (; plain(u) && plain(u + 1); u += 2) {
+                next(u);
+                step(u, sa, sb, std::integral_constant<int, kPlain>{});
+                next(u + 1);
+                step(u + 1, sb, sa, std::integral_constant<int, kPlain>{});
+            }
+        }
+        for (; u < tiles; ++u) alone(u);
     };
-    int u = 0;
-    for (; u < tiles && !(plain(u) && plain(u + 1) && u >= list.head); ++u) alone(u);
-    for (; plain(u) && plain(u + 1); u += 2) {
-        next(u);
-        step(u, sa, sb, std::false_type{});
-        next(u + 1);
-        step(u + 1, sb, sa, std::false_type{});
-    }
-    for (; u < tiles; ++u) alone(u);
+    walk(std::false_type{});
+    // An infinity or NaN behind the mask has made its column NaN: the walk once more, looking through the
+    // values.  (Looked through at every masked tile they cost a third of the vector work.)
+    float zero = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < VT::ND; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) zero = fmaf(o[dt][i], 0.f, zero);
+    if (__syncthreads_or(zero != 0.f)) walk(std::true_type{});
 
     l = half_sum(l);
     if (a.lse && live && half == 0) a.lse[tok * a.Hq + h] = (mc + log2f(l)) * kLn2;

@@ -11,6 +11,30 @@ __device__ __forceinline__ bool window_sees(const WindowArgs& w, int row, int ke
     return key <= row && (row - key < w.window || key < w.sinks);
 }
 
+// Piece number p of the batch, in the sequences' order, as find_tile past 64 sequences: behind the first
+// window's rows all pieces have the same work, and one round of sums is all it takes.
+template <int BM>
+__device__ __forceinline__ bool find_window_tile(const int32_t* cu, int N, int T_tot, int p, SeqTile& s) {
+    const int lane = threadIdx.x & 63;
+    for (int n0 = 0; n0 < N; n0 += 64) {
+        int2 bl = make_int2(0, 0);
+        if (n0 + lane < N) bl = seq_bounds(cu, n0 + lane, T_tot);
+        const int nt = (bl.y + BM - 1) / BM;
+        const int incl = wave_scan(nt);
+        const int total = __builtin_amdgcn_readlane(incl, 63);
+        if (p < total) {
+            const int n = __builtin_ctzll(__ballot(incl > p));
+            s.beg = __builtin_amdgcn_readlane(bl.x, n);
+            s.len = __builtin_amdgcn_readlane(bl.y, n);
+            s.tile = p - (__builtin_amdgcn_readlane(incl, n) - __builtin_amdgcn_readlane(nt, n));
+            s.n = n0 + n;
+            return true;
+        }
+        p -= total;
+    }
+    return false;
+}
+
 // The tiles of BN keys that a block of rows [row0, end) walks: those of the
 // sinks that lie before the first row's window, then from that window to the
 // diagonal.

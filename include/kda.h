@@ -540,13 +540,21 @@ size_t attn_window_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int
  *              out.  With width = max_pages * page_size, what kv_evict and
  *              attn_weighed_decode take for one layer.
  *   width      in [1, 2^30], with ceil(width / 256) * N * H_kv < 2^24
+ *   workspace  at least attn_prefill_weights_workspace_size bytes (NULL if 0),
+ *              256-byte aligned, used until the queued work ends
  * Sums are fp32, in one order: the same inputs give the same bits.
  */
 kda_status attn_prefill_weights(const void* q, const void* k, const float* lse,
                                 const int32_t* cu_seqlens, int32_t N, int64_t T_tot, int32_t H_q,
                                 int32_t H_kv, int32_t d_k, int64_t q_stride, int64_t k_stride,
                                 int32_t rows, float scale, kda_dtype dtype, float* weights,
-                                int32_t width, void* stream);
+                                int32_t width, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Workspace bytes attn_prefill_weights needs on the current device (0 for
+ * unsupported sizes): the sums of the parts that the rows are given to. */
+size_t attn_prefill_weights_workspace_size(int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv,
+                                           int32_t rows);
 
 /*
  * A paged cache holds the keys and values of many sequences of growing

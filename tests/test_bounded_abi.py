@@ -144,7 +144,7 @@ def test_decode_workspaces():
 
 def _weights(**kw):
     a = dict(q=FAKE, k=FAKE, lse=FAKE, cu_seqlens=FAKE, N=1, T_tot=64, H_q=4, H_kv=2, d_k=64, q_stride=256, k_stride=128, rows=32,
-             scale=0.125, dtype=BF16, weights=FAKE, width=64, stream=None)
+             scale=0.125, dtype=BF16, weights=FAKE, width=64, workspace=FAKE, workspace_bytes=1 << 40, stream=None)
     a.update(kw)
     return kda.attn_prefill_weights(**a)
 
@@ -158,10 +158,21 @@ def _weights(**kw):
     (dict(weights=None), BAD, "weights"),
     (dict(weights=FAKE + 2), BAD, "weights"),
     (dict(width=1 << 30, N=2, H_q=4, H_kv=2), BAD, "ceil(width / 256)"),
+    (dict(T_tot=2000, rows=2000, workspace=None), BAD, "workspace must not be NULL"),
+    (dict(T_tot=2000, rows=2000, workspace=FAKE + 16), BAD, "256-byte aligned"),
+    (dict(T_tot=2000, rows=2000, workspace_bytes=2000 * 2 * 4), BAD, "workspace smaller"),
 ])
 def test_prefill_weights_refuses(kw, status, needle):
     assert _weights(**kw) == status
     assert needle in kda.kda_last_error()
+
+
+def test_prefill_weights_workspace():
+    size = kda.attn_prefill_weights_workspace_size
+    assert size(1, 300, 2, 2, 32) == 0  # a few rows: one part
+    assert size(1, 4000, 8, 2, 4000) >= 2 * 2 * 4000 * 4
+    for kw in ((0, 10, 1, 1, 5), (1, -1, 1, 1, 5), (1, 10, 3, 2, 5), (1, 10, 1, 1, 0)):
+        assert size(*kw) == 0
 
 
 def _evict(**kw):

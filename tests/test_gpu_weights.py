@@ -333,10 +333,14 @@ def test_prompt_offsets_past_32_bits():
     lse = torch.full((t, 2), 5.0, device="cuda")
     cu = torch.tensor([0, 32800, 33000], dtype=torch.int32).cuda()
     w = kda.attn_prefill_weights_t(q, k, lse, cu, weights=torch.empty(2, 1, 256, device="cuda"))
-    alone = kda.attn_prefill_weights_t(q[32800:].contiguous(), k[32800:].contiguous(), lse[32800:].contiguous(),
-                                       weights=torch.empty(1, 1, 256, device="cuda"))
     torch.cuda.synchronize()
-    assert torch.equal(w[1], alone[0])
+    value, bound = torch.zeros(1, 256, dtype=torch.float64), torch.zeros(1, 256, dtype=torch.float64)
+    for h in range(2):
+        x, y = weights_of(q[32800:, h].cpu().double(), k[32800:, 0].cpu().double(), torch.ones(200, 200, dtype=torch.bool).tril(),
+                          1 / math.sqrt(128), lse[32800:, h].cpu().double())
+        value[0, :200] += x
+        bound[0, :200] += y + 2 * E24 * x
+    attn_ref.check(w[1], (value, bound), "weights")
 
 
 def test_prompt_refusals():
