@@ -229,10 +229,14 @@ def _prefill_weights_on(q, k, lse, cu_seqlens, weights, rows, scale, workspace, 
     width = weights.shape[2]
     _need(weights, "weights", (N, Hkv, width), torch.float32, dev)
     rows = max(T, 1) if rows is None else rows
-    ws = _workspace(workspace, attn_prefill_weights_workspace_size(N, T, Hq, Hkv, rows), dev)
+    need = attn_prefill_weights_workspace_size(N, T, Hq, Hkv, rows)
+    ws, size = None, 0  # few rows need none
+    if need or workspace is not None:
+        buf = _workspace(workspace, need, dev)
+        ws, size = buf.data_ptr(), buf.numel()
     _check(attn_prefill_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(), N, T, Hq, Hkv, dk,
-                                strides[0], strides[1], rows, _scale(scale, dk), code, weights.data_ptr(), width, ws.data_ptr(),
-                                ws.numel(), stream))
+                                strides[0], strides[1], rows, _scale(scale, dk), code, weights.data_ptr(), width, ws, size,
+                                stream))
     return weights
 
 

@@ -157,6 +157,8 @@ kda_status check_window(int32_t window, int32_t sinks) {
     return KDA_OK;
 }
 
+int32_t window_heads(int32_t group) { return group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1; }
+
 }  // namespace
 
 extern "C" {
@@ -173,7 +175,7 @@ kda_status attn_window_prefill(const void* q, const void* k, const void* v, cons
                           scale, dtype == KDA_DTYPE_BF16, o, lse, stream,
                           kda::attn_split(N, T_tot, H_q, dtype == KDA_DTYPE_BF16, kda::device_cus_or_default())};
     (void)hipGetLastError();  // report only this launch's status
-    const hipError_t e = kda::launch_attn_window({a, window, sinks});
+    const hipError_t e = kda::launch_attn_window({a, window, sinks, window_heads(H_q / H_kv)});
     return e == hipSuccess ? KDA_OK : hip_fail(e, "windowed attention kernel launch");
 }
 

@@ -54,6 +54,7 @@ struct WindowArgs {
     AttnArgs f;
     int32_t window;  // in [1, 2^30]
     int32_t sinks;   // in [0, kMaxSinks]
+    int32_t heads;   // query heads of one key head in a workgroup's four waves: 1, 2 or 4
 };
 constexpr int32_t kMaxSinks = 256;
 

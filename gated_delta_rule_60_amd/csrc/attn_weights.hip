@@ -44,8 +44,9 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = a.Hq / a.Hkv;
     // the first keys have the most rows: their workgroups come first, over all sequences
-    const int g = blockIdx.x % a.Hkv, n = blockIdx.x / a.Hkv % a.N;
-    const int key0 = static_cast<int>(blockIdx.x / a.Hkv / a.N) * kBK, wkey = key0 + kKeys * wave;
+    const int KBn = (wa.width + kBK - 1) / kBK;
+    const int g = blockIdx.x % a.Hkv, n = blockIdx.x / a.Hkv / KBn;
+    const int key0 = static_cast<int>(blockIdx.x / a.Hkv % KBn) * kBK, wkey = key0 + kKeys * wave;
     const int2 bl = seq_bounds(a.cu_seqlens, n, a.T_tot);
     const int beg = bl.x, len = bl.y;
     if (wa.parts > 1 && key0 >= len) return;

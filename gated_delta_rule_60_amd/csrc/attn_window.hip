@@ -42,14 +42,16 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
     const AttnArgs& a = w.f;
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int hp = blockIdx.x % a.Hq;  // consecutive workgroups, consecutive key heads: as in attn_prefill.hip
-    const int group = a.Hq / a.Hkv;
-    const int g = hp % a.Hkv, h = g * group + hp / a.Hkv;
+    // The waves are w.heads query heads of one key head by 4 / w.heads blocks of 32 rows.  Consecutive
+    // workgroups take consecutive key heads: as in attn_prefill.hip.
+    const int sets = a.Hq / w.heads, hp = blockIdx.x % sets;
+    const int g = hp % a.Hkv, h = g * (a.Hq / a.Hkv) + hp / a.Hkv * w.heads + wave % w.heads;
+    const int span = kBM / w.heads;  // rows of the workgroup
     SeqTile st;
-    if (!find_window_tile<kBM>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hq, st)) return;
+    if (!find_window_tile(a.cu_seqlens, a.N, a.T_tot, span, blockIdx.x / sets, st)) return;
 
-    const int row0 = st.tile * kBM;
-    const int wrow = row0 + 32 * wave;   // the wave's first row
+    const int row0 = st.tile * span;
+    const int wrow = row0 + 32 * (wave / w.heads);   // the wave's first row
     const int qi = wrow + (lane & 31);   // the lane's query row in its sequence
     const bool live = qi < st.len;
     const size_t tok = static_cast<size_t>(st.beg) + (live ? qi : 0);
@@ -65,7 +67,7 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
     const int kat = KT::row_at(lane);
     const auto vat = VT::col_at(lane);
 
-    const WindowTiles<BN> list(w, row0, st.len < row0 + kBM ? st.len : row0 + kBM);
+    const WindowTiles<BN> list(w, row0, st.len - row0 < span ? st.len : row0 + span);
     const WindowRows<BN> rows(w, wrow, 32);
     // the wave's last tile in the list, and whether it works on tile u of it
     const int upto = wrow < st.len ? list.number(wrow / BN) : -1;
@@ -87,18 +89,19 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
 #pragma unroll
         for (int n = 0; n < NS; ++n) s[n] = KT::rows_times(f32x16_t{}, lds[u & 1], kat, 32 * n, q);
     };
-    // One tile's scores into the row's statistics and O.  kPlain: every row sees every key of it, and the
-    // next tile's scores go to `s1`, between the two dependent halves of the step.  kCareful: values
-    // behind the mask may be infinite or NaN, which a weight of zero does not keep out.
-    enum { kPlain, kMasked, kCareful };
+    // One tile's scores into the row's statistics and O.  kAhead: the next tile's scores go to `s1`,
+    // between the two dependent halves of the step.  kCareful: values behind the mask may be infinite or
+    // NaN, which a weight of zero does not keep out.
+    enum { kAhead, kAlone, kCareful };
     auto step = [&](int u, f32x16_t (&s)[NS], f32x16_t (&s1)[NS], auto kind) __attribute__((always_inline)) {
         const char* vt = lds[u & 1] + KB;
         const int key0 = list.tile(u) * BN;
         auto cols = vat;
-        if constexpr (kind != kPlain) {
-            // what is worked out from them stays in here: kept over the loop it would be spilled
-            asm volatile("" : "+v"(cols.v[0]), "+v"(cols.v[1]));
-            const int at = key0 + 4 * half;  // of the lane's first score
+        // what is worked out from them stays in here: kept over the loop it would be spilled
+        if constexpr (kind != kAhead) asm volatile("" : "+v"(cols.v[0]), "+v"(cols.v[1]));
+        if (!rows.sees_all(list.tile(u))) {
+            int at = key0 + 4 * half;  // of the lane's first score
+            asm volatile("" : "+v"(at));
             if (key0 + BN - 1 > wrow) {
 #pragma unroll
                 for (int n = 0; n < NS; ++n)
@@ -131,7 +134,7 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[dt][i] *= r;
         }
-        if constexpr (kind == kPlain) scores(u + 1, s1);
+        if constexpr (kind == kAhead) scores(u + 1, s1);
         ColOp<BF16> p[NS];
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
@@ -165,13 +168,9 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
         if (u + 2 < tiles) stage_k(u + 2);
         if (u + 1 < tiles) stage_v(u + 1);
     };
-    // a tile that all rows see all of, before another that the wave works on
-    auto plain = [&](int u) __attribute__((always_inline)) { return active(u) && rows.sees_all(list.tile(u)) && active(u + 1); };
     f32x16_t sa[NS], sb[NS];
-    // The walk over the tiles.  sa holds the scores of tile u, if the wave works on it.  Masked tiles, a
-    // few a row at either end, are taken one by one, with their scores not ahead; the run of plain ones
-    // between them in pairs.  In loops of their own: what the masked ones need would take registers from
-    // the pairs.
+    // The walk over the tiles.  sa holds the scores of tile u, if the wave works on it.  Tiles before two
+    // others that it works on go in pairs, the last ones and those before a gap one by one.
     auto walk = [&](auto careful) __attribute__((always_inline)) {
 #pragma unroll
         for (int dt = 0; dt < VT::ND; ++dt) o[dt] = f32x16_t{};
@@ -179,9 +178,10 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
         l = 0.f;
         auto alone = [&](int u) __attribute__((always_inline)) {
             next(u);
-            if (active(u)) step(u, sa, sb, std::integral_constant<int, careful ? kCareful : kMasked>{});
+            if (active(u)) step(u, sa, sb, std::integral_constant<int, careful ? kCareful : kAlone>{});
             if (active(u + 1)) scores(u + 1, sa);
         };
+        auto paired = [&](int u) __attribute__((always_inline)) { return active(u) && active(u + 1) && active(u + 2); };
         stage_k(0);
         stage_v(0);
         loads_done();
@@ -190,12 +190,12 @@ __global__ __launch_bounds__(256, 2) void attn_window_kernel(WindowArgs w, float
         if (active(0)) scores(0, sa);
         int u = 0;
         if constexpr (!careful) {
-            for (; u < tiles && !(plain(u) && plain(u + 1) && u >= list.head); ++u) alone(u);
-            for (; plain(u) && plain(u + 1); u += 2) {
+            for (; u < tiles && !paired(u); ++u) alone(u);
+            for (; paired(u); u += 2) {
                 next(u);
-                step(u, sa, sb, std::integral_constant<int, kPlain>{});
+                step(u, sa, sb, std::integral_constant<int, kAhead>{});
                 next(u + 1);
-                step(u + 1, sb, sa, std::integral_constant<int, kPlain>{});
+                step(u + 1, sb, sa, std::integral_constant<int, kAhead>{});
             }
         }
         for (; u < tiles; ++u) alone(u);
@@ -367,9 +367,9 @@ hipError_t launch(const WindowArgs& w) {
                            st, w, a.scale * kLog2e);
         return hipGetLastError();
     }
-    const int64_t units = (static_cast<int64_t>(a.T_tot) + kBM - 1) / kBM + a.N;
-    hipLaunchKernelGGL((attn_window_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hq)), dim3(64 * kWaves), 0, st, w,
-                       a.scale * kLog2e);
+    const int64_t span = kBM / w.heads, units = (static_cast<int64_t>(a.T_tot) + span - 1) / span + a.N;
+    hipLaunchKernelGGL((attn_window_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * (a.Hq / w.heads))), dim3(64 * kWaves), 0,
+                       st, w, a.scale * kLog2e);
     return hipGetLastError();
 }
 

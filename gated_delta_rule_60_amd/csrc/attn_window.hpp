@@ -13,8 +13,7 @@ __device__ __forceinline__ bool window_sees(const WindowArgs& w, int row, int ke
 
 // Piece number p of the batch, in the sequences' order, as find_tile past 64 sequences: behind the first
 // window's rows all pieces have the same work, and one round of sums is all it takes.
-template <int BM>
-__device__ __forceinline__ bool find_window_tile(const int32_t* cu, int N, int T_tot, int p, SeqTile& s) {
+__device__ __forceinline__ bool find_window_tile(const int32_t* cu, int N, int T_tot, int BM, int p, SeqTile& s) {
     const int lane = threadIdx.x & 63;
     for (int n0 = 0; n0 < N; n0 += 64) {
         int2 bl = make_int2(0, 0);

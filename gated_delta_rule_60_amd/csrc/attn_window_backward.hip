@@ -31,7 +31,7 @@ struct Stats {
     float* D;
 };
 
-__device__ __forceinline__ WindowArgs window_of(const WindowBwdArgs& w) { return {w.b.f, w.window, w.sinks}; }
+__device__ __forceinline__ WindowArgs window_of(const WindowBwdArgs& w) { return {w.b.f, w.window, w.sinks, 1}; }
 
 // Rows past the first key's window of a sequence, in pieces of w.rows: the number of pieces.
 __device__ __forceinline__ int sink_pieces(const WindowBwdArgs& w, int len) {
