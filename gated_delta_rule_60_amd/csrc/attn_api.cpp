@@ -222,7 +222,8 @@ kda_status attn_window_prefill_backward(const void* q, const void* k, const void
     (void)hipGetLastError();  // report only this launch's status
     const hipError_t e = kda::launch_attn_window_bwd({{a, d_o, d_q, d_k_out, d_v_out, workspace, parts, plan.head_parts},
                                                       static_cast<int32_t>(window < T_tot ? window : T_tot), sinks, plan.rows,
-                                                      plan.blocks, static_cast<int32_t>(plan.pieces), sink_parts, band_parts},
+                                                      plan.blocks, static_cast<int32_t>(plan.pieces), window_heads(H_q / H_kv), sink_parts,
+                                                      band_parts},
                                                      plan);
     return e == hipSuccess ? KDA_OK : hip_fail(e, "windowed attention backward kernel launch");
 }

@@ -31,7 +31,7 @@ struct Stats {
     float* D;
 };
 
-__device__ __forceinline__ WindowArgs window_of(const WindowBwdArgs& w) { return {w.b.f, w.window, w.sinks, 1}; }
+__device__ __forceinline__ WindowArgs window_of(const WindowBwdArgs& w) { return {w.b.f, w.window, w.sinks, w.heads}; }
 
 // Rows past the first key's window of a sequence, in pieces of w.rows: the number of pieces.
 __device__ __forceinline__ int sink_pieces(const WindowBwdArgs& w, int len) {
@@ -55,14 +55,15 @@ __global__ __launch_bounds__(256, BF16 || DK < 128 ? 2 : 1) void attn_window_dq_
     const WindowArgs w = window_of(wb);
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int hp = blockIdx.x % a.Hq;
-    const int group = a.Hq / a.Hkv;
-    const int g = hp % a.Hkv, h = g * group + hp / a.Hkv;
+    // waves on heads and blocks of rows as in attn_window.hip
+    const int sets = a.Hq / w.heads, hp = blockIdx.x % sets;
+    const int g = hp % a.Hkv, h = g * (a.Hq / a.Hkv) + hp / a.Hkv * w.heads + wave % w.heads;
+    const int span = kBM / w.heads;
     SeqTile st;
-    if (!find_tile<kBM>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hq, false, st)) return;
+    if (!find_window_tile(a.cu_seqlens, a.N, a.T_tot, span, blockIdx.x / sets, st)) return;
 
-    const int row0 = st.tile * kBM;
-    const int wrow = row0 + 32 * wave;
+    const int row0 = st.tile * span;
+    const int wrow = row0 + 32 * (wave / w.heads);
     const int qi = wrow + (lane & 31);
     const bool live = qi < st.len;
     const size_t tok = static_cast<size_t>(st.beg) + (live ? qi : 0);
@@ -88,7 +89,7 @@ __global__ __launch_bounds__(256, BF16 || DK < 128 ? 2 : 1) void attn_window_dq_
     const int kat = KT::row_at(lane), vat = VT::row_at(lane);
     const auto kct = KT::col_at(lane);
 
-    const WindowTiles<BN> list(w, row0, st.len < row0 + kBM ? st.len : row0 + kBM);
+    const WindowTiles<BN> list(w, row0, st.len - row0 < span ? st.len : row0 + span);
     const WindowRows<BN> rows(w, wrow, 32);
     const int upto = wrow < st.len ? list.number(wrow / BN) : -1;  // the wave's last tile in the list
 
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(256, BF16 || DK < 128 ? 2 : 1) void attn_window_dq_
 
     // Rows with few keys take D from their weights, not from the rounded o (attn_backward.hip): the
     // same walk over the keys, a few tiles.
-    if (BF16 && (st.tile == 0 || w.window + w.sinks <= kBM)) {
+    if (BF16 && (row0 < kBM || w.window + w.sinks <= kBM)) {
         float sum = 0.f;
         stage_tile(0);
         loads_done();
@@ -151,9 +152,18 @@ __global__ __launch_bounds__(256, BF16 || DK < 128 ? 2 : 1) void attn_window_dq_
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse2)) * (dp[i] - D);
             if (masked) {
+                const int at = t * BN + 32 * n + 4 * half;  // of the lane's first key
+                if (t * BN + BN - 1 > wrow) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[i] = window_sees(w, qi, t * BN + 32 * n + 8 * (i >> 2) + 4 * half + (i & 3)) ? s[i] : 0.f;
+                    for (int i = 0; i < 16; ++i) s[i] = 8 * (i >> 2) + (i & 3) <= qi - at ? s[i] : 0.f;
+                }
+                if (t * BN < rows.all_lo) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int x = 8 * (i >> 2) + (i & 3);
+                        s[i] = x > qi - w.window - at || x < w.sinks - at ? s[i] : 0.f;
+                    }
+                }
             }
             ColOp<BF16> ds;
             ds.set(s);
@@ -621,28 +631,26 @@ __global__ __launch_bounds__(256) void attn_window_join_kernel(WindowBwdArgs wb)
         pieces = sink_pieces(wb, st.len);
         if (first + pieces > wb.pieces) pieces = first < wb.pieces ? wb.pieces - first : 0;  // offsets that overlap: no more
     }
-    constexpr int W = DK + DV, Q = W / 4;
+    constexpr int W = DK + DV, Q = W / 4;  // a thread has four elements of a row
     const size_t keys = 32 * static_cast<size_t>(wb.blocks);
-    for (int x = threadIdx.x; x < 32 * Q; x += 256) {
-        const int row = st.tile * 32 + x / Q, e = 4 * (x % Q);
-        if (row >= st.len) return;
-        const size_t at = (static_cast<size_t>(st.beg) + row) * a.Hkv + g;
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        auto add = [&](const float* p, int n, size_t step) __attribute__((always_inline)) {
-#pragma unroll 4
-            for (int s = 0; s < n; ++s) {
-                const f32x4_t z = *reinterpret_cast<const f32x4_t*>(p + s * step);
+    const int x = blockIdx.y * 256 + threadIdx.x, row = st.tile * 32 + x / Q, e = 4 * (x % Q);
+    if (row >= st.len) return;
+    const size_t at = (static_cast<size_t>(st.beg) + row) * a.Hkv + g;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](const float* p, int n, size_t step) __attribute__((always_inline)) {
+#pragma unroll 8
+        for (int s = 0; s < n; ++s) {
+            const f32x4_t z = *reinterpret_cast<const f32x4_t*>(p + s * step);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] += z[i];
-            }
-        };
-        if constexpr (WHOLE)
-            add(wb.band_parts + ((st.n * keys + row) * a.Hkv + g) * W + e, 1, 0);
-        else
-            add(b.parts + at * W + e, b.head_parts, static_cast<size_t>(a.T_tot) * a.Hkv * W);
-        add(wb.sink_parts + ((first * keys + row) * a.Hkv + g) * W + e, pieces, keys * a.Hkv * W);
-        T::store4(e < DK ? static_cast<typename T::G*>(b.d_k) + at * DK + e : static_cast<typename T::G*>(b.d_v) + at * DV + e - DK, y);
-    }
+            for (int i = 0; i < 4; ++i) y[i] += z[i];
+        }
+    };
+    if constexpr (WHOLE)
+        add(wb.band_parts + ((st.n * keys + row) * a.Hkv + g) * W + e, 1, 0);
+    else
+        add(b.parts + at * W + e, b.head_parts, static_cast<size_t>(a.T_tot) * a.Hkv * W);
+    add(wb.sink_parts + ((first * keys + row) * a.Hkv + g) * W + e, pieces, keys * a.Hkv * W);
+    T::store4(e < DK ? static_cast<typename T::G*>(b.d_k) + at * DK + e : static_cast<typename T::G*>(b.d_v) + at * DV + e - DK, y);
 }
 
 namespace {
@@ -660,8 +668,11 @@ hipError_t launch(const WindowBwdArgs& w, const WindowBwdPlan& plan) {
     const dim3 threads(64 * kWaves);
     if (a.split)
         hipLaunchKernelGGL((attn_window_dq_split_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units32 * a.Hq)), threads, 0, st, w, c, stats);
-    else
-        hipLaunchKernelGGL((attn_window_dq_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hq)), threads, 0, st, w, c, stats);
+    else {
+        const int64_t span = kBM / w.heads, pieces = (static_cast<int64_t>(a.T_tot) + span - 1) / span + a.N;
+        hipLaunchKernelGGL((attn_window_dq_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(pieces * (a.Hq / w.heads))), threads, 0, st, w, c,
+                           stats);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const bool whole = b.head_parts == 0;
@@ -680,9 +691,10 @@ hipError_t launch(const WindowBwdArgs& w, const WindowBwdPlan& plan) {
     }
     if (whole && w.blocks > 0)
         hipLaunchKernelGGL((attn_window_join_kernel<BF16, DK, DV, true>),
-                           dim3(static_cast<unsigned>(static_cast<int64_t>(a.N) * w.blocks * a.Hkv)), dim3(256), 0, st, w);
+                           dim3(static_cast<unsigned>(static_cast<int64_t>(a.N) * w.blocks * a.Hkv), (DK + DV) / 32), dim3(256), 0, st, w);
     else if (!whole && (b.head_parts > 1 || w.blocks > 0))
-        hipLaunchKernelGGL((attn_window_join_kernel<BF16, DK, DV, false>), dim3(static_cast<unsigned>(units32 * a.Hkv)), dim3(256), 0, st, w);
+        hipLaunchKernelGGL((attn_window_join_kernel<BF16, DK, DV, false>), dim3(static_cast<unsigned>(units32 * a.Hkv), (DK + DV) / 32),
+                           dim3(256), 0, st, w);
     return hipGetLastError();
 }
 
@@ -708,8 +720,8 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-// Pieces of rows: so long that their workgroups are about two for every compute unit, and at least one
-// group of 128 rows.
+// Pieces of rows: so long that their workgroups are about one for every compute unit (it holds no second
+// one), and at least one group of 128 rows.
 WindowBwdPlan attn_window_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t d_k, int32_t d_v, int32_t window,
                                    int32_t sinks, bool bf16, int cus) {
     const BwdPlan plain = attn_bwd_plan(N, T_tot, Hq, Hkv, d_k, d_v, bf16, cus);
@@ -720,7 +732,7 @@ WindowBwdPlan attn_window_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t
     if (sinks > 0 && window < T_tot) {
         const int64_t keys = sinks < T_tot ? sinks : T_tot;
         p.blocks = static_cast<int32_t>((keys + 31) / 32);
-        const int64_t rows = (T_tot * p.blocks * Hkv / (2 * static_cast<int64_t>(cus)) + 127) / 128 * 128;
+        const int64_t rows = (T_tot * p.blocks * Hkv / cus + 127) / 128 * 128;
         p.rows = static_cast<int32_t>(rows < 128 ? 128 : rows);
         p.pieces = (T_tot - window) / p.rows + N;
         p.parts_bytes = up256(static_cast<size_t>(p.pieces) * 32 * p.blocks * row);
