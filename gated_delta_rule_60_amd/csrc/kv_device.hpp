@@ -8,9 +8,10 @@ namespace kda {
 
 namespace {
 
-constexpr int kThreads = 1024;  // of such a workgroup: one per request
+constexpr int kThreads = 1024;  // of the bookkeeping workgroup: one per request
 
-// Inclusive prefix sum over the workgroup's threads; `total` in every thread.
+// Inclusive prefix sum over the workgroup's NT threads; `total` in every thread.
+template <int NT = kThreads>
 __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* s_wave, int64_t& total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -24,7 +25,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* s_wave, int64_
     int64_t before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) {
+    for (int w = 0; w < NT / 64; ++w) {
         const int64_t y = s_wave[w];
         if (w < wave) before += y;
         total += y;
@@ -33,13 +34,14 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* s_wave, int64_
 }
 
 // The same for sums that fit 32 bits, by lane moves instead of shuffles.
+template <int NT = kThreads>
 __device__ __forceinline__ int block_scan(int x, int* s_wave, int& total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     x = wave_scan(x);
     __syncthreads();
     if (lane == 63) s_wave[wave] = x;
     __syncthreads();
-    const int all = wave_scan(lane < kThreads / 64 ? s_wave[lane & (kThreads / 64 - 1)] : 0);
+    const int all = wave_scan(lane < NT / 64 ? s_wave[lane & (NT / 64 - 1)] : 0);
     total = __builtin_amdgcn_readlane(all, 63);
     return x + (wave ? __builtin_amdgcn_readlane(all, __builtin_amdgcn_readfirstlane(wave) - 1) : 0);
 }

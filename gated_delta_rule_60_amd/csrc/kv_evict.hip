@@ -22,6 +22,8 @@
 // behind the budget back.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "attn_device.hpp"
 #include "attn_launch.hpp"
 #include "kv_device.hpp"
@@ -31,8 +33,9 @@ namespace kda {
 namespace {
 
 constexpr int kBins = 2048;
+constexpr int kNT = 512;                 // threads of the workgroup that evicts
 constexpr int kPer = 4;                  // candidates a thread looks at in a turn
-constexpr int kTurn = kPer * kThreads;
+constexpr int kTurn = kPer * kNT;
 constexpr int kList = 2 * kTurn;         // places listed at a time: turns until one is full
 constexpr int kMoves = 8;                // 16-byte units of a thread in flight
 
@@ -49,7 +52,7 @@ __device__ __forceinline__ unsigned order_of(float w) {
 __device__ __forceinline__ int evict_request(const PageArgs& a, const int32_t* rows, int i, int& row, bool& good) {
     row = rows[i];
     int bad = 0;
-    for (int j = threadIdx.x; j < i; j += kThreads) bad |= rows[j] == row;
+    for (int j = threadIdx.x; j < i; j += kNT) bad |= rows[j] == row;
     good = row >= 0 && row < a.n_rows;
     int len = 0, held = 0;
     if (good) {
@@ -58,7 +61,7 @@ __device__ __forceinline__ int evict_request(const PageArgs& a, const int32_t* r
         good = len >= 0 && held >= 0 && held <= a.max_pages && len <= static_cast<int64_t>(held) << a.page_shift;
     }
     if (good)
-        for (int p = threadIdx.x; p < held; p += kThreads) {
+        for (int p = threadIdx.x; p < held; p += kNT) {
             const int page = a.table[static_cast<int64_t>(row) * a.max_pages + p];
             bad |= page < 0 || page >= a.n_pages || a.refs[page] != 1;
         }
@@ -66,9 +69,9 @@ __device__ __forceinline__ int evict_request(const PageArgs& a, const int32_t* r
     return good ? len : 0;
 }
 
-__global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArgs c, EvictArgs e, const int32_t* rows, int32_t* status) {
-    __shared__ int s_hist[kBins], s_wave[kThreads / 64], s_pick[2];
-    __shared__ int s_src[kList], s_dst[kList];  // the listed positions, from where to where
+__global__ __launch_bounds__(kNT) void kv_evict_kernel(PageArgs a, CacheArgs c, EvictArgs e, const int32_t* rows, int32_t* status) {
+    __shared__ int s_hist[kBins], s_wave[kNT / 64], s_pick[2];
+    __shared__ int s_src[kList], s_dst[kList];  // the listed positions, from where to where; then their places in the cache
     const int tid = threadIdx.x;
     const int g = blockIdx.x % e.Hkv, layer = blockIdx.x / e.Hkv % c.n_layers, i = blockIdx.x / e.Hkv / c.n_layers;
     int row;
@@ -79,7 +82,7 @@ __global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArg
 
     const int32_t* table = a.table + static_cast<int64_t>(row) * a.max_pages;
     auto token = [&](int pos) __attribute__((always_inline)) {
-        return (static_cast<int64_t>(table[pos >> a.page_shift]) << a.page_shift) + (pos & (a.page_size - 1));
+        return (table[pos >> a.page_shift] << a.page_shift) + (pos & (a.page_size - 1));
     };
     float* w = e.weights ? e.weights + ((static_cast<int64_t>(layer) * a.n_rows + row) * e.Hkv + g) * (static_cast<int64_t>(a.max_pages) << a.page_shift)
                          : nullptr;
@@ -92,31 +95,64 @@ __global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArg
     u32x4_t* const kc = static_cast<u32x4_t*>(c.k_cache) + layer * positions * c.k_row + g * ku;
     u32x4_t* const vc = static_cast<u32x4_t*>(c.v_cache) + layer * positions * c.v_row + g * vu;
 
+    // The first n listed moves: the places of their positions, then 16 bytes a lane.  ORDERED: all of a
+    // block is read before any of it is written.
+    auto places = [&](int n) __attribute__((always_inline)) {
+        for (int m = tid; m < n; m += kNT) {
+            s_src[m] = token(s_src[m]);
+            s_dst[m] = token(s_dst[m]);
+        }
+        __syncthreads();
+    };
+    auto move = [&](u32x4_t* cache, int units, int64_t step, int n, auto ORDERED) __attribute__((always_inline)) {
+        const int lg = __builtin_ctz(units), all = n << lg;
+        for (int x0 = 0; x0 < all; x0 += kNT * kMoves) {
+            u32x4_t y[kMoves];
+#pragma unroll
+            for (int b = 0; b < kMoves; ++b) {
+                const int x = x0 + b * kNT + tid;
+                if (x < all) y[b] = cache[s_src[x >> lg] * step + (x & (units - 1))];
+            }
+            if constexpr (ORDERED) {
+                loads_done();
+                __syncthreads();
+            }
+#pragma unroll
+            for (int b = 0; b < kMoves; ++b) {
+                const int x = x0 + b * kNT + tid;
+                if (x < all) cache[s_dst[x >> lg] * step + (x & (units - 1))] = y[b];
+            }
+        }
+    };
+
     if (choose > 0) {
         // the weight `least` that the choose-th heaviest has, and how many of exactly that are chosen
         unsigned least = 0, known = 0;  // digits found so far, and their bits
         int ties = choose;
         for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
             const unsigned bins = shift == 0 ? 1024 : kBins;
-            for (int b = tid; b < kBins; b += kThreads) s_hist[b] = 0;
+            for (int b = tid; b < kBins; b += kNT) s_hist[b] = 0;
             __syncthreads();
-            for (int p = from + tid; p < to; p += kThreads) {
+            for (int p = from + tid; p < to; p += kNT) {
                 const unsigned x = order_of(w[p]);
                 if ((x & known) == least) atomicAdd(&s_hist[(x >> shift) & (bins - 1)], 1);
             }
             __syncthreads();
-            // thread t has bins 2 t' and 2 t' + 1 from the top: the bin in which the count passes `ties`
-            const int top = kBins - 1 - 2 * tid;
-            const int n0 = s_hist[top], n1 = s_hist[top - 1];
-            int total;
-            const int upto = block_scan(n0 + n1, s_wave, total);
-            const int before = upto - n0 - n1;
-            if (before < ties && before + n0 >= ties) {
-                s_pick[0] = top;
-                s_pick[1] = ties - before;
-            } else if (before + n0 < ties && upto >= ties) {
-                s_pick[0] = top - 1;
-                s_pick[1] = ties - before - n0;
+            // a thread has four bins, from the top down: the bin in which the count passes `ties`
+            constexpr int B = kBins / kNT;
+            const int top = kBins - 1 - B * tid;
+            int n = 0, all;
+#pragma unroll
+            for (int x = 0; x < B; ++x) n += s_hist[top - x];
+            int before = block_scan<kNT>(n, s_wave, all) - n;
+#pragma unroll
+            for (int x = 0; x < B; ++x) {
+                const int m = s_hist[top - x];
+                if (before < ties && before + m >= ties) {
+                    s_pick[0] = top - x;
+                    s_pick[1] = ties - before;
+                }
+                before += m;
             }
             __syncthreads();
             least |= static_cast<unsigned>(s_pick[0]) << shift;
@@ -126,14 +162,14 @@ __global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArg
 
         // chosen ones before `front`
         int over = 0, equal = 0;
-        for (int p = from + tid; p < front; p += kThreads) {
+        for (int p = from + tid; p < front; p += kNT) {
             const unsigned x = order_of(w[p]);
             over += x > least;
             equal += x == least;
         }
         int over_front, equal_front;
-        block_scan(over, s_wave, over_front);
-        block_scan(equal, s_wave, equal_front);
+        block_scan<kNT>(over, s_wave, over_front);
+        block_scan<kNT>(equal, s_wave, equal_front);
         const int moves = choose - over_front - (equal_front < ties ? equal_front : ties);
 
         // Two streams of places, each in rising order: given up before `front`, chosen behind it.  A turn is
@@ -156,7 +192,7 @@ __global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArg
                     eq += same[x];
                 }
                 int all_equal, all_found;
-                int rank_equal = s.equal + block_scan(eq, s_wave, all_equal) - eq;
+                int rank_equal = s.equal + block_scan<kNT>(eq, s_wave, all_equal) - eq;
                 bool found[kPer];
                 int n = 0;
 #pragma unroll
@@ -166,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArg
                     found[x] = kept == want && s.pos + kPer * tid + x < end;
                     n += found[x];
                 }
-                int at = s.n + block_scan(n, s_wave, all_found) - n;
+                int at = s.n + block_scan<kNT>(n, s_wave, all_found) - n;
 #pragma unroll
                 for (int x = 0; x < kPer; ++x)
                     if (found[x]) out[at++] = s.pos + kPer * tid + x;
@@ -177,16 +213,16 @@ __global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArg
         };
         // the first n of a list are done: the others move up
         auto used = [&](Stream& s, int n, int* out) __attribute__((always_inline)) {
-            int rest[kList / kThreads];
+            int rest[kList / kNT];
 #pragma unroll
-            for (int x = 0; x < kList / kThreads; ++x) {
-                const int at = x * kThreads + tid;
+            for (int x = 0; x < kList / kNT; ++x) {
+                const int at = x * kNT + tid;
                 rest[x] = at < s.n - n ? out[n + at] : 0;
             }
             __syncthreads();
 #pragma unroll
-            for (int x = 0; x < kList / kThreads; ++x) {
-                const int at = x * kThreads + tid;
+            for (int x = 0; x < kList / kNT; ++x) {
+                const int at = x * kNT + tid;
                 if (at < s.n - n) out[at] = rest[x];
             }
             s.n -= n;
@@ -196,27 +232,10 @@ __global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArg
             list(come, to, true, s_src);
             __syncthreads();
             const int n = gone.n < come.n ? gone.n : come.n;  // at least one: each is listed until it is long or all there
-            auto copy = [&](u32x4_t* cache, int units, int64_t step) __attribute__((always_inline)) {
-                const int lg = __builtin_ctz(units), all = n << lg;
-                for (int x0 = tid; x0 < all; x0 += kThreads * kMoves) {
-                    u32x4_t y[kMoves];
-                    int64_t at[kMoves];
-#pragma unroll
-                    for (int b = 0; b < kMoves; ++b) {
-                        const int x = x0 + b * kThreads, m = x >> lg, u = x & (units - 1);
-                        at[b] = -1;
-                        if (x >= all) continue;
-                        y[b] = cache[token(s_src[m]) * step + u];
-                        at[b] = token(s_dst[m]) * step + u;
-                    }
-#pragma unroll
-                    for (int b = 0; b < kMoves; ++b)
-                        if (at[b] >= 0) cache[at[b]] = y[b];
-                }
-            };
-            copy(kc, ku, c.k_row);
-            copy(vc, vu, c.v_row);
-            for (int m = tid; m < n; m += kThreads) w[s_dst[m]] = w[s_src[m]];
+            for (int m = tid; m < n; m += kNT) w[s_dst[m]] = w[s_src[m]];
+            places(n);
+            move(kc, ku, c.k_row, n, std::false_type{});
+            move(vc, vu, c.v_row, n, std::false_type{});
             done += n;
             __syncthreads();
             if (done < moves) {
@@ -227,36 +246,23 @@ __global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArg
         }
     }
 
-    // The last ones: block by block, all of a block read before any of it is written.  A block's writes lie
-    // before every later block's reads.
+    // The last ones, in order, each block of them read before it is written; its writes lie before every
+    // later block's reads.
     const int back = len - e.budget;
-    auto shift = [&](u32x4_t* cache, int units, int64_t step) __attribute__((always_inline)) {
-        const int lg = __builtin_ctz(units);
-        const int64_t all = static_cast<int64_t>(e.recent) << lg;
-        for (int64_t x0 = 0; x0 < all; x0 += kThreads * kMoves) {
-            u32x4_t y[kMoves];
-            int64_t at[kMoves];
-#pragma unroll
-            for (int b = 0; b < kMoves; ++b) {
-                const int64_t x = x0 + b * kThreads + tid;
-                at[b] = -1;
-                if (x >= all) continue;
-                const int m = front + static_cast<int>(x >> lg), u = static_cast<int>(x & (units - 1));
-                y[b] = cache[token(m + back) * step + u];
-                at[b] = token(m) * step + u;
-            }
-            loads_done();
-            __syncthreads();
-#pragma unroll
-            for (int b = 0; b < kMoves; ++b)
-                if (at[b] >= 0) cache[at[b]] = y[b];
+    for (int m0 = 0; m0 < e.recent; m0 += kList) {
+        const int n = e.recent - m0 < kList ? e.recent - m0 : kList;
+        __syncthreads();  // what goes to places in front has been read, and the list used
+        for (int m = tid; m < n; m += kNT) {
+            s_src[m] = front + m0 + m + back;
+            s_dst[m] = front + m0 + m;
         }
-    };
-    __syncthreads();  // what goes to places in front has been read
-    shift(kc, ku, c.k_row);
-    shift(vc, vu, c.v_row);
+        places(n);
+        move(kc, ku, c.k_row, n, std::true_type{});
+        move(vc, vu, c.v_row, n, std::true_type{});
+    }
+    __syncthreads();
     if (!w) return;
-    for (int m0 = 0; m0 < e.recent; m0 += kThreads) {
+    for (int m0 = 0; m0 < e.recent; m0 += kNT) {
         const int m = m0 + tid;
         const float x = m < e.recent ? w[front + m + back] : 0.f;
         loads_done();
@@ -264,7 +270,7 @@ __global__ __launch_bounds__(kThreads) void kv_evict_kernel(PageArgs a, CacheArg
         if (m < e.recent) w[front + m] = x;
     }
     __syncthreads();  // written before cleared, read before cleared
-    for (int p = e.budget + tid; p < len; p += kThreads) w[p] = 0.f;
+    for (int p = e.budget + tid; p < len; p += kNT) w[p] = 0.f;
 }
 
 // The pages behind the budget go back, in the order of the requests and of the rows' pages.
@@ -302,7 +308,7 @@ __global__ __launch_bounds__(kThreads) void kv_evict_pages_kernel(PageArgs a, in
 hipError_t launch_kv_evict(const PageArgs& a, const CacheArgs& c, const EvictArgs& e, const int32_t* rows, int n, int32_t* status) {
     if (n == 0) return hipSuccess;
     const hipStream_t st = static_cast<hipStream_t>(a.stream);
-    hipLaunchKernelGGL(kv_evict_kernel, dim3(static_cast<unsigned>(n) * c.n_layers * e.Hkv), dim3(kThreads), 0, st, a, c, e, rows, status);
+    hipLaunchKernelGGL(kv_evict_kernel, dim3(static_cast<unsigned>(n) * c.n_layers * e.Hkv), dim3(kNT), 0, st, a, c, e, rows, status);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     hipLaunchKernelGGL(kv_evict_pages_kernel, dim3(1), dim3(kThreads), 0, st, a, e.budget, rows, n, status);
