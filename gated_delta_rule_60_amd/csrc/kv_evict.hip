@@ -104,28 +104,38 @@ __global__ __launch_bounds__(kNT) void kv_evict_kernel(PageArgs a, CacheArgs c, 
         }
         __syncthreads();
     };
-    auto move = [&](u32x4_t* cache, int units, int64_t step, int n, auto ORDERED) __attribute__((always_inline)) {
-        const int lg = __builtin_ctz(units), all = n << lg;
+    auto move = [&](int n, auto ORDERED) __attribute__((always_inline)) {
+        const int lk = __builtin_ctz(ku), lv = __builtin_ctz(vu), keys = n << lk, all = keys + (n << lv);
         for (int x0 = 0; x0 < all; x0 += kNT * kMoves) {
             u32x4_t y[kMoves];
-#pragma unroll
-            for (int b = 0; b < kMoves; ++b) {
+            // unit x0 + b kNT + tid of the keys and then the values: its place, from the list of places
+            auto at = [&](int b, const int* list) __attribute__((always_inline)) {
                 const int x = x0 + b * kNT + tid;
-                if (x < all) y[b] = cache[s_src[x >> lg] * step + (x & (units - 1))];
-            }
+                return x < keys ? kc + (list[x >> lk] * c.k_row + (x & (ku - 1))) : vc + (list[(x - keys) >> lv] * c.v_row + ((x - keys) & (vu - 1)));
+            };
+#pragma unroll
+            for (int b = 0; b < kMoves; ++b)
+                if (x0 + b * kNT + tid < all) y[b] = *at(b, s_src);
             if constexpr (ORDERED) {
                 loads_done();
                 __syncthreads();
             }
 #pragma unroll
-            for (int b = 0; b < kMoves; ++b) {
-                const int x = x0 + b * kNT + tid;
-                if (x < all) cache[s_dst[x >> lg] * step + (x & (units - 1))] = y[b];
-            }
+            for (int b = 0; b < kMoves; ++b)
+                if (x0 + b * kNT + tid < all) *at(b, s_dst) = y[b];
         }
     };
 
+    // Up to kFew candidates stay in registers, in the order of two turns.
+    constexpr int kFew = 2 * kTurn;
+    const bool few = to - from <= kFew;
+    unsigned kept_keys[kFew / kNT];
+    auto few_position = [&](int x) __attribute__((always_inline)) { return from + x / kPer * kTurn + kPer * tid + x % kPer; };
     if (choose > 0) {
+        if (few) {
+#pragma unroll
+            for (int x = 0; x < kFew / kNT; ++x) kept_keys[x] = few_position(x) < to ? order_of(w[few_position(x)]) : 0u;
+        }
         // the weight `least` that the choose-th heaviest has, and how many of exactly that are chosen
         unsigned least = 0, known = 0;  // digits found so far, and their bits
         int ties = choose;
@@ -133,9 +143,15 @@ __global__ __launch_bounds__(kNT) void kv_evict_kernel(PageArgs a, CacheArgs c, 
             const unsigned bins = shift == 0 ? 1024 : kBins;
             for (int b = tid; b < kBins; b += kNT) s_hist[b] = 0;
             __syncthreads();
-            for (int p = from + tid; p < to; p += kNT) {
-                const unsigned x = order_of(w[p]);
+            auto count = [&](unsigned x) __attribute__((always_inline)) {
                 if ((x & known) == least) atomicAdd(&s_hist[(x >> shift) & (bins - 1)], 1);
+            };
+            if (few) {
+#pragma unroll
+                for (int x = 0; x < kFew / kNT; ++x)
+                    if (few_position(x) < to) count(kept_keys[x]);
+            } else {
+                for (int p = from + tid; p < to; p += kNT) count(order_of(w[p]));
             }
             __syncthreads();
             // a thread has four bins, from the top down: the bin in which the count passes `ties`
@@ -160,88 +176,131 @@ __global__ __launch_bounds__(kNT) void kv_evict_kernel(PageArgs a, CacheArgs c, 
             ties = s_pick[1];
         }
 
-        // chosen ones before `front`
-        int over = 0, equal = 0;
-        for (int p = from + tid; p < front; p += kNT) {
-            const unsigned x = order_of(w[p]);
-            over += x > least;
-            equal += x == least;
-        }
-        int over_front, equal_front;
-        block_scan<kNT>(over, s_wave, over_front);
-        block_scan<kNT>(equal, s_wave, equal_front);
-        const int moves = choose - over_front - (equal_front < ties ? equal_front : ties);
-
-        // Two streams of places, each in rising order: given up before `front`, chosen behind it.  A turn is
-        // looked at once: a place that has been filled has another weight.
-        struct Stream {
-            int pos, equal;  // where it goes on, and equal weights before
-            int n;           // listed
-        };
-        Stream gone{from, 0, 0}, come{front, equal_front, 0};
-        auto list = [&](Stream& s, int end, bool want, int* out) __attribute__((always_inline)) {
-            while (s.pos < end && s.n <= kList - kTurn) {
-                bool over[kPer], same[kPer];
-                int eq = 0;
-#pragma unroll
-                for (int x = 0; x < kPer; ++x) {
-                    const int p = s.pos + kPer * tid + x;
-                    const unsigned y = p < end ? order_of(w[p]) : 0u;
-                    over[x] = p < end && y > least;
-                    same[x] = p < end && y == least;
-                    eq += same[x];
-                }
-                int all_equal, all_found;
-                int rank_equal = s.equal + block_scan<kNT>(eq, s_wave, all_equal) - eq;
-                bool found[kPer];
-                int n = 0;
-#pragma unroll
-                for (int x = 0; x < kPer; ++x) {
-                    const bool kept = over[x] || (same[x] && rank_equal < ties);
-                    rank_equal += same[x];
-                    found[x] = kept == want && s.pos + kPer * tid + x < end;
-                    n += found[x];
-                }
-                int at = s.n + block_scan<kNT>(n, s_wave, all_found) - n;
-#pragma unroll
-                for (int x = 0; x < kPer; ++x)
-                    if (found[x]) out[at++] = s.pos + kPer * tid + x;
-                s.pos += kTurn;
-                s.equal += all_equal;
-                s.n += all_found;
-            }
-        };
-        // the first n of a list are done: the others move up
-        auto used = [&](Stream& s, int n, int* out) __attribute__((always_inline)) {
-            int rest[kList / kNT];
-#pragma unroll
-            for (int x = 0; x < kList / kNT; ++x) {
-                const int at = x * kNT + tid;
-                rest[x] = at < s.n - n ? out[n + at] : 0;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int x = 0; x < kList / kNT; ++x) {
-                const int at = x * kNT + tid;
-                if (at < s.n - n) out[at] = rest[x];
-            }
-            s.n -= n;
-        };
-        for (int done = 0; done < moves;) {
-            list(gone, front, false, s_dst);
-            list(come, to, true, s_src);
-            __syncthreads();
-            const int n = gone.n < come.n ? gone.n : come.n;  // at least one: each is listed until it is long or all there
+        // the listed moves, n of them: weights, keys and values
+        auto carry_out = [&](int n) __attribute__((always_inline)) {
             for (int m = tid; m < n; m += kNT) w[s_dst[m]] = w[s_src[m]];
             places(n);
-            move(kc, ku, c.k_row, n, std::false_type{});
-            move(vc, vu, c.v_row, n, std::false_type{});
-            done += n;
+            move(n, std::false_type{});
+        };
+        if (few) {
+            // counts of the two turns in the halves of one number
+            int eq = 0, all;
+#pragma unroll
+            for (int x = 0; x < kFew / kNT; ++x) eq += (few_position(x) < to && kept_keys[x] == least) << (x / kPer * 16);
+            int rank = block_scan<kNT>(eq, s_wave, all) - eq;
+            rank += (all & 0xFFFF) << 16;  // the first turn's come before
+            int gone = 0, come = 0;
+            bool is_gone[kFew / kNT], is_come[kFew / kNT];
+#pragma unroll
+            for (int x = 0; x < kFew / kNT; ++x) {
+                const int p = few_position(x), half = x / kPer * 16;
+                const bool same = kept_keys[x] == least;
+                const bool kept = kept_keys[x] > least || (same && ((rank >> half) & 0xFFFF) < ties);
+                if (p < to && same) rank += 1 << half;
+                is_gone[x] = p < front && !kept;
+                is_come[x] = p >= front && p < to && kept;
+                gone += is_gone[x] << half;
+                come += is_come[x] << half;
+            }
+            int all_gone, all_come;
+            int g0 = block_scan<kNT>(gone, s_wave, all_gone) - gone, c0 = block_scan<kNT>(come, s_wave, all_come) - come;
+            g0 += (all_gone & 0xFFFF) << 16;
+            c0 += (all_come & 0xFFFF) << 16;
+#pragma unroll
+            for (int x = 0; x < kFew / kNT; ++x) {
+                const int half = x / kPer * 16;
+                if (is_gone[x]) {
+                    s_dst[(g0 >> half) & 0xFFFF] = few_position(x);
+                    g0 += 1 << half;
+                }
+                if (is_come[x]) {
+                    s_src[(c0 >> half) & 0xFFFF] = few_position(x);
+                    c0 += 1 << half;
+                }
+            }
             __syncthreads();
-            if (done < moves) {
-                used(gone, n, s_dst);
-                used(come, n, s_src);
+            carry_out((all_gone & 0xFFFF) + (all_gone >> 16));
+        } else {
+            // chosen ones before `front`
+            int over = 0, equal = 0;
+            for (int p = from + tid; p < front; p += kNT) {
+                const unsigned x = order_of(w[p]);
+                over += x > least;
+                equal += x == least;
+            }
+            int over_front, equal_front;
+            block_scan<kNT>(over, s_wave, over_front);
+            block_scan<kNT>(equal, s_wave, equal_front);
+            const int moves = choose - over_front - (equal_front < ties ? equal_front : ties);
+
+            // Two streams of places, each in rising order: given up before `front`, chosen behind it.  A turn is
+            // looked at once: a place that has been filled has another weight.
+            struct Stream {
+                int pos, equal;  // where it goes on, and equal weights before
+                int n;           // listed
+            };
+            Stream gone{from, 0, 0}, come{front, equal_front, 0};
+            auto list = [&](Stream& s, int end, bool want, int* out) __attribute__((always_inline)) {
+                while (s.pos < end && s.n <= kList - kTurn) {
+                    bool over[kPer], same[kPer];
+                    int eq = 0;
+#pragma unroll
+                    for (int x = 0; x < kPer; ++x) {
+                        const int p = s.pos + kPer * tid + x;
+                        const unsigned y = p < end ? order_of(w[p]) : 0u;
+                        over[x] = p < end && y > least;
+                        same[x] = p < end && y == least;
+                        eq += same[x];
+                    }
+                    int all_equal, all_found;
+                    int rank_equal = s.equal + block_scan<kNT>(eq, s_wave, all_equal) - eq;
+                    bool found[kPer];
+                    int n = 0;
+#pragma unroll
+                    for (int x = 0; x < kPer; ++x) {
+                        const bool kept = over[x] || (same[x] && rank_equal < ties);
+                        rank_equal += same[x];
+                        found[x] = kept == want && s.pos + kPer * tid + x < end;
+                        n += found[x];
+                    }
+                    int at = s.n + block_scan<kNT>(n, s_wave, all_found) - n;
+#pragma unroll
+                    for (int x = 0; x < kPer; ++x)
+                        if (found[x]) out[at++] = s.pos + kPer * tid + x;
+                    s.pos += kTurn;
+                    s.equal += all_equal;
+                    s.n += all_found;
+                }
+            };
+            // the first n of a list are done: the others move up
+            auto used = [&](Stream& s, int n, int* out) __attribute__((always_inline)) {
+                int rest[kList / kNT];
+#pragma unroll
+                for (int x = 0; x < kList / kNT; ++x) {
+                    const int at = x * kNT + tid;
+                    rest[x] = at < s.n - n ? out[n + at] : 0;
+                }
                 __syncthreads();
+#pragma unroll
+                for (int x = 0; x < kList / kNT; ++x) {
+                    const int at = x * kNT + tid;
+                    if (at < s.n - n) out[at] = rest[x];
+                }
+                s.n -= n;
+            };
+            for (int done = 0; done < moves;) {
+                list(gone, front, false, s_dst);
+                list(come, to, true, s_src);
+                __syncthreads();
+                const int n = gone.n < come.n ? gone.n : come.n;  // at least one: each is listed until it is long or all there
+                carry_out(n);
+                done += n;
+                __syncthreads();
+                if (done < moves) {
+                    used(gone, n, s_dst);
+                    used(come, n, s_src);
+                    __syncthreads();
+                }
             }
         }
     }
@@ -257,8 +316,7 @@ __global__ __launch_bounds__(kNT) void kv_evict_kernel(PageArgs a, CacheArgs c, 
             s_dst[m] = front + m0 + m;
         }
         places(n);
-        move(kc, ku, c.k_row, n, std::true_type{});
-        move(vc, vu, c.v_row, n, std::true_type{});
+        move(n, std::true_type{});
     }
     __syncthreads();
     if (!w) return;
