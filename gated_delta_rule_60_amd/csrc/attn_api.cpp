@@ -203,8 +203,8 @@ kda_status attn_window_prefill_backward(const void* q, const void* k, const void
     const int cus = kda::device_cus_or_default();
     const kda::WindowBwdPlan plan =
         kda::attn_window_bwd_plan(N, T_tot, H_q, H_kv, d_k, d_v, window, sinks, dtype == KDA_DTYPE_BF16, cus);
-    // the sinks' sums: one workgroup of 256 per (sequence, 32 sinks, key head)
-    if (static_cast<int64_t>(N) * plan.blocks * H_kv * 256 >= kMaxItems)
+    // the sinks' sums: one workgroup of 256 per (piece of rows, 32 sinks, key head)
+    if (plan.pieces * plan.blocks * H_kv * 256 >= kMaxItems)
         return fail(KDA_ERR_INVALID_ARG, "N * ceil(sinks / 32) * H_kv too large");
     if (workspace_bytes < plan.bytes)
         return fail(KDA_ERR_INVALID_ARG, "workspace smaller than attn_window_prefill_backward_workspace_size");

@@ -68,7 +68,7 @@ struct WindowBwdArgs {
     int32_t blocks;     // of 32 keys that hold the sinks; 0: no row is past their window
     int32_t pieces;     // at most
     int32_t heads;      // as WindowArgs'
-    float* sink_parts;  // [pieces][32 blocks][Hkv][d_k + d_v]
+    float* sink_parts;  // [pieces][head parts][32 blocks][Hkv][d_k + d_v]
     float* band_parts;  // [N][32 blocks][Hkv][d_k + d_v]: what the window gives those keys (whole blocks only)
 };
 

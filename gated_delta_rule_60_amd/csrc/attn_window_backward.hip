@@ -438,10 +438,11 @@ __global__ __launch_bounds__(256, 1) void attn_window_dq_split_kernel(WindowBwdA
     if (wave == 0) store_col_as_row<BF16, DK>(static_cast<G*>(b.d_q) + (tok * a.Hq + h) * DK, dq, a.scale, half, live);
 }
 
-// dk and dv of 32 keys a workgroup, its four waves on every fourth 32-row tile:
-// the rows of their window for batches that leave compute units idle, or
-// (SINKS) one piece of the rows past the window of the sinks' keys.
-template <bool BF16, int DK, int DV, bool SINKS>
+// dk and dv of 32 keys a workgroup, its four waves on every fourth 32-row tile,
+// for a part of the query heads: one piece of the rows past the window of the
+// sinks' keys, or the rows of the keys' window (for batches that leave compute
+// units idle).  Both in one launch, the sinks' first.
+template <bool BF16, int DK, int DV>
 __global__ __launch_bounds__(256, 1) void attn_window_dkv_split_kernel(WindowBwdArgs wb, float c, Stats stats) {
     using Op = AttnOp<BF16>;
     using QT = AttnTile<BF16, DK>;
@@ -461,13 +462,15 @@ __global__ __launch_bounds__(256, 1) void attn_window_dkv_split_kernel(WindowBwd
     const int g = blockIdx.x % a.Hkv;
     const int group = a.Hq / a.Hkv;
     // the query heads of this workgroup, of those of the key head
-    const int h0 = SINKS ? 0 : group * blockIdx.y / b.head_parts;
-    const int heads = SINKS ? group : group * (blockIdx.y + 1) / b.head_parts - h0;
+    const int head_parts = gridDim.y;
+    const int h0 = group * blockIdx.y / head_parts, heads = group * (blockIdx.y + 1) / head_parts - h0;
+    const int unit = blockIdx.x / a.Hkv, sink_units = wb.pieces * wb.blocks;
+    const bool sinks = unit < sink_units;
     SeqTile st;
     int key0, base, end;  // rows [base, end)
-    if constexpr (SINKS) {
-        int p = blockIdx.x / a.Hkv;
-        key0 = 32 * blockIdx.y;
+    if (sinks) {
+        int p = unit / wb.blocks;
+        key0 = 32 * (unit % wb.blocks);
         st.n = -1;
         for (int n0 = 0; n0 < a.N; n0 += 64) {
             int2 bl = make_int2(0, 0);
@@ -489,7 +492,7 @@ __global__ __launch_bounds__(256, 1) void attn_window_dkv_split_kernel(WindowBwd
         base = wb.window + st.tile * wb.rows;
         end = st.len - base < wb.rows ? st.len : base + wb.rows;
     } else {
-        if (!find_tile<32>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hkv, true, st)) return;
+        if (!find_tile<32>(a.cu_seqlens, a.N, a.T_tot, unit - sink_units, true, st)) return;
         key0 = st.tile * 32;
         base = key0;
         end = st.len - key0 < 31 + wb.window ? st.len : key0 + 31 + wb.window;
@@ -560,14 +563,14 @@ __global__ __launch_bounds__(256, 1) void attn_window_dkv_split_kernel(WindowBwd
                     dp[i] = s[i] * (dp[i] - dd[e]);
                 }
             }
-            // SINKS: rows past the window of every sink of the block see it whole
-            const bool masked = SINKS ? r0 - key0 - 31 < wb.window || key0 + 32 > wb.sinks
+            // rows past the window of every sink of the block see it whole
+            const bool masked = sinks ? r0 - key0 - 31 < wb.window || key0 + 32 > wb.sinks
                                       : r0 < key0 + 31 || r0 + 31 - key0 >= wb.window;
             if (masked) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int back = r0 + 8 * (i >> 2) + 4 * half + (i & 3) - kj;
-                    const bool sees = SINKS ? back >= wb.window && kj < wb.sinks : back >= 0 && back < wb.window;
+                    const bool sees = sinks ? back >= wb.window && kj < wb.sinks : back >= 0 && back < wb.window;
                     s[i] = sees ? s[i] : 0.f;
                     dp[i] = sees ? dp[i] : 0.f;
                 }
@@ -591,10 +594,10 @@ __global__ __launch_bounds__(256, 1) void attn_window_dkv_split_kernel(WindowBwd
     join_waves(dk, lds, wave, lane);
     join_waves(dv, lds, wave, lane);
     if (wave != 0) return;
-    if (SINKS || b.head_parts > 1 || wb.blocks > 0) {
-        const size_t row = SINKS ? static_cast<size_t>(blockIdx.x / a.Hkv) * 32 * wb.blocks + kj
+    if (sinks || head_parts > 1 || wb.blocks > 0) {
+        const size_t row = sinks ? (static_cast<size_t>(unit / wb.blocks) * head_parts + blockIdx.y) * 32 * wb.blocks + kj
                                  : static_cast<size_t>(blockIdx.y) * a.T_tot + tok;
-        float* p = (SINKS ? wb.sink_parts : b.parts) + (row * a.Hkv + g) * (DK + DV);
+        float* p = (sinks ? wb.sink_parts : b.parts) + (row * a.Hkv + g) * (DK + DV);
         store_col_as_row<false, DK>(p, dk, a.scale, half, live);
         store_col_as_row<false, DV>(p + DK, dv, 1.f, half, live);
         return;
@@ -649,7 +652,8 @@ __global__ __launch_bounds__(256) void attn_window_join_kernel(WindowBwdArgs wb)
         add(wb.band_parts + ((st.n * keys + row) * a.Hkv + g) * W + e, 1, 0);
     else
         add(b.parts + at * W + e, b.head_parts, static_cast<size_t>(a.T_tot) * a.Hkv * W);
-    add(wb.sink_parts + ((first * keys + row) * a.Hkv + g) * W + e, pieces, keys * a.Hkv * W);
+    const int head_parts = WHOLE ? 1 : b.head_parts;  // of every piece
+    add(wb.sink_parts + ((first * head_parts * keys + row) * a.Hkv + g) * W + e, pieces * head_parts, keys * a.Hkv * W);
     T::store4(e < DK ? static_cast<typename T::G*>(b.d_k) + at * DK + e : static_cast<typename T::G*>(b.d_v) + at * DV + e - DK, y);
 }
 
@@ -676,16 +680,15 @@ hipError_t launch(const WindowBwdArgs& w, const WindowBwdPlan& plan) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const bool whole = b.head_parts == 0;
-    if (whole)
+    if (whole) {
         hipLaunchKernelGGL((attn_window_dkv_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(units * a.Hkv)), threads, 0, st, w, c, stats);
-    else
-        hipLaunchKernelGGL((attn_window_dkv_split_kernel<BF16, DK, DV, false>), dim3(static_cast<unsigned>(units32 * a.Hkv), b.head_parts),
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const int64_t small = plan.pieces * w.blocks + (whole ? 0 : units32);
+    if (small > 0) {
+        hipLaunchKernelGGL((attn_window_dkv_split_kernel<BF16, DK, DV>), dim3(static_cast<unsigned>(small * a.Hkv), whole ? 1 : b.head_parts),
                            threads, 0, st, w, c, stats);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (w.blocks > 0) {
-        hipLaunchKernelGGL((attn_window_dkv_split_kernel<BF16, DK, DV, true>),
-                           dim3(static_cast<unsigned>(plan.pieces * a.Hkv), w.blocks), threads, 0, st, w, c, stats);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -735,7 +738,7 @@ WindowBwdPlan attn_window_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t
         const int64_t rows = (T_tot * p.blocks * Hkv / cus + 127) / 128 * 128;
         p.rows = static_cast<int32_t>(rows < 128 ? 128 : rows);
         p.pieces = (T_tot - window) / p.rows + N;
-        p.parts_bytes = up256(static_cast<size_t>(p.pieces) * 32 * p.blocks * row);
+        p.parts_bytes = up256(static_cast<size_t>(p.pieces) * (p.head_parts > 1 ? p.head_parts : 1) * 32 * p.blocks * row);
         if (p.head_parts == 0) p.band_bytes = up256(static_cast<size_t>(N) * 32 * p.blocks * row);
     }
     size_t heads = 0;

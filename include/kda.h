@@ -504,7 +504,8 @@ kda_status attn_window_prefill(const void* q, const void* k, const void* v, cons
  * attn_window_prefill_backward -- its gradients with respect to q, k and v:
  * attn_prefill_backward's formulas over the pairs that are seen, from the
  * forward's o and lse of the same window and sinks.  Sums and roundings as
- * there; N * ceil(sinks / 32) * H_kv < 2^24.
+ * there; N * ceil(sinks / 32) * H_kv and the device's compute units must
+ * together number less than 2^24.
  *   workspace  at least attn_window_prefill_backward_workspace_size bytes,
  *   256-byte aligned, used until the queued work ends.
  */
