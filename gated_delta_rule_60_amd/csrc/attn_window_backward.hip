@@ -323,7 +323,9 @@ __global__ __launch_bounds__(256, 1) void attn_window_dq_split_kernel(WindowBwdA
     using G = typename Op::G;
     constexpr int KB = 32 * KT::ROWB, VB = 32 * VT::ROWB;  // of a wave's tile
     constexpr int SLOT = kWaves * (KB + VB);
-    constexpr int NBUF = 2 * SLOT <= 128 * 1024 ? 2 : 1;
+    // two slots only where two workgroups a compute unit still fit (2048 tokens, 8/2 bf16 heads of 128, window
+    // 1024, backward: 99 us, 111 with two slots and one workgroup)
+    constexpr int NBUF = 2 * SLOT <= 64 * 1024 ? 2 : 1;
     constexpr int JOIN = 2 * KT::ND * 4096;
     __shared__ __attribute__((aligned(1024))) char lds[NBUF * SLOT > JOIN ? NBUF * SLOT : JOIN];
     __shared__ float s_D[kWaves][32];
@@ -450,7 +452,9 @@ __global__ __launch_bounds__(256, 1) void attn_window_dkv_split_kernel(WindowBwd
     using G = typename Op::G;
     constexpr int TG = 32 * kWaves;  // query rows the waves take together
     constexpr int QB = TG * QT::ROWB, OB = TG * OT::ROWB, SB = TG * 4;
-    constexpr int NBUF = 2 * (QB + OB + 2 * SB) <= 144 * 1024 ? 2 : 1;
+    // fp32: as in the dq kernel (4096 tokens, 8/2 heads of 64, window 512, backward: 229 us, 238 with two slots);
+    // bf16, whose steps are shorter than its loads: two (2048 tokens as above: 99 us, 107 with one)
+    constexpr int NBUF = 2 * (QB + OB + 2 * SB) <= (BF16 ? 144 : 80) * 1024 ? 2 : 1;
     constexpr int SLOT = (QB + OB + 2 * SB + 1023) / 1024 * 1024;
     constexpr int JOIN = 2 * 4096 * (QT::ND > OT::ND ? QT::ND : OT::ND);
     __shared__ __attribute__((aligned(1024))) char lds[NBUF * SLOT > JOIN ? NBUF * SLOT : JOIN];
