@@ -14,11 +14,11 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 _CSRC = os.path.join(_HERE, "csrc")
 
-SOURCES = ["kda_api.cpp", "kda_prefill.hip", "kda_segment.hip", "kda_decode.hip", "kda_backward.hip",
-           "kda_bwd_chunk.hip", "kda_noalloc.hip", "kda_anymap.hip", "attn_api.cpp", "attn_prefill.hip",
-           "attn_backward.hip", "attn_tree.hip", "kv_pages.hip", "attn_window.hip",
-           "attn_window_backward.hip", "attn_window_decode.hip", "attn_weighed.hip",
-           "attn_weights.hip", "kv_evict.hip"]
+# the longest to compile first
+SOURCES = ["attn_window_backward.hip", "attn_tree.hip", "attn_window_decode.hip", "attn_weighed.hip", "attn_backward.hip",
+           "attn_window.hip", "attn_prefill.hip", "kda_backward.hip", "kda_bwd_chunk.hip", "kda_prefill.hip",
+           "kda_api.cpp", "kda_segment.hip", "kda_decode.hip", "kda_noalloc.hip", "kda_anymap.hip", "attn_api.cpp",
+           "kv_pages.hip", "attn_weights.hip", "kv_evict.hip"]
 ARCH = "gfx950"
 
 
@@ -53,7 +53,7 @@ def _compile(src: str, obj: str, verbose: bool) -> None:
         print(err, file=sys.stderr)
 
 
-def build_library(verbose: bool = False, jobs: int = 3) -> str:
+def build_library(verbose: bool = False, jobs: int = 6) -> str:
     """Compile every source for gfx950 and link libkda.so (always rebuilds)."""
     from concurrent.futures import ThreadPoolExecutor
 

@@ -104,6 +104,7 @@ struct TreeArgs {
     int32_t items = 0;
     float* part_o = nullptr;
     float* part_ml = nullptr;
+    int32_t join_heads = 1;
     // of a window
     int32_t window = 0, sinks = 0;
     // of a weighed step
@@ -120,6 +121,7 @@ struct TreePlan {
     size_t bytes;
     bool split;   // sequences may have several chunks
     bool chunky;  // they have many
+    int32_t cus;
 };
 
 TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus);

@@ -45,6 +45,7 @@ namespace kda {
 // (256 decode rows: 349 us, 359 with two).  Never more than the blocks.
 TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus) {
     TreePlan p;
+    p.cus = cus;
     const int64_t rows = T_q * (Hq / Hkv);
     const int64_t avg = (rows + N - 1) / N;
     p.rows = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 128;

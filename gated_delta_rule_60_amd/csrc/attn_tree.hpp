@@ -32,12 +32,14 @@ constexpr float kLazyLog2 = 8.f;  // as in attn_prefill.hip
 __device__ const float kZeroRow[128] = {};
 
 // NQ 16-row groups a wave, RW waves to a tile (KW tiles at a time, TT in a slot of LDS).
-template <bool BF16, int DK, int DV, int NQ, int RW>
+template <bool BF16, int DK, int DV, int NQ, int RW, TreeMode M>
 struct TreeShape {
     static constexpr int ES = BF16 ? 2 : 4;
     static constexpr int KB = kTK * DK * ES, VB = kTK * DV * ES;  // tile bytes
     // two waves a SIMD where the tiles have a load for each (329 drafted tokens of 12 trees: 241 us with one)
-    static constexpr int NW = RW == 1 ? (8 * (KB + VB) <= 128 * 1024 ? 4 : 2) : BF16 && DK >= 64 && DV >= 64 ? 8 : 4;
+    // a window's walk is short: two waves, and with them a second workgroup to run under the first one's
+    // look-ups (256 decode rows, window 1024: 190 us, 211 with four; whole contexts: 398 and 383)
+    static constexpr int NW = RW == 1 ? (M != TreeMode::kWindow && 8 * (KB + VB) <= 128 * 1024 ? 4 : 2) : BF16 && DK >= 64 && DV >= 64 ? 8 : 4;
     static constexpr int KW = NW / RW;
     static constexpr int R = 16 * NQ * RW;  // query rows
     // slots: of one wave's tile (RW = 1), or of two tiles that all waves load
@@ -198,8 +200,8 @@ __device__ __forceinline__ void load_lds16_from(const char* p, char* lds) {
 }
 
 template <bool BF16, int DK, int DV, int NQ, int RW, TreeMode M>
-__global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW>::NW), (TreeShape<BF16, DK, DV, NQ, RW>::WPS)) void attn_tree_kernel(TreeArgs a, float c) {
-    using Sh = TreeShape<BF16, DK, DV, NQ, RW>;
+__global__ __launch_bounds__((64 * TreeShape<BF16, DK, DV, NQ, RW, M>::NW), (TreeShape<BF16, DK, DV, NQ, RW, M>::WPS)) void attn_tree_kernel(TreeArgs a, float c) {
+    using Sh = TreeShape<BF16, DK, DV, NQ, RW, M>;
     using T = Elem<BF16>;
     using KT = AttnTile<BF16, DK>;
     using VT = AttnTile<BF16, DV>;
@@ -625,100 +627,108 @@ __global__ __launch_bounds__(256) void attn_tree_join_kernel(TreeArgs a, int R) 
     constexpr int ROWS = 256 / TPR / CG;    // rows a workgroup
     __shared__ __attribute__((aligned(16))) float s_o[CG][ROWS][DV];
     __shared__ float s_ml[CG][ROWS][2];
-    const int g = blockIdx.x % a.Hkv;
+    // the key heads of this workgroup: with many row tiles the look-up is most of the work where nothing is
+    // to be joined, and one serves several heads
+    const int heads = M == TreeMode::kTree || CG > 1 ? 1 : a.join_heads, sets = a.Hkv / heads;
     const int group = a.Hq / a.Hkv;
     TreeItem it;
-    if (!find_item<4, M>(a, blockIdx.x / a.Hkv, R, false, it) || it.chunks == 1) return;
+    if (!find_item<4, M>(a, blockIdx.x / sets, R, false, it) || it.chunks == 1) return;
     if (it.item + it.chunks > a.items) return;  // offsets that overlap: no such partial results
-    const int x = threadIdx.x / TPR, row = x % ROWS, cg = x / ROWS;
-    const int rr = blockIdx.y * ROWS + row;
-    const int r = it.rt * R + rr, t = r / group, h = g * group + r % group;
-    const bool live = rr < R && t < it.lq;
-    if (CG == 1 && !live) return;
-    const int d = 4 * (threadIdx.x % TPR);
-    const size_t step = static_cast<size_t>(a.Hkv) * R;
-    const size_t row0 = (static_cast<size_t>(it.item) * a.Hkv + g) * R + (live ? rr : 0);
-    float m = -INFINITY, l = 0.f;
-    f32x4_t o = {};
-    // a group's next B chunks of those there are; past the last, the last again without weight
-    auto add = [&](int c, auto Bc) __attribute__((always_inline)) {
-        constexpr int B = Bc;
-        float m2[B], l2[B];
-        f32x4_t y[B];
+    for (int hh = 0; hh < heads; ++hh) {
+        const int g = blockIdx.x % sets * heads + hh;
+        const int x = threadIdx.x / TPR, row = x % ROWS, cg = x / ROWS;
+        const int rr = blockIdx.y * ROWS + row;
+        const int r = it.rt * R + rr, t = r / group, h = g * group + r % group;
+        const bool live = rr < R && t < it.lq;
+        if (CG == 1 && !live) return;
+        const int d = 4 * (threadIdx.x % TPR);
+        const size_t step = static_cast<size_t>(a.Hkv) * R;
+        const size_t row0 = (static_cast<size_t>(it.item) * a.Hkv + g) * R + (live ? rr : 0);
+        float m = -INFINITY, l = 0.f;
+        f32x4_t o = {};
+        // a group's next B chunks of those there are; past the last, the last again without weight
+        auto add = [&](int c, auto Bc) __attribute__((always_inline)) {
+            constexpr int B = Bc;
+            float m2[B], l2[B];
+            f32x4_t y[B];
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const int cb = c + b * CG;
-            const size_t at = row0 + (cb < it.chunks ? cb : it.chunks - 1) * step;
-            m2[b] = a.part_ml[2 * at];
-            l2[b] = a.part_ml[2 * at + 1];
-            y[b] = *reinterpret_cast<const f32x4_t*>(a.part_o + at * DV + d);
+            for (int b = 0; b < B; ++b) {
+                const int cb = c + b * CG;
+                const size_t at = row0 + (cb < it.chunks ? cb : it.chunks - 1) * step;
+                m2[b] = a.part_ml[2 * at];
+                l2[b] = a.part_ml[2 * at + 1];
+                y[b] = *reinterpret_cast<const f32x4_t*>(a.part_o + at * DV + d);
+            }
+            float m1 = m;
+#pragma unroll
+            for (int b = 0; b < B; ++b) m1 = fmaxf(m1, m2[b]);
+            const float w0 = m == m1 ? 1.f : exp2f(m - m1);
+            m = m1;
+            l *= w0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] *= w0;
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (c + b * CG >= it.chunks) break;
+                const float w = m2[b] == m ? 1.f : exp2f(m2[b] - m);
+                l = fmaf(l2[b], w, l);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = fmaf(y[b][e], w, o[e]);
+            }
+        };
+        int c = cg;
+        for (; c + 4 * CG < it.chunks; c += 8 * CG) add(c, std::integral_constant<int, 8>{});
+        if (c < it.chunks) add(c, std::integral_constant<int, 4>{});
+        if constexpr (CG > 1) {
+            *reinterpret_cast<f32x4_t*>(&s_o[cg][row][d]) = o;
+            if (d == 0) {
+                s_ml[cg][row][0] = m;
+                s_ml[cg][row][1] = l;
+            }
+            __syncthreads();
+            if (cg > 0 || !live) return;
+            // a group without a chunk left -infinity and zeros
+            float m1 = m;
+#pragma unroll
+            for (int k = 1; k < CG; ++k) m1 = fmaxf(m1, s_ml[k][row][0]);
+            const float w0 = m == m1 ? 1.f : exp2f(m - m1);
+            m = m1;
+            l *= w0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] *= w0;
+#pragma unroll
+            for (int k = 1; k < CG; ++k) {
+                const float m2 = s_ml[k][row][0], w = m2 == m ? 1.f : exp2f(m2 - m);
+                const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&s_o[k][row][d]);
+                l = fmaf(s_ml[k][row][1], w, l);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = fmaf(y[e], w, o[e]);
+            }
         }
-        float m1 = m;
-#pragma unroll
-        for (int b = 0; b < B; ++b) m1 = fmaxf(m1, m2[b]);
-        const float w0 = m == m1 ? 1.f : exp2f(m - m1);
-        m = m1;
-        l *= w0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] *= w0;
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            if (c + b * CG >= it.chunks) break;
-            const float w = m2[b] == m ? 1.f : exp2f(m2[b] - m);
-            l = fmaf(l2[b], w, l);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = fmaf(y[b][e], w, o[e]);
-        }
-    };
-    int c = cg;
-    for (; c + 4 * CG < it.chunks; c += 8 * CG) add(c, std::integral_constant<int, 8>{});
-    if (c < it.chunks) add(c, std::integral_constant<int, 4>{});
-    if constexpr (CG > 1) {
-        *reinterpret_cast<f32x4_t*>(&s_o[cg][row][d]) = o;
-        if (d == 0) {
-            s_ml[cg][row][0] = m;
-            s_ml[cg][row][1] = l;
-        }
-        __syncthreads();
-        if (cg > 0 || !live) return;
-        // a group without a chunk left -infinity and zeros
-        float m1 = m;
-#pragma unroll
-        for (int k = 1; k < CG; ++k) m1 = fmaxf(m1, s_ml[k][row][0]);
-        const float w0 = m == m1 ? 1.f : exp2f(m - m1);
-        m = m1;
-        l *= w0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] *= w0;
-#pragma unroll
-        for (int k = 1; k < CG; ++k) {
-            const float m2 = s_ml[k][row][0], w = m2 == m ? 1.f : exp2f(m2 - m);
-            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&s_o[k][row][d]);
-            l = fmaf(s_ml[k][row][1], w, l);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = fmaf(y[e], w, o[e]);
-        }
+        const size_t out = static_cast<size_t>(it.tok0 + t) * a.Hq + h;
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const float y[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+        T::store4(static_cast<typename T::G*>(a.o) + out * DV + d, y);
+        if (a.lse && d == 0) a.lse[out] = (m + log2f(l)) * kLn2;
     }
-    const size_t out = static_cast<size_t>(it.tok0 + t) * a.Hq + h;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const float y[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
-    T::store4(static_cast<typename T::G*>(a.o) + out * DV + d, y);
-    if (a.lse && d == 0) a.lse[out] = (m + log2f(l)) * kLn2;
 }
 
 namespace {
 
 template <bool BF16, int DV, int CG, TreeMode M>
-hipError_t launch_join(const TreeArgs& a, const TreePlan& p) {
+hipError_t launch_join(TreeArgs a, const TreePlan& p) {
     constexpr int rows = 256 / (DV / 4) / CG;  // of a workgroup
-    hipLaunchKernelGGL((attn_tree_join_kernel<BF16, DV, CG, M>), dim3(static_cast<unsigned>(p.tiles * a.Hkv), (p.rows + rows - 1) / rows),
-                       dim3(256), 0, static_cast<hipStream_t>(a.stream), a, p.rows);
+    const int sets = (p.rows + rows - 1) / rows;
+    if (M != TreeMode::kTree && CG == 1)  // two workgroups a compute unit, at least
+        while (a.Hkv % (2 * a.join_heads) == 0 && p.tiles * sets * a.Hkv / (2 * a.join_heads) >= 2 * p.cus) a.join_heads *= 2;
+    hipLaunchKernelGGL((attn_tree_join_kernel<BF16, DV, CG, M>), dim3(static_cast<unsigned>(p.tiles * a.Hkv / a.join_heads), sets), dim3(256),
+                       0, static_cast<hipStream_t>(a.stream), a, p.rows);
     return hipGetLastError();
 }
 
 template <bool BF16, int DK, int DV, int NQ, int RW, TreeMode M>
 hipError_t launch(const TreeArgs& a, const TreePlan& p) {
-    using Sh = TreeShape<BF16, DK, DV, NQ, RW>;
+    using Sh = TreeShape<BF16, DK, DV, NQ, RW, M>;
     const hipStream_t st = static_cast<hipStream_t>(a.stream);
     hipLaunchKernelGGL((attn_tree_kernel<BF16, DK, DV, NQ, RW, M>), dim3(static_cast<unsigned>(p.items * a.Hkv)), dim3(64 * Sh::NW), 0,
                        st, a, a.scale * kLog2e);
