@@ -321,8 +321,8 @@ kda_status check_decode(kda::TreeArgs& a, int64_t T_q, int64_t q_stride, kda_dty
 }
 
 // The launch shape over at most `room` positions a row tile.
-kda_status check_tree_plan(const kda::TreeArgs& a, int64_t room, kda::TreePlan& plan) {
-    plan = kda::tree_plan(a.N, a.T_q, a.Hq, a.Hkv, a.d_v, room, kda::device_cus_or_default());
+kda_status check_tree_plan(const kda::TreeArgs& a, int64_t room, kda::TreePlan& plan, int32_t most_rows = 128) {
+    plan = kda::tree_plan(a.N, a.T_q, a.Hq, a.Hkv, a.d_v, room, kda::device_cus_or_default(), most_rows);
     if (!tree_countable(plan, a.T_q, room, a.Hq, a.Hkv))
         return fail(KDA_ERR_INVALID_ARG, "too many drafted tokens for sequences this long");
     return KDA_OK;
@@ -340,6 +340,8 @@ int64_t window_room(int32_t page_size, int32_t max_pages, int32_t window, int32_
     const int64_t room = static_cast<int64_t>(max_pages) * page_size, most = static_cast<int64_t>(window) + sinks + 128;
     return room < most ? room : most;
 }
+
+constexpr int32_t kWeighedRows = 32;  // of a pass
 
 // A weighed step's workspace: the partial results, the scores, and lse if the caller wants none.
 struct WeighedBytes {
@@ -418,7 +420,7 @@ size_t attn_weighed_decode_workspace_size(int32_t N, int32_t H_q, int32_t H_kv, 
     if (!decode_sizes(N, N, H_q, H_kv, d_v, page_size, max_pages)) return 0;
     return weighed_bytes(N, H_q, static_cast<int64_t>(max_pages) * page_size,
                          kda::tree_plan(N, N, H_q, H_kv, d_v, static_cast<int64_t>(max_pages) * page_size,
-                                        kda::device_cus_or_default())).all;
+                                        kda::device_cus_or_default(), kWeighedRows)).all;
 }
 
 kda_status attn_weighed_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -434,7 +436,7 @@ kda_status attn_weighed_decode(const void* q, const void* k_cache, const void* v
     if (!weights || !aligned(weights, 4)) return fail(KDA_ERR_INVALID_ARG, "weights must not be NULL, and 4-byte aligned");
     const int64_t room = static_cast<int64_t>(max_pages) * page_size;
     kda::TreePlan plan;
-    if ((s = check_tree_plan(a, room, plan)) != KDA_OK) return s;
+    if ((s = check_tree_plan(a, room, plan, kWeighedRows)) != KDA_OK) return s;
     // the weights: workgroups of 256, at most 4096 turns of 1024 positions each
     const int64_t turns = (room + 1023) / 1024 < 4096 ? (room + 1023) / 1024 : 4096;
     if (static_cast<int64_t>(N) * H_kv * turns * 256 >= kMaxItems)

@@ -43,12 +43,13 @@ namespace kda {
 // one, 132 with four; 329 tokens of 12 trees: 169 us, 202 and 186); four where
 // the sequences alone are four a unit and more, and only the longest are cut
 // (256 decode rows: 349 us, 359 with two).  Never more than the blocks.
-TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus) {
+TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus, int32_t most_rows) {
     TreePlan p;
     p.cus = cus;
     const int64_t rows = T_q * (Hq / Hkv);
     const int64_t avg = (rows + N - 1) / N;
     p.rows = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
+    if (p.rows > most_rows) p.rows = most_rows;
     p.tiles = rows / p.rows + N;
     if (p.tiles > rows) p.tiles = rows;
     const int64_t blocks = (room + kBlock - 1) / kBlock;

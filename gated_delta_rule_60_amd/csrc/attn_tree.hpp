@@ -739,11 +739,15 @@ hipError_t launch(const TreeArgs& a, const TreePlan& p) {
 
 template <bool BF16, int DK, int DV, TreeMode M>
 hipError_t launch_rows(const TreeArgs& a, const TreePlan& p) {
-    switch (p.rows) {
-        case 16: return launch<BF16, DK, DV, 1, 1, M>(a, p);
-        case 32: return launch<BF16, DK, DV, 2, 1, M>(a, p);
-        case 64: return launch<BF16, DK, DV, 1, 4, M>(a, p);
-        default: return launch<BF16, DK, DV, 2, 4, M>(a, p);
+    if constexpr (M == TreeMode::kWeighed) {  // one token a sequence: of more than 32 query heads a key head, 32 at a time
+        return p.rows == 16 ? launch<BF16, DK, DV, 1, 1, M>(a, p) : launch<BF16, DK, DV, 2, 1, M>(a, p);
+    } else {
+        switch (p.rows) {
+            case 16: return launch<BF16, DK, DV, 1, 1, M>(a, p);
+            case 32: return launch<BF16, DK, DV, 2, 1, M>(a, p);
+            case 64: return launch<BF16, DK, DV, 1, 4, M>(a, p);
+            default: return launch<BF16, DK, DV, 2, 4, M>(a, p);
+        }
     }
 }
 

@@ -660,8 +660,9 @@ size_t attn_window_decode_workspace_size(int32_t N, int64_t T_q, int32_t H_q, in
  *   lse        may be NULL
  *   workspace  at least attn_weighed_decode_workspace_size bytes, 256-byte
  *              aligned, used until the queued work ends
- * Everything else as for attn_tree_decode with cu_q = 0, 1, ..., N.  The
- * result is the same bits every time.  attn_prefill_weights starts a prompt's
+ * Everything else as for attn_tree_decode with cu_q = 0, 1, ..., N; of more
+ * than 32 query heads a key head, every 32 walk the positions in their turn.
+ * The result is the same bits every time.  attn_prefill_weights starts a prompt's
  * weights, kv_evict uses them.
  */
 kda_status attn_weighed_decode(const void* q, const void* k_cache, const void* v_cache,
