@@ -22,10 +22,12 @@ enum class TreeMode {
     kWeighed,  // one token a sequence, all positions; the scores go to a.scores
 };
 
+// Chunks are multiples of this many keys: a window's few keys go to more workgroups.
+constexpr int tree_block(TreeMode m) { return m == TreeMode::kWindow ? 64 : 128; }
+
 namespace {
 
 constexpr int kTK = 32;      // keys of a wave's tile
-constexpr int kBlock = 128;  // chunks are multiples of this many keys
 constexpr float kLazyLog2 = 8.f;  // as in attn_prefill.hip
 
 // what the loads of rows outside the cache read instead
@@ -83,7 +85,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeArgs& a, int n, int rows) 
         s.lq = bl.y;
         s.ctx = ctx;
         s.tiles = (bl.y * (a.Hq / a.Hkv) + rows - 1) / rows;
-        s.blocks = (total + kBlock - 1) / kBlock;
+        s.blocks = (total + tree_block(M) - 1) / tree_block(M);
     }
     return s;
 }
@@ -157,8 +159,8 @@ __device__ __forceinline__ bool find_item(const TreeArgs& a, int p, int rows, bo
             t.item = base + __builtin_amdgcn_readlane(upto_chunks, l) - __builtin_amdgcn_readlane(all, l) + t.rt * t.chunks + c;
             const int blocks = __builtin_amdgcn_readlane(s.blocks, l);
             // even chunks, in blocks
-            t.k0 = static_cast<int>(static_cast<int64_t>(blocks) * c / t.chunks) * kBlock;
-            t.k1 = static_cast<int>(static_cast<int64_t>(blocks) * (c + 1) / t.chunks) * kBlock;
+            t.k0 = static_cast<int>(static_cast<int64_t>(blocks) * c / t.chunks) * tree_block(M);
+            t.k1 = static_cast<int>(static_cast<int64_t>(blocks) * (c + 1) / t.chunks) * tree_block(M);
             sound = true;
             return true;
         }
@@ -719,8 +721,10 @@ template <bool BF16, int DV, int CG, TreeMode M>
 hipError_t launch_join(TreeArgs a, const TreePlan& p) {
     constexpr int rows = 256 / (DV / 4) / CG;  // of a workgroup
     const int sets = (p.rows + rows - 1) / rows;
-    if (M != TreeMode::kTree && CG == 1)  // two workgroups a compute unit, at least
-        while (a.Hkv % (2 * a.join_heads) == 0 && p.tiles * sets * a.Hkv / (2 * a.join_heads) >= 2 * p.cus) a.join_heads *= 2;
+    // at least so many workgroups a compute unit: a window's sequences hardly ever have chunks to join
+    const int least = M == TreeMode::kWindow ? 2 : 8;
+    if (M != TreeMode::kTree && CG == 1)
+        while (a.Hkv % (2 * a.join_heads) == 0 && p.tiles * sets * a.Hkv / (2 * a.join_heads) >= least * p.cus) a.join_heads *= 2;
     hipLaunchKernelGGL((attn_tree_join_kernel<BF16, DV, CG, M>), dim3(static_cast<unsigned>(p.tiles * a.Hkv / a.join_heads), sets), dim3(256),
                        0, static_cast<hipStream_t>(a.stream), a, p.rows);
     return hipGetLastError();

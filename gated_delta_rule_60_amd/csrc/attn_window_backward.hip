@@ -727,8 +727,8 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-// Pieces of rows: so long that their workgroups are about one for every compute unit (it holds no second
-// one), and at least one group of 128 rows.
+// Pieces of rows: so long that there is at most one workgroup for every compute unit (it holds no second
+// one), a short last piece of every sequence counted, and at least one group of 128 rows.
 WindowBwdPlan attn_window_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t d_k, int32_t d_v, int32_t window,
                                    int32_t sinks, bool bf16, int cus) {
     const BwdPlan plain = attn_bwd_plan(N, T_tot, Hq, Hkv, d_k, d_v, bf16, cus);
@@ -739,7 +739,8 @@ WindowBwdPlan attn_window_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t
     if (sinks > 0 && window < T_tot) {
         const int64_t keys = sinks < T_tot ? sinks : T_tot;
         p.blocks = static_cast<int32_t>((keys + 31) / 32);
-        const int64_t rows = (T_tot * p.blocks * Hkv / cus + 127) / 128 * 128;
+        const int64_t places = cus / (p.blocks * Hkv) - N, left = T_tot - window;
+        const int64_t rows = (left / (places > 1 ? places : 1) + 127) / 128 * 128;
         p.rows = static_cast<int32_t>(rows < 128 ? 128 : rows);
         p.pieces = (T_tot - window) / p.rows + N;
         p.parts_bytes = up256(static_cast<size_t>(p.pieces) * (p.head_parts > 1 ? p.head_parts : 1) * 32 * p.blocks * row);
