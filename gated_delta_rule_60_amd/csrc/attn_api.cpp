@@ -287,8 +287,8 @@ kda_status check_cache(int32_t n_pages, int32_t page_size, int32_t max_pages) {
 
 // Query rows, row tiles times key blocks, and the work items of workgroups of up to 512, must stay
 // countable in 32 bits.
-bool tree_countable(const kda::TreePlan& p, int64_t T_q, int64_t room, int32_t H_q, int32_t H_kv, int32_t block) {
-    const int64_t blocks = room / block + 1;
+bool tree_countable(const kda::TreePlan& p, int64_t T_q, int64_t room, int32_t H_q, int32_t H_kv) {
+    const int64_t blocks = room / 128 + 1;
     return T_q * (H_q / H_kv) <= (int64_t{1} << 30) && p.tiles <= INT32_MAX / blocks && (p.items + p.tiles) * H_kv * 512 < kMaxItems;
 }
 
@@ -321,10 +321,9 @@ kda_status check_decode(kda::TreeArgs& a, int64_t T_q, int64_t q_stride, kda_dty
 }
 
 // The launch shape over at most `room` positions a row tile.
-kda_status check_tree_plan(const kda::TreeArgs& a, int64_t room, kda::TreePlan& plan, int32_t block = 128,
-                           int32_t most_rows = 128) {
-    plan = kda::tree_plan(a.N, a.T_q, a.Hq, a.Hkv, a.d_v, room, kda::device_cus_or_default(), block, most_rows);
-    if (!tree_countable(plan, a.T_q, room, a.Hq, a.Hkv, block))
+kda_status check_tree_plan(const kda::TreeArgs& a, int64_t room, kda::TreePlan& plan, int32_t most_rows = 128) {
+    plan = kda::tree_plan(a.N, a.T_q, a.Hq, a.Hkv, a.d_v, room, kda::device_cus_or_default(), most_rows);
+    if (!tree_countable(plan, a.T_q, room, a.Hq, a.Hkv))
         return fail(KDA_ERR_INVALID_ARG, "too many drafted tokens for sequences this long");
     return KDA_OK;
 }
@@ -343,7 +342,6 @@ int64_t window_room(int32_t page_size, int32_t max_pages, int32_t window, int32_
 }
 
 constexpr int32_t kWeighedRows = 32;  // of a pass
-constexpr int32_t kWindowBlock = 64;  // keys that a window's chunks are multiples of
 
 // A weighed step's workspace: the partial results, the scores, and lse if the caller wants none.
 struct WeighedBytes {
@@ -394,8 +392,7 @@ size_t attn_window_decode_workspace_size(int32_t N, int64_t T_q, int32_t H_q, in
     if (!decode_sizes(N, T_q, H_q, H_kv, d_v, page_size, max_pages) || window < 1 || window > (1 << 30) || sinks < 0 ||
         sinks > kda::kMaxSinks)
         return 0;
-    return kda::tree_plan(N, T_q, H_q, H_kv, d_v, window_room(page_size, max_pages, window, sinks), kda::device_cus_or_default(),
-                          kWindowBlock).bytes;
+    return kda::tree_plan(N, T_q, H_q, H_kv, d_v, window_room(page_size, max_pages, window, sinks), kda::device_cus_or_default()).bytes;
 }
 
 kda_status attn_window_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -411,7 +408,7 @@ kda_status attn_window_decode(const void* q, const void* k_cache, const void* v_
     kda_status s = check_decode(a, T_q, q_stride, dtype, "block_table, ctx_lens and cu_q must not be NULL", cu_q);
     if (s != KDA_OK || (s = check_window(window, sinks)) != KDA_OK) return s;
     kda::TreePlan plan;
-    if ((s = check_tree_plan(a, window_room(page_size, max_pages, window, sinks), plan, kWindowBlock)) != KDA_OK) return s;
+    if ((s = check_tree_plan(a, window_room(page_size, max_pages, window, sinks), plan)) != KDA_OK) return s;
     if ((s = check_tree_workspace(a, plan.bytes, workspace_bytes, "attn_window_decode_workspace_size")) != KDA_OK) return s;
     if (T_q == 0) return KDA_OK;
     (void)hipGetLastError();  // report only this launch's status
@@ -423,7 +420,7 @@ size_t attn_weighed_decode_workspace_size(int32_t N, int32_t H_q, int32_t H_kv, 
     if (!decode_sizes(N, N, H_q, H_kv, d_v, page_size, max_pages)) return 0;
     return weighed_bytes(N, H_q, static_cast<int64_t>(max_pages) * page_size,
                          kda::tree_plan(N, N, H_q, H_kv, d_v, static_cast<int64_t>(max_pages) * page_size,
-                                        kda::device_cus_or_default(), 128, kWeighedRows)).all;
+                                        kda::device_cus_or_default(), kWeighedRows)).all;
 }
 
 kda_status attn_weighed_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -439,7 +436,7 @@ kda_status attn_weighed_decode(const void* q, const void* k_cache, const void* v
     if (!weights || !aligned(weights, 4)) return fail(KDA_ERR_INVALID_ARG, "weights must not be NULL, and 4-byte aligned");
     const int64_t room = static_cast<int64_t>(max_pages) * page_size;
     kda::TreePlan plan;
-    if ((s = check_tree_plan(a, room, plan, 128, kWeighedRows)) != KDA_OK) return s;
+    if ((s = check_tree_plan(a, room, plan, kWeighedRows)) != KDA_OK) return s;
     // the weights: workgroups of 256, at most 4096 turns of 1024 positions each
     const int64_t turns = (room + 1023) / 1024 < 4096 ? (room + 1023) / 1024 : 4096;
     if (static_cast<int64_t>(N) * H_kv * turns * 256 >= kMaxItems)

@@ -124,10 +124,8 @@ struct TreePlan {
     int32_t cus;
 };
 
-// block: keys that chunks are multiples of (64 for a window); most_rows: of a pass, 32 (a weighed step's
-// kernels) or 128.
-TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus, int32_t block = 128,
-                   int32_t most_rows = 128);
+// most_rows: of a pass, 32 (a weighed step's kernels) or 128.
+TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus, int32_t most_rows = 128);
 hipError_t launch_attn_tree(const TreeArgs& a, const TreePlan& p);
 hipError_t launch_attn_window_decode(const TreeArgs& a, const TreePlan& p);
 hipError_t launch_attn_weighed(const TreeArgs& a, const TreePlan& p);

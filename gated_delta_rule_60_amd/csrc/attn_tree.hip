@@ -43,8 +43,7 @@ namespace kda {
 // one, 132 with four; 329 tokens of 12 trees: 169 us, 202 and 186); four where
 // the sequences alone are four a unit and more, and only the longest are cut
 // (256 decode rows: 349 us, 359 with two).  Never more than the blocks.
-TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus, int32_t block,
-                   int32_t most_rows) {
+TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v, int64_t room, int cus, int32_t most_rows) {
     TreePlan p;
     p.cus = cus;
     const int64_t rows = T_q * (Hq / Hkv);
@@ -53,7 +52,7 @@ TreePlan tree_plan(int32_t N, int64_t T_q, int32_t Hq, int32_t Hkv, int32_t d_v,
     if (p.rows > most_rows) p.rows = most_rows;
     p.tiles = rows / p.rows + N;
     if (p.tiles > rows) p.tiles = rows;
-    const int64_t blocks = (room + block - 1) / block;
+    const int64_t blocks = (room + kBlock - 1) / kBlock;
     const int64_t least = N > rows / p.rows ? N : rows / p.rows;  // row tiles
     const int64_t rounds = 4 * least * Hkv <= cus ? 1 : least * Hkv < 4 * static_cast<int64_t>(cus) ? 2 : 4;
     int64_t target = rounds * cus / Hkv;

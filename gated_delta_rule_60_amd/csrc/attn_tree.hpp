@@ -22,12 +22,10 @@ enum class TreeMode {
     kWeighed,  // one token a sequence, all positions; the scores go to a.scores
 };
 
-// Chunks are multiples of this many keys: a window's few keys go to more workgroups.
-constexpr int tree_block(TreeMode m) { return m == TreeMode::kWindow ? 64 : 128; }
-
 namespace {
 
 constexpr int kTK = 32;      // keys of a wave's tile
+constexpr int kBlock = 128;  // chunks are multiples of this many keys
 constexpr float kLazyLog2 = 8.f;  // as in attn_prefill.hip
 
 // what the loads of rows outside the cache read instead
@@ -85,7 +83,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeArgs& a, int n, int rows) 
         s.lq = bl.y;
         s.ctx = ctx;
         s.tiles = (bl.y * (a.Hq / a.Hkv) + rows - 1) / rows;
-        s.blocks = (total + tree_block(M) - 1) / tree_block(M);
+        s.blocks = (total + kBlock - 1) / kBlock;
     }
     return s;
 }
@@ -159,8 +157,8 @@ __device__ __forceinline__ bool find_item(const TreeArgs& a, int p, int rows, bo
             t.item = base + __builtin_amdgcn_readlane(upto_chunks, l) - __builtin_amdgcn_readlane(all, l) + t.rt * t.chunks + c;
             const int blocks = __builtin_amdgcn_readlane(s.blocks, l);
             // even chunks, in blocks
-            t.k0 = static_cast<int>(static_cast<int64_t>(blocks) * c / t.chunks) * tree_block(M);
-            t.k1 = static_cast<int>(static_cast<int64_t>(blocks) * (c + 1) / t.chunks) * tree_block(M);
+            t.k0 = static_cast<int>(static_cast<int64_t>(blocks) * c / t.chunks) * kBlock;
+            t.k1 = static_cast<int>(static_cast<int64_t>(blocks) * (c + 1) / t.chunks) * kBlock;
             sound = true;
             return true;
         }
