@@ -5,13 +5,24 @@
 //     w[n, g, j] = sum_{h of g} sum_{i >= j} exp(s_ij - lse_i).
 //
 // The scores of the forward pass once more, with the keys kept and the rows
-// walked: a wave has 64 keys of a key head in registers, the tiles of 32 query
+// walked: a wave has 64 keys of a key head in registers, the tiles of 64 query
 // rows of its heads come through LDS, and S = Q K^T in 32x32 MFMAs leaves a
 // lane the scores of 16 rows against one key, whose weights it adds into one
 // number.  So there is one product a pair and no second one to feed; 64 keys
-// a wave and not 32, because a row read from LDS then serves two products (at
-// one product a read LDS bounds it).  Each sum is one lane's, in one order,
-// joined with the other half-wave's at the end.
+// a wave and not 32, because a row read from LDS then serves two products.
+// Each sum is one lane's, in one order, joined with the other half-wave's at
+// the end.
+//
+// A long sequence's first keys have all of its rows; a block's rows (of all the
+// query heads of its key head, one after another) are therefore given to several
+// workgroups, and a second launch adds their sums in order (32k tokens in 8
+// prompts, 32/8 heads of 128, every row: 1156 us in one part, 915 in six, 936 and
+// 941 in three and twelve; with a sequence's blocks following one another 850 in
+// six).  Bound by nothing alone there: 880 TFLOP/s, the matrix cores busy 40 %
+// and the vector units 57 %, two waves a SIMD that wait for their products,
+// exponentials and loads in turn.  Taking turns by hand (products of the next
+// rows between the exponentials) took 877 to 928 us beside 846 to 870,
+// workgroups that stay 943 to 996 beside 849 to 856.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -43,7 +54,7 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = a.Hq / a.Hkv;
-    // the first keys have the most rows: their workgroups come first, over all sequences
+    // a sequence's blocks of keys follow one another, the key heads of a block side by side
     const int KBn = (wa.width + kBK - 1) / kBK;
     const int g = blockIdx.x % a.Hkv, n = blockIdx.x / a.Hkv / KBn;
     const int key0 = static_cast<int>(blockIdx.x / a.Hkv % KBn) * kBK, wkey = key0 + kKeys * wave;

@@ -8,12 +8,19 @@
 //     dk_j = scale sum_h sum_i ds_ij q_i,   dv_j = sum_h sum_i p_ij do_i.
 //
 // Laid out as attn_backward.hip: a pass over the keys of a block of rows (dq,
-// and D), one over the rows of a block of keys (dk, dv); no atomics, one order
-// of every sum.  The rows that see a key are those of its window; the few
-// sinks are seen by all rows behind them too.  Left to the workgroup of their
-// block those would be a chain as long as the sequence, so the rows past the
-// window go in pieces to workgroups of their own (32 keys each), and a last
-// launch adds what the pieces give the sinks to what their window gave.
+// and D; its waves on the heads of a group as in attn_window.hip), one over the
+// rows of a block of keys (dk, dv); no atomics, one order of every sum.  The
+// rows that see a key are those of its window; the few sinks are seen by all
+// rows behind them too.  Left to the workgroup of their block those would be a
+// chain as long as the sequence, so the rows past the window go in pieces to
+// workgroups of their own (32 keys each), and a last launch adds what the
+// pieces give the sinks to what their window gave.
+//
+// Bound by what feeds the matrix cores (16k tokens in 4 sequences, 32/8 heads
+// of 128, bf16, window 1024: forward and backward 1.33 ms; one by one under the
+// profiler, at lower clocks, forward 0.38, dq 0.48, 44 % busy, dk/dv 0.63, 41 %
+// busy, its waves waiting half of their time, the sinks' pieces 0.07, the join
+// 0.005).
 #include <hip/hip_runtime.h>
 
 #include "attn_window.hpp"

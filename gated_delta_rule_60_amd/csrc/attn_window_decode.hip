@@ -9,7 +9,9 @@
 // window's beginning for some of the tokens, or the tokens themselves are
 // masked.  What lies in the gap is not read: however long the context, a
 // sequence costs its window and sinks once per key head, and the step is
-// bound by HBM as that of the whole context is.
+// bound by HBM as that of the whole context is (256 sequences, 32/8 heads of
+// 128, window 1024: 181 us, 4.6 TB/s; 64 with a window of 8192: 384 us, 5.6
+// TB/s).  One sequence of 16k: two launches one after the other, 8.4 and 4.5 us.
 #include "attn_tree.hpp"
 
 namespace kda {
