@@ -12,6 +12,8 @@
 // positions, 32/8 heads of 128, bf16: 380 us; one by one under the profiler the
 // pass 361, the join 10, the weights 19).  Bound by HBM: 3.9 TB/s of keys, values
 // and weights.
+#include <cfloat>
+
 #include "attn_tree.hpp"
 
 namespace kda {
@@ -34,13 +36,15 @@ __global__ __launch_bounds__(256) void attn_weigh_kernel(TreeArgs a, float c) {
     for (int k0 = blockIdx.y * kKeys; k0 < total; k0 += gridDim.y * kKeys) {
         float sum[kKeys / 256] = {};
         for (int r = 0; r < group; ++r) {
-            const float l2 = lse[r] * kLog2e;
+            // lse is -infinity where every score was below the range of fp32, by the product or by c: from the
+            // lowest finite number such scores weigh nothing
+            const float l2 = lse[r] == -INFINITY ? -FLT_MAX : lse[r] * kLog2e;
             const float* row = s + static_cast<size_t>(r) * a.score_pitch;
 #pragma unroll
             for (int i = 0; i < kKeys / 256; ++i) {
                 const int j = k0 + i * 256 + threadIdx.x;
                 const float x = j < total ? row[j] : -INFINITY;
-                // a position without a page is seen by no row, and lse is -infinity where there is none else
+                // a position without a page is seen by no row
                 sum[i] += x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(fmaf(x, c, -l2));
             }
         }

@@ -161,6 +161,22 @@ def test_decode_streams_graph_replays_and_the_same_bits(dtype):
         assert torch.equal(want, c.weights) and all(torch.equal(x, y) for x, y in zip(kept, eager)), f"replay {n}"
 
 
+def test_decode_scores_below_the_range_weigh_nothing():
+    """Finite queries and keys whose scores pass -2^128, by the product or only by the scale: a row without another
+    score has a statistic of -infinity, and weighs nothing."""
+    for size, scale in ((1e20, 1 / 8), (1e19, 10.0)):
+        c = Case([60, 40], 4, 2, 64, 64, 16, "bf16", seed=4)
+        c.q[1, :, 0] = size
+        pages = c.table[1][c.table[1] >= 0].long()
+        c.k[pages] = 0
+        c.k[pages, :, :, 0] = -size
+        before = c.weights.clone()
+        c.call(scale=scale)
+        torch.cuda.synchronize()
+        assert torch.equal(c.weights[1], before[1]), f"{size} {scale}"
+        assert c.weights[0].isfinite().all()
+
+
 def test_decode_refusals():
     c = Case([30], 2, 1, 32, 32, 16, "f32")
     with pytest.raises(ValueError, match="weights must have shape"):
