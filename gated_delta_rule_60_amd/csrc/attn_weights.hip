@@ -25,6 +25,7 @@
 // workgroups that stay 943 to 996 beside 849 to 856.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "attn_device.hpp"
@@ -84,16 +85,25 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
             const size_t r = static_cast<size_t>(beg) + static_cast<size_t>(t) * BN;
             QT::template stage<kWaves, BN>(lds[slot], static_cast<const char*>(a.q) + (r * a.q_stride + static_cast<size_t>(h) * DK) * Op::ES,
                                            left, qs, qsrc, wave);
-            if (wave == 0) {  // the rows' statistics; lanes past the tile's last row read past the range: zero
-                const int there = left < BN ? left : BN;
-                load_lds4(buffer_rsrc(a.lse + r * a.Hq + h, ((there - 1) * a.Hq + 1) * 4), lds[slot] + QB, lane * a.Hq * 4, 0);
-            }
+        };
+        // the rows' statistics, one a lane of the first wave; rows past the last are masked
+        auto statistic = [&](int hh, int t) __attribute__((always_inline)) {
+            const int row = t * BN + lane < len ? t * BN + lane : len - 1;
+            return a.lse[(static_cast<size_t>(beg) + row) * a.Hq + g * group + hh];
+        };
+        // As powers of two, once for all waves and keys.  A row whose scores are all below the range of fp32
+        // has -infinity: from the lowest finite number they weigh nothing (-infinity less -infinity is NaN).
+        auto keep_statistic = [&](int slot, float lse) __attribute__((always_inline)) {
+            reinterpret_cast<float*>(lds[slot] + QB)[lane] = fmaxf(lse * kLog2e, -FLT_MAX);
         };
         // this workgroup's part of them
         const int64_t all = static_cast<int64_t>(group) * (t1 - t0);
         const int begin = static_cast<int>(all * blockIdx.y / wa.parts), end = static_cast<int>(all * (blockIdx.y + 1) / wa.parts);
         int hh = begin / (t1 - t0), t = t0 + begin % (t1 - t0), slot = 0;
-        if (begin < end) stage_tile(0, hh, t);
+        if (begin < end) {
+            if (wave == 0) keep_statistic(0, statistic(hh, t));
+            stage_tile(0, hh, t);
+        }
         loads_done();
         for (int step = begin; step < end; ++step) {
             int nh = hh, nt = t + 1;
@@ -102,7 +112,11 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
                 ++nh;
             }
             lds_ready();
-            if (step + 1 < end) stage_tile(slot ^ 1, nh, nt);
+            float next = 0.f;
+            if (step + 1 < end) {
+                if (wave == 0) next = statistic(nh, nt);
+                stage_tile(slot ^ 1, nh, nt);
+            }
             if (t * BN + BN > wkey && wkey < len) {
                 const char* qt = lds[slot];
                 const float* sl = reinterpret_cast<const float*>(qt + QB);
@@ -119,11 +133,7 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
                 auto add = [&](int r0, const f32x16_t (&s)[NK], auto MASKED) __attribute__((always_inline)) {
                     f32x4_t l2[4];
 #pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) {
-                        l2[i4] = *reinterpret_cast<const f32x4_t*>(sl + r0 + 8 * i4 + 4 * half);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) l2[i4][e] *= kLog2e;
-                    }
+                    for (int i4 = 0; i4 < 4; ++i4) l2[i4] = *reinterpret_cast<const f32x4_t*>(sl + r0 + 8 * i4 + 4 * half);
 #pragma unroll
                     for (int x = 0; x < NK; ++x) {
                         float p[16];
@@ -157,6 +167,7 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
                     add(32, s1, std::false_type{});
                 }
             }
+            if (step + 1 < end && wave == 0) keep_statistic(slot ^ 1, next);
             hh = nh;
             t = nt;
             slot ^= 1;

@@ -366,6 +366,56 @@ def test_prompt_offsets_past_32_bits():
     attn_ref.check(w[1], (value, bound), "weights")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size,scale", [(1e20, 1 / 8), (1e19, 10.0)])
+def test_prompt_scores_below_the_range_weigh_nothing(dtype, size, scale):
+    """The first keys' scores pass -2^128, by the product or only by the scale: their rows have a statistic of
+    -infinity and weigh nothing, and the later rows do not see them."""
+    gone, n = 100, 300
+    g = torch.Generator().manual_seed(12)
+    q, k, v = (0.1 * torch.randn(n, h, 64, generator=g) for h in (2, 1, 1))
+    q[:, :, 0], k[:gone, :, 0], k[gone:, :, 0] = size, -size, 0.0
+    q, k, v = (x.to(DT[dtype]).cuda() for x in (q, k, v))
+    cu = torch.tensor([0, n], dtype=torch.int32).cuda()
+    _, lse = kda.attn_prefill_t(q, k, v, cu, scale=scale)
+    w = kda.attn_prefill_weights_t(q, k, lse, cu, weights=torch.empty(1, 1, n, device="cuda"), scale=scale)
+    torch.cuda.synchronize()
+    assert (lse[:gone] == -math.inf).all() and (w[0, 0, :gone] == 0).all()
+    value, bound = torch.zeros(n - gone, dtype=torch.float64), torch.zeros(n - gone, dtype=torch.float64)
+    for h in range(2):
+        x, y = weights_of(q[gone:, h].cpu().double(), k[gone:, 0].cpu().double(), torch.ones(n - gone, n - gone, dtype=torch.bool).tril(), scale)
+        value += x
+        bound += y + 2 * E24 * x
+    attn_ref.check(w[0, 0, gone:], (value, bound), "weights")
+
+
+def test_prompt_parts_at_once_and_replayed():
+    """A long prompt's rows go to several workgroups, with a workspace: two calls at once, and replays."""
+    q, k, v = (torch.randn(4096, h, 64, generator=torch.Generator().manual_seed(h)).bfloat16().cuda() for h in (8, 2, 3))
+    v = v[:, :2].contiguous()
+    cu = torch.tensor([0, 4000, 4096], dtype=torch.int32).cuda()
+    assert kda.attn_prefill_weights_workspace_size(2, 4096, 8, 2, 4096) > 0
+    _, lse = kda.attn_prefill_t(q, k, v, cu)
+    call = lambda rows, **kw: kda.attn_prefill_weights_t(q, k, lse, cu, weights=torch.empty(2, 2, 4096, device="cuda"), rows=rows, **kw)  # noqa: E731
+    want = [call(rows) for rows in (None, 3000)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(4):
+        for i, rows in enumerate((None, 3000)):
+            got[i].append(call(rows, stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i]) for i in range(2) for x in got[i])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = call(None)
+    for n in range(3):
+        lse.add_(0.25 * n)
+        kept.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kept, call(None)), f"replay {n}"
+
+
 def test_prompt_refusals():
     q, k, lse, cu = _prompt([20], 4, 2, 32, "f32", 1)
     w = torch.empty(1, 2, 32, device="cuda")
