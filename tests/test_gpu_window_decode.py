@@ -249,6 +249,28 @@ def test_offsets_past_32_bits():
         attn_ref.check(lse[:, h], r["lse"], "lse")
 
 
+def test_two_steps_at_once_over_one_cache():
+    """A windowed and a weighed step read one cache on two streams, each with its own workspace and outputs."""
+    c = Case([3000, 90, 700], [1, 1, 1], 100, 4, 8, 2, 64, 64, 16, "bf16", clear=False)
+    weights = torch.zeros(3, 2, c.table.shape[1] * 16, device="cuda")
+    weighed = lambda **kw: kda.attn_weighed_decode_t(c.q, c.k, c.v, c.table, c.lens, weights, **kw)  # noqa: E731
+    want, other = c.call(), weighed()
+    torch.cuda.synchronize()
+    once = weights.clone()
+    weights.zero_()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(4):
+        got.append((c.call(stream=streams[0]), weighed(stream=streams[1])))
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert all(torch.equal(a, b) for a, b in zip(x, want)) and all(torch.equal(a, b) for a, b in zip(y, other))
+    total = torch.zeros_like(once)
+    for _ in range(4):
+        total += once
+    assert torch.equal(weights, total)
+
+
 def test_torch_helper_refusals():
     c = Case([30], [1], 8, 2, 2, 1, 32, 32, 16, "f32", clear=False)
     with pytest.raises(kda.KDAError, match="window"):
