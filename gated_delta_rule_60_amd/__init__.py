@@ -9,7 +9,11 @@ kernels behind the C ABI of include/kda.h (libkda.so).
 
 The full-attention layers of a hybrid model have ``attn_prefill_t`` (and its
 backward pass), and ``attn_tree_decode_t`` over a paged cache whose pages the
-``kv_*_t`` functions keep.
+``kv_*_t`` functions keep.  Long contexts can be bounded: ``attn_window_prefill_t``
+(and its backward pass) and ``attn_window_decode_t`` see a sliding window and
+the first positions; ``attn_prefill_weights_t`` and ``attn_weighed_decode_t``
+add up the attention that each position draws, by which ``kv_evict_t`` keeps a
+budget of positions.
 
 ``import gated_delta_rule_60_amd`` does not load the library; the first call
 does, and raises if it has not been built.

@@ -10,7 +10,7 @@
 // launch turns them into weights: one read of the scores, one of w and one
 // write, against a second pass over the keys (256 sequences of 300 to 4000
 // positions, 32/8 heads of 128, bf16: 380 us; one by one under the profiler the
-// pass 361, the join 10, the weights 19).  Bound by HBM: 3.9 TB/s of keys, values
+// pass 355, the join 9, the weights 18).  Bound by HBM: 3.9 TB/s of keys, values
 // and weights.
 #include <cfloat>
 

@@ -18,9 +18,10 @@
 // workgroups, and a second launch adds their sums in order (32k tokens in 8
 // prompts, 32/8 heads of 128, every row: 1156 us in one part, 915 in six, 936 and
 // 941 in three and twelve; with a sequence's blocks following one another 850 in
-// six).  Bound by nothing alone there: 880 TFLOP/s, the matrix cores busy 40 %
-// and the vector units 57 %, two waves a SIMD that wait for their products,
-// exponentials and loads in turn.  Taking turns by hand (products of the next
+// six; 880 to 895 now, where the statistics of rows without a score are seen to
+// and the card ran slower).  Bound by nothing alone there: 840 TFLOP/s, the matrix
+// cores busy 40 % and the vector units 53 %, two waves a SIMD that wait for their
+// products, exponentials and loads in turn.  Taking turns by hand (products of the next
 // rows between the exponentials) took 877 to 928 us beside 846 to 870,
 // workgroups that stay 943 to 996 beside 849 to 856.
 #include <hip/hip_runtime.h>

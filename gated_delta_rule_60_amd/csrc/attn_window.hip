@@ -19,8 +19,8 @@
 // weight of zero would let through the mask: they turn a column of the result
 // NaN, and a workgroup that finds one walks again, looking.
 //
-// Bound, as the plain attention, by what feeds the matrix cores: 610 to 625 us,
-// 770 to 790 TFLOP/s on those 32k tokens; on 16k in 4 sequences the matrix cores
+// Bound, as the plain attention, by what feeds the matrix cores: 610 to 645 us,
+// 745 to 790 TFLOP/s on those 32k tokens; on 16k in 4 sequences the matrix cores
 // are busy 36 % and the vector units 41 % of the time.  A workgroup walks some 18
 // tiles: its look-up, first loads and last steps are a fifth of its time (read
 // from the clock: 9 of 87 thousand cycles before the first pair of tiles, 10
