@@ -94,8 +94,10 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
         };
         // As powers of two, once for all waves and keys.  A row whose scores are all below the range of fp32
         // has -infinity: from the lowest finite number they weigh nothing (-infinity less -infinity is NaN).
+        // NaN stays NaN, and so do the weights of that row (fmaxf would take the number).
         auto keep_statistic = [&](int slot, float lse) __attribute__((always_inline)) {
-            reinterpret_cast<float*>(lds[slot] + QB)[lane] = fmaxf(lse * kLog2e, -FLT_MAX);
+            const float l2 = lse * kLog2e;
+            reinterpret_cast<float*>(lds[slot] + QB)[lane] = l2 == -INFINITY ? -FLT_MAX : l2;
         };
         // this workgroup's part of them
         const int64_t all = static_cast<int64_t>(group) * (t1 - t0);

@@ -389,6 +389,80 @@ def test_prompt_scores_below_the_range_weigh_nothing(dtype, size, scale):
     attn_ref.check(w[0, 0, gone:], (value, bound), "weights")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [0, 63, 350, 640, 699])
+@pytest.mark.parametrize("lens", [[700, 40], [700, 40] + [64] * 150])
+def test_prompt_rows_that_are_not_a_number(dtype, at, lens):
+    """A NaN query: every key that its row sees is NaN, and the later ones and the other sequences keep their bits.
+    A NaN key: the rows from its own on are NaN, and with them every key of the sequence.  (A statistic of NaN
+    read as the lowest finite number gave keys an infinite weight, the heaviest.)"""
+    g = torch.Generator().manual_seed(at)
+    q, k = (torch.randn(sum(lens), h, 64, generator=g).to(DT[dtype]).cuda() for h in (2, 1))
+    cu = torch.tensor([0, *torch.tensor(lens).cumsum(0).tolist()], dtype=torch.int32).cuda()
+
+    def call(q, k):
+        _, lse = kda.attn_prefill_t(q, k, k, cu)
+        return kda.attn_prefill_weights_t(q, k, lse, cu, weights=torch.empty(len(lens), 1, 700, device="cuda")), lse
+
+    want, _ = call(q, k)
+    q2, k2 = q.clone(), k.clone()
+    q2[at, 1, 5] = k2[at, 0, 5] = float("nan")
+    got, lse = call(q2, k)
+    torch.cuda.synchronize()
+    assert torch.isnan(lse[at, 1]) and torch.isnan(lse).sum() == 1
+    assert torch.isnan(got[0, 0, :at + 1]).all()
+    assert torch.equal(got[0, 0, at + 1:], want[0, 0, at + 1:]) and torch.equal(got[1:], want[1:])
+    got, lse = call(q, k2)
+    torch.cuda.synchronize()
+    assert torch.isnan(lse[at:700]).all() and not torch.isnan(lse[:at]).any()
+    assert torch.isnan(got[0, 0]).all() and torch.equal(got[1:], want[1:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [0, 100, 300])
+def test_decode_rows_that_are_not_a_number(dtype, at):
+    """A NaN key or query: NaN for every position that the row sees, as for a prompt's; the positions behind it, the
+    other sequences and key heads keep theirs."""
+    c = Case([300, 40], 4, 2, 64, 32, 16, dtype, seed=9)
+    before = c.weights.clone()
+    c.call()
+    want = c.weights.clone()
+    k, q = c.k.clone(), c.q.clone()
+    page, row = c.rows[0][at]
+    for poison in ("key", "query"):
+        c.k.copy_(k), c.q.copy_(q), c.weights.copy_(before)
+        if poison == "key":
+            c.k[page, row, 1, 7] = float("nan")
+        else:
+            c.q[0, 3, 7] = float("nan")
+        c.call()
+        torch.cuda.synchronize()
+        assert torch.isnan(c.weights[0, 1, :301]).all(), poison
+        assert torch.equal(c.weights[0, 1, 301:], before[0, 1, 301:])
+        assert torch.equal(c.weights[0, 0], want[0, 0]) and torch.equal(c.weights[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_keys_of_minus_infinity_weigh_nothing(dtype):
+    """A key whose scores are all -infinity (an infinite element that every query meets with a positive one)."""
+    n, at = 300, 100
+    g = torch.Generator().manual_seed(3)
+    q, k = (torch.randn(n, h, 64, generator=g).to(DT[dtype]).cuda() for h in (2, 1))
+    q[:, :, 5], k[at, 0, 5] = 1.0, -math.inf
+    _, lse = kda.attn_prefill_t(q, k, k[..., 32:].contiguous())
+    w = kda.attn_prefill_weights_t(q, k, lse, weights=torch.empty(1, 1, n, device="cuda"))
+    c = Case([n], 2, 1, 64, 32, 16, dtype, seed=4)
+    c.weights.zero_()
+    c.q[..., 5] = 1.0
+    page, row = c.rows[0][at]
+    c.k[page, row, 0, 5] = -math.inf
+    c.call()
+    torch.cuda.synchronize()
+    for x, m in ((w, n), (c.weights, n + 1)):
+        assert x[0, 0, at] == 0 and x[0, 0, :m].isfinite().all()
+        assert (x[0, 0, :m] > 0).sum() == m - 1
+
+
 def test_prompt_parts_at_once_and_replayed():
     """A long prompt's rows go to several workgroups, with a workspace: two calls at once, and replays."""
     q, k, v = (torch.randn(4096, h, 64, generator=torch.Generator().manual_seed(h)).bfloat16().cuda() for h in (8, 2, 3))
