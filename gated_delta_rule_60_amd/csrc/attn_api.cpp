@@ -203,8 +203,8 @@ kda_status attn_window_prefill_backward(const void* q, const void* k, const void
     const int cus = kda::device_cus_or_default();
     const kda::WindowBwdPlan plan =
         kda::attn_window_bwd_plan(N, T_tot, H_q, H_kv, d_k, d_v, window, sinks, dtype == KDA_DTYPE_BF16, cus);
-    // the sinks' sums: one workgroup of 256 per (piece of rows, 32 sinks, key head)
-    if (plan.pieces * plan.blocks * H_kv * 256 >= kMaxItems)
+    // the sinks' sums: one workgroup of 256 per (piece of rows, 32 sinks, key head), and some for every sequence
+    if ((plan.pieces > N ? plan.pieces : N) * plan.blocks * H_kv * 256 >= kMaxItems)
         return fail(KDA_ERR_INVALID_ARG, "N * ceil(sinks / 32) * H_kv too large");
     if (workspace_bytes < plan.bytes)
         return fail(KDA_ERR_INVALID_ARG, "workspace smaller than attn_window_prefill_backward_workspace_size");
@@ -222,8 +222,8 @@ kda_status attn_window_prefill_backward(const void* q, const void* k, const void
     (void)hipGetLastError();  // report only this launch's status
     const hipError_t e = kda::launch_attn_window_bwd({{a, d_o, d_q, d_k_out, d_v_out, workspace, parts, plan.head_parts},
                                                       static_cast<int32_t>(window < T_tot ? window : T_tot), sinks, plan.rows,
-                                                      plan.blocks, static_cast<int32_t>(plan.pieces), window_heads(H_q / H_kv), sink_parts,
-                                                      band_parts},
+                                                      plan.blocks, static_cast<int32_t>(plan.pieces), window_heads(H_q / H_kv), plan.bands,
+                                                      sink_parts, band_parts},
                                                      plan);
     return e == hipSuccess ? KDA_OK : hip_fail(e, "windowed attention backward kernel launch");
 }

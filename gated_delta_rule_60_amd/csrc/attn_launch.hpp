@@ -68,14 +68,15 @@ struct WindowBwdArgs {
     int32_t blocks;     // of 32 keys that hold the sinks; 0: no row is past their window
     int32_t pieces;     // at most
     int32_t heads;      // as WindowArgs'
+    int32_t bands;      // sequences longer than the window, at most
     float* sink_parts;  // [pieces][head parts][32 blocks][Hkv][d_k + d_v]
-    float* band_parts;  // [N][32 blocks][Hkv][d_k + d_v]: what the window gives those keys (whole blocks only)
+    float* band_parts;  // [bands][32 blocks][Hkv][d_k + d_v]: what the window gives those keys (whole blocks only)
 };
 
 struct WindowBwdPlan {
     size_t stats_bytes, parts_bytes, band_bytes, bytes;
     int32_t head_parts;  // as BwdPlan's
-    int32_t rows, blocks;
+    int32_t rows, blocks, bands;
     int64_t pieces;
 };
 WindowBwdPlan attn_window_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t d_k, int32_t d_v, int32_t window,

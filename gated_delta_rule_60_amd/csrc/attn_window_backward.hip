@@ -44,6 +44,12 @@ __device__ __forceinline__ int sink_pieces(const WindowBwdArgs& w, int len) {
     return len > w.window ? (len - w.window - 1) / w.rows + 1 : 0;
 }
 
+// Where the band parts of sequence n stand, if it is longer than the window: at n if there are places for
+// all, else by its beginning (two such sequences begin more than a window apart).  Below w.bands.
+__device__ __forceinline__ int band_place(const WindowBwdArgs& w, int n, int beg) {
+    return w.b.f.N <= w.bands ? n : beg / (w.window + 1);
+}
+
 }  // namespace
 
 template <bool BF16, int DK, int DV>
@@ -309,8 +315,8 @@ __global__ __launch_bounds__(256, BF16 || DK + DV <= 128 ? 2 : 1) void attn_wind
         t = nt;
         slot ^= 1;
     }
-    if (wkey < 32 * wb.blocks) {  // the sinks' rows past the window are added later
-        float* p = wb.band_parts + ((static_cast<size_t>(st.n) * 32 * wb.blocks + kj) * a.Hkv + g) * (DK + DV);
+    if (wkey < 32 * wb.blocks && st.len > wb.window) {  // the sinks' rows past the window are added later
+        float* p = wb.band_parts + ((static_cast<size_t>(band_place(wb, st.n, st.beg)) * 32 * wb.blocks + kj) * a.Hkv + g) * (DK + DV);
         store_col_as_row<false, DK>(p, dk, a.scale, half, live);
         store_col_as_row<false, DV>(p + DK, dv, 1.f, half, live);
         return;
@@ -627,15 +633,24 @@ __global__ __launch_bounds__(256) void attn_window_join_kernel(WindowBwdArgs wb)
     const int lane = threadIdx.x & 63;
     const int g = blockIdx.x % a.Hkv;
     SeqTile st;
-    if constexpr (WHOLE) {
-        const int x = blockIdx.x / a.Hkv;
-        st.n = x / wb.blocks;
-        st.tile = x % wb.blocks;
-        const int2 bl = seq_bounds(a.cu_seqlens, st.n, a.T_tot);
-        st.beg = bl.x;
-        st.len = bl.y;
+    const int place = blockIdx.x / a.Hkv / (WHOLE ? wb.blocks : 1);
+    if constexpr (WHOLE) {  // the sequence whose band parts stand at `place`
+        st.n = -1;
+        st.tile = blockIdx.x / a.Hkv % wb.blocks;
+        for (int n0 = 0; n0 < a.N && st.n < 0; n0 += 64) {
+            int2 bl = make_int2(0, 0);
+            if (n0 + lane < a.N) bl = seq_bounds(a.cu_seqlens, n0 + lane, a.T_tot);
+            const unsigned long long m = __ballot(bl.y > wb.window && band_place(wb, n0 + lane, bl.x) == place);
+            if (m) {
+                const int n = __builtin_ctzll(m);
+                st.n = n0 + n;
+                st.beg = __builtin_amdgcn_readlane(bl.x, n);
+                st.len = __builtin_amdgcn_readlane(bl.y, n);
+            }
+        }
+        if (st.n < 0) return;
     } else {
-        if (!find_tile<32>(a.cu_seqlens, a.N, a.T_tot, blockIdx.x / a.Hkv, true, st)) return;
+        if (!find_tile<32>(a.cu_seqlens, a.N, a.T_tot, place, true, st)) return;
     }
     int first = 0, pieces = 0;  // of the sequence, among all
     if (st.tile < wb.blocks) {
@@ -659,7 +674,7 @@ __global__ __launch_bounds__(256) void attn_window_join_kernel(WindowBwdArgs wb)
         }
     };
     if constexpr (WHOLE)
-        add(wb.band_parts + ((st.n * keys + row) * a.Hkv + g) * W + e, 1, 0);
+        add(wb.band_parts + ((place * keys + row) * a.Hkv + g) * W + e, 1, 0);
     else
         add(b.parts + at * W + e, b.head_parts, static_cast<size_t>(a.T_tot) * a.Hkv * W);
     const int head_parts = WHOLE ? 1 : b.head_parts;  // of every piece
@@ -704,7 +719,7 @@ hipError_t launch(const WindowBwdArgs& w, const WindowBwdPlan& plan) {
     }
     if (whole && w.blocks > 0)
         hipLaunchKernelGGL((attn_window_join_kernel<BF16, DK, DV, true>),
-                           dim3(static_cast<unsigned>(static_cast<int64_t>(a.N) * w.blocks * a.Hkv), (DK + DV) / 32), dim3(256), 0, st, w);
+                           dim3(static_cast<unsigned>(static_cast<int64_t>(w.bands) * w.blocks * a.Hkv), (DK + DV) / 32), dim3(256), 0, st, w);
     else if (!whole && (b.head_parts > 1 || w.blocks > 0))
         hipLaunchKernelGGL((attn_window_join_kernel<BF16, DK, DV, false>), dim3(static_cast<unsigned>(units32 * a.Hkv), (DK + DV) / 32),
                            dim3(256), 0, st, w);
@@ -748,9 +763,13 @@ WindowBwdPlan attn_window_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t
         const int64_t places = cus / (p.blocks * Hkv) - N, left = T_tot - window;
         const int64_t rows = (left / (places > 1 ? places : 1) + 127) / 128 * 128;
         p.rows = static_cast<int32_t>(rows < 128 ? 128 : rows);
-        p.pieces = (T_tot - window) / p.rows + N;
+        // k sequences longer than the window have at most (T_tot - k (window + 1)) / rows + k pieces: the most with
+        // one of them or with all
+        p.bands = static_cast<int32_t>(N < T_tot / (window + 1) ? N : T_tot / (window + 1));
+        const int64_t one = (left - 1) / p.rows + 1, all = (T_tot - p.bands * (int64_t{window} + 1)) / p.rows + p.bands;
+        p.pieces = one > all ? one : all;
         p.parts_bytes = up256(static_cast<size_t>(p.pieces) * (p.head_parts > 1 ? p.head_parts : 1) * 32 * p.blocks * row);
-        if (p.head_parts == 0) p.band_bytes = up256(static_cast<size_t>(N) * 32 * p.blocks * row);
+        if (p.head_parts == 0) p.band_bytes = up256(static_cast<size_t>(p.bands) * 32 * p.blocks * row);
     }
     size_t heads = 0;
     if (p.head_parts > 1 || (p.head_parts == 1 && p.blocks > 0)) heads = up256(static_cast<size_t>(p.head_parts) * T_tot * row);

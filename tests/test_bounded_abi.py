@@ -64,6 +64,22 @@ def test_window_backward_workspace():
         assert size(*kw) == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_window_backward_workspace_of_short_sequences(dtype):
+    """What the sinks' rows take goes by the sequences that can be longer than the window, T_tot / (window + 1), not by
+    all: 4096 sequences of 64 tokens with a window of 1024 took 2.2 GB."""
+    size = kda.attn_window_prefill_backward_workspace_size
+    for n, t, window, sinks in ((4096, 4096 * 64, 1024, 4), (4096, 4096 * 64, 1024, 32), (100000, 400000, 8000, 64)):
+        plain = kda.attn_prefill_backward_workspace_size(n, t, 32, 8, 128, 128, dtype)
+        blocks, bands = (sinks + 31) // 32, t // (window + 1)
+        part = 32 * blocks * 8 * 256 * 4  # of a piece or a sequence
+        assert size(n, t, 32, 8, 128, 128, window, sinks, dtype) <= plain + part * (2 * bands + 64)
+    # one sequence can be longer than the window, however many there are
+    assert size(1000, 2000, 8, 8, 64, 64, 1500, 4, dtype) <= size(1, 2000, 8, 8, 64, 64, 1500, 4, dtype) + 2 * 32 * 8 * 128 * 4
+    # a batch of as many long ones as fit
+    assert size(16, 16 * 1025, 32, 8, 128, 128, 1024, 4, dtype) >= 16 * 2 * 32 * 8 * 256 * 4
+
+
 def _window_decode(**kw):
     a = dict(q=FAKE, k_cache=FAKE, v_cache=FAKE, block_table=FAKE, ctx_lens=FAKE, cu_q=FAKE, N=2, T_q=3, H_q=4, H_kv=2, d_k=64,
              d_v=32, n_pages=100, page_size=16, max_pages=50, q_stride=256, window=64, sinks=4, scale=0.125, dtype=BF16, o=FAKE,

@@ -85,6 +85,24 @@ def test_longer_sequences(dtype, window, sinks, hq, hkv):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window,sinks", [(200, 4), (80, 40), (75, 4), (600, 130), (2000, 4)])
+@pytest.mark.parametrize("before", [0, 37])
+def test_long_sequences_among_many_short_ones(dtype, window, sinks, before):
+    """A full batch in which few sequences have rows past their window, some of them by one, and more sequences than
+    can have any."""
+    lens = [64] * 70 + [701] + [65] * 3 + [64] * 100 + [201, 1, 0, 200, 601, 513]
+    t = sum(lens)
+    assert len(lens) > (t + before) // (window + 1)
+    q, k, v, d_o, _ = _make([before + t], 4, 2, 32, 64, dtype, window)
+    cu = torch.tensor([before, *(before + torch.tensor(lens).cumsum(0)).tolist()], dtype=torch.int32).cuda()
+    got = _run(q, k, v, d_o, cu, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    want = window_ref.prefill(q[before:], k[before:], v[before:], lens, window, sinks, 1 / math.sqrt(32), d_o[before:])
+    for name, x in zip(NAMES, got):
+        attn_ref.check(x[before:], want[name], f"{dtype} {name}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("scale,spread", [(1.0, 1.0), (1e-3, 1.0), (0.3, 3.0)])
 def test_scales(dtype, scale, spread):
     """Peaked rows (scores of tens) and flat ones."""
