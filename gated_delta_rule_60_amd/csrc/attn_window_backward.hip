@@ -748,8 +748,13 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-// Pieces of rows: so long that there is at most one workgroup for every compute unit (it holds no second
-// one), a short last piece of every sequence counted, and at least one group of 128 rows.
+// Pieces of rows: of one length, a workgroup for every compute unit (it holds no second one) if one sequence had
+// all the rows, and at least one group of 128 rows.  The length does not depend on the number of sequences, most of
+// which may have no row past their window; a short last piece of each is a small matter.  Without the forward pass,
+// 32/8 heads of 128, window 1024: 16k tokens in 4 sequences with 4 sinks 989 us, 996 with two workgroups a unit, 1015
+// with four, 990 with so many fewer pieces that the short ones fit the round too; with 256 sinks 1237, 1222 and
+// 1221, 1354 in one piece a sequence; 8192 tokens beside 31 sequences of 256, 4 sinks, 682, 670 and 674, 1163 in one
+// piece (644 without sinks).
 WindowBwdPlan attn_window_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t d_k, int32_t d_v, int32_t window,
                                    int32_t sinks, bool bf16, int cus) {
     const BwdPlan plain = attn_bwd_plan(N, T_tot, Hq, Hkv, d_k, d_v, bf16, cus);
@@ -760,12 +765,12 @@ WindowBwdPlan attn_window_bwd_plan(int32_t N, int64_t T_tot, int32_t Hq, int32_t
     if (sinks > 0 && window < T_tot) {
         const int64_t keys = sinks < T_tot ? sinks : T_tot;
         p.blocks = static_cast<int32_t>((keys + 31) / 32);
-        const int64_t places = cus / (p.blocks * Hkv) - N, left = T_tot - window;
-        const int64_t rows = (left / (places > 1 ? places : 1) + 127) / 128 * 128;
-        p.rows = static_cast<int32_t>(rows < 128 ? 128 : rows);
         // k sequences longer than the window have at most (T_tot - k (window + 1)) / rows + k pieces: the most with
         // one of them or with all
         p.bands = static_cast<int32_t>(N < T_tot / (window + 1) ? N : T_tot / (window + 1));
+        const int64_t wgs = static_cast<int64_t>(p.blocks) * Hkv, left = T_tot - window;  // workgroups of a piece
+        const int64_t share = left * wgs / cus, rows = share < left ? share : left;
+        p.rows = static_cast<int32_t>(rows < 1 ? 128 : (rows + 127) / 128 * 128);
         const int64_t one = (left - 1) / p.rows + 1, all = (T_tot - p.bands * (int64_t{window} + 1)) / p.rows + p.bands;
         p.pieces = one > all ? one : all;
         p.parts_bytes = up256(static_cast<size_t>(p.pieces) * (p.head_parts > 1 ? p.head_parts : 1) * 32 * p.blocks * row);

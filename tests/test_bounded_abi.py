@@ -80,6 +80,20 @@ def test_window_backward_workspace_of_short_sequences(dtype):
     assert size(16, 16 * 1025, 32, 8, 128, 128, 1024, 4, dtype) >= 16 * 2 * 32 * 8 * 256 * 4
 
 
+def test_window_backward_cuts_long_sequences_whatever_stands_beside_them():
+    """Pieces of the rows behind the sinks' windows, as the workspace has places for them: workgroups for at
+    least half of 256 compute units, also beside many sequences and with many sinks.  (One piece a sequence from 31
+    sequences on, or with 256 sinks from 4, left a long one's rows to 8 workgroups.)"""
+    for n, t, sinks in ((32, 8192 + 31 * 256, 4), (32, 8192 + 31 * 256, 64), (4, 16214, 64), (4, 16214, 256), (64, 40000, 4)):
+        plain = kda.attn_prefill_backward_workspace_size(n, t, 32, 8, 128, 128, BF16)
+        blocks, bands = (sinks + 31) // 32, min(n, t // 1025)
+        part = 32 * blocks * 8 * 256 * 4
+        pieces = (kda.attn_window_prefill_backward_workspace_size(n, t, 32, 8, 128, 128, 1024, sinks, BF16) - plain) // part - bands
+        assert pieces >= 256 // (blocks * 8) // 2, (n, t, sinks, pieces)
+    # the largest numbers: no overflow on the way
+    assert kda.attn_window_prefill_backward_workspace_size(1, 1 << 30, 4096, 4096, 32, 32, 1, 256, BF16) > 0
+
+
 def _window_decode(**kw):
     a = dict(q=FAKE, k_cache=FAKE, v_cache=FAKE, block_table=FAKE, ctx_lens=FAKE, cu_q=FAKE, N=2, T_q=3, H_q=4, H_kv=2, d_k=64,
              d_v=32, n_pages=100, page_size=16, max_pages=50, q_stride=256, window=64, sinks=4, scale=0.125, dtype=BF16, o=FAKE,

@@ -103,6 +103,13 @@ def test_long_sequences_among_many_short_ones(dtype, window, sinks, before):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,sinks", [([100] * 90 + [3000, 1, 1500], 40), ([2200, 1700] + [131] * 60, 4), ([2600] * 5, 100)])
+def test_many_pieces_of_a_full_batch(dtype, lens, sinks):
+    """Whole blocks, and several pieces of a sequence's rows behind the sinks' window to join."""
+    _check_all(lens, 8, 4, 64, 128, dtype, sinks, 256, sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("scale,spread", [(1.0, 1.0), (1e-3, 1.0), (0.3, 3.0)])
 def test_scales(dtype, scale, spread):
     """Peaked rows (scores of tens) and flat ones."""
