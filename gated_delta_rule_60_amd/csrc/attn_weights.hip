@@ -18,8 +18,8 @@
 // workgroups, and a second launch adds their sums in order (32k tokens in 8
 // prompts, 32/8 heads of 128, every row: 1156 us in one part, 915 in six, 936 and
 // 941 in three and twelve; with a sequence's blocks following one another 850 in
-// six; 880 to 895 now, where the statistics of rows without a score are seen to
-// and the card ran slower).  Bound by nothing alone there: 840 TFLOP/s, the matrix
+// six; with the statistics of rows without a score seen to 880, and 852 where the
+// parts look their blocks of keys up, in turn).  Bound by nothing alone there: 840 TFLOP/s, the matrix
 // cores busy 40 % and the vector units 53 %, two waves a SIMD that wait for their
 // products, exponentials and loads in turn.  Taking turns by hand (products of the next
 // rows between the exponentials) took 877 to 928 us beside 846 to 870,
@@ -29,8 +29,7 @@
 #include <cfloat>
 #include <type_traits>
 
-#include "attn_device.hpp"
-#include "attn_launch.hpp"
+#include "attn_window.hpp"
 
 namespace kda {
 
@@ -56,13 +55,22 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = a.Hq / a.Hkv;
-    // a sequence's blocks of keys follow one another, the key heads of a block side by side
-    const int KBn = (wa.width + kBK - 1) / kBK;
-    const int g = blockIdx.x % a.Hkv, n = blockIdx.x / a.Hkv / KBn;
-    const int key0 = static_cast<int>(blockIdx.x / a.Hkv % KBn) * kBK, wkey = key0 + kKeys * wave;
-    const int2 bl = seq_bounds(a.cu_seqlens, n, a.T_tot);
-    const int beg = bl.x, len = bl.y;
-    if (wa.parts > 1 && key0 >= len) return;
+    // A sequence's blocks of keys follow one another, the key heads of a block side by side: in several parts the
+    // blocks that there are, found among the sequences; in one all blocks of the width, whose zeros are written here.
+    const int g = blockIdx.x % a.Hkv;
+    SeqTile st;
+    if (wa.parts > 1) {
+        if (!find_window_tile(a.cu_seqlens, a.N, a.T_tot, kBK, blockIdx.x / a.Hkv, st) || st.tile * kBK >= wa.width) return;
+    } else {
+        const int KBn = (wa.width + kBK - 1) / kBK;
+        st.n = blockIdx.x / a.Hkv / KBn;
+        st.tile = static_cast<int>(blockIdx.x / a.Hkv % KBn);
+        const int2 bl = seq_bounds(a.cu_seqlens, st.n, a.T_tot);
+        st.beg = bl.x;
+        st.len = bl.y;
+    }
+    const int key0 = st.tile * kBK, wkey = key0 + kKeys * wave;
+    const int n = st.n, beg = st.beg, len = st.len;
 
     // A tile's weights are summed by themselves and added with what the sum before has lost to rounding
     // (compensated): one number takes thousands of rows of every head.
@@ -213,7 +221,11 @@ hipError_t launch(const WeightsArgs& w) {
     const AttnArgs& a = w.f;
     const unsigned blocks = static_cast<unsigned>((w.width + kBK - 1) / kBK) * a.N * a.Hkv;
     const hipStream_t st = static_cast<hipStream_t>(a.stream);
-    hipLaunchKernelGGL((attn_weights_kernel<BF16, DK>), dim3(blocks, w.parts), dim3(64 * kWaves), 0, st, w, a.scale * kLog2e);
+    // blocks of 256 keys that there can be (4000 tokens, 32/8 heads of 128, a table of 131072 positions: 122 us, 174
+    // with the blocks of the width for every part; 16 prompts of 500 in one of 32768: 81 and 251)
+    const int64_t there = (static_cast<int64_t>(a.T_tot) / kBK + a.N) * a.Hkv;
+    hipLaunchKernelGGL((attn_weights_kernel<BF16, DK>), dim3(w.parts > 1 ? static_cast<unsigned>(there) : blocks, w.parts), dim3(64 * kWaves), 0,
+                       st, w, a.scale * kLog2e);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || w.parts == 1) return e;
     hipLaunchKernelGGL(attn_weights_join_kernel, dim3(blocks), dim3(256), 0, st, w);

@@ -1,5 +1,6 @@
 // attn_window.hpp -- which keys a row of windowed attention sees, by row, by
-// tile and by block of rows; shared by the forward and the backward kernels.
+// tile and by block of rows; shared by the forward and the backward kernels
+// (the look-up of a piece also by attn_weights.hip).
 #pragma once
 
 #include "attn_device.hpp"

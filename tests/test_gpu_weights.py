@@ -463,6 +463,15 @@ def test_keys_of_minus_infinity_weigh_nothing(dtype):
         assert (x[0, 0, :m] > 0).sum() == m - 1
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", [700, 2100, 70000])
+def test_prompt_parts_of_many_sequences(dtype, width):
+    """Rows in parts, more sequences than a look-up's round, and a table narrower and much wider than they are."""
+    lens = [40] * 70 + [0, 1, 2100, 300]
+    assert kda.attn_prefill_weights_workspace_size(len(lens), sum(lens), 8, 2, sum(lens)) > 0
+    _check_prompt(lens, 8, 2, 64, dtype, width=width, seed=3)
+
+
 def test_prompt_parts_at_once_and_replayed():
     """A long prompt's rows go to several workgroups, with a workspace: two calls at once, and replays."""
     q, k, v = (torch.randn(4096, h, 64, generator=torch.Generator().manual_seed(h)).bfloat16().cuda() for h in (8, 2, 3))
