@@ -597,8 +597,9 @@ kda_status kv_evict(int32_t* block_table, int32_t* lens, int32_t* held, int32_t*
     if (static_cast<int64_t>(n) * n_layers * H_kv * 1024 >= kMaxItems)
         return fail(KDA_ERR_INVALID_ARG, "n * n_layers * H_kv too large");
     if (overlap(status, n, rows, n) || overlap(status, n, lens, n_rows) || overlap(status, n, held, n_rows) ||
-        overlap(status, n, refs, n_pages) || overlap(status, n, block_table, static_cast<int64_t>(n_rows) * max_pages))
-        return fail(KDA_ERR_INVALID_ARG, "status must not lie in rows or the bookkeeping: other workgroups read them");
+        overlap(status, n, refs, n_pages) || overlap(status, n, block_table, static_cast<int64_t>(n_rows) * max_pages) ||
+        overlap(status, n, free_list, n_pages) || overlap(status, n, n_free, 1))
+        return fail(KDA_ERR_INVALID_ARG, "status must not lie in rows or the bookkeeping: they are read after it is written");
     (void)hipGetLastError();
     const hipError_t e = kda::launch_kv_evict({block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size,
                                                __builtin_ctz(page_size), max_pages, stream}, c,

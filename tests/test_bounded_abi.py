@@ -246,3 +246,10 @@ def _evict(**kw):
 def test_evict_refuses(kw, status, needle):
     assert _evict(**kw) == status
     assert needle in kda.kda_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(n_free=FAKE + (5 << 20)), dict(n_free=FAKE + (5 << 20) + 12), dict(free_list=FAKE + (5 << 20) - 396)])
+def test_evict_refuses_a_status_over_the_free_pages(kw):
+    """The pages are given back by a second launch, which reads their number and list after status is written."""
+    assert _evict(**kw) == BAD
+    assert "status" in kda.kda_last_error()
