@@ -253,3 +253,21 @@ def test_evict_refuses_a_status_over_the_free_pages(kw):
     """The pages are given back by a second launch, which reads their number and list after status is written."""
     assert _evict(**kw) == BAD
     assert "status" in kda.kda_last_error()
+
+
+@pytest.mark.parametrize("call,kw,name", [
+    (_prefill, dict(window=(1 << 32) + 5), "window"), (_prefill, dict(sinks=1 << 32), "sinks"),
+    (_backward, dict(window=(1 << 32) + 5), "window"), (_window_decode, dict(window=(1 << 32) + 5), "window"),
+    (_window_decode, dict(sinks=-(1 << 32)), "sinks"), (_weights, dict(rows=(1 << 32) + 1), "rows"),
+    (_weights, dict(width=(1 << 32) + 64), "width"), (_evict, dict(budget=(1 << 32) + 64), "budget"),
+    (_evict, dict(recent=(1 << 32) + 16), "recent"), (_evict, dict(sinks=1 << 40), "sinks")])
+def test_numbers_past_32_bits_are_not_cut(call, kw, name):
+    """ctypes takes the lowest 32 bits of a number: a window of 2^32 + 5 would have been one of 5."""
+    with pytest.raises(ValueError, match=name):
+        call(**kw)
+
+
+def test_workspaces_of_numbers_past_32_bits():
+    assert kda.attn_window_prefill_backward_workspace_size(1, 1000, 4, 2, 64, 64, (1 << 32) + 5, 4, BF16) == 0
+    assert kda.attn_window_decode_workspace_size(1, 1, 4, 2, 64, 16, 100, 64, 1 << 32) == 0
+    assert kda.attn_prefill_weights_workspace_size(1, 4000, 8, 2, (1 << 32) + 4000) == 0

@@ -472,6 +472,15 @@ def test_prompt_parts_of_many_sequences(dtype, width):
     _check_prompt(lens, 8, 2, 64, dtype, width=width, seed=3)
 
 
+def test_prompt_more_rows_than_there_are():
+    """All of them, whatever the number."""
+    q, k, lse, cu = _prompt([300, 40], 4, 2, 64, "bf16", 3)
+    call = lambda **kw: kda.attn_prefill_weights_t(q, k, lse, cu, weights=torch.empty(2, 2, 320, device="cuda"), **kw)  # noqa: E731
+    want = call()
+    for rows in (340, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 7, 10 ** 15):
+        assert torch.equal(call(rows=rows), want), rows
+
+
 def test_prompt_parts_at_once_and_replayed():
     """A long prompt's rows go to several workgroups, with a workspace: two calls at once, and replays."""
     q, k, v = (torch.randn(4096, h, 64, generator=torch.Generator().manual_seed(h)).bfloat16().cuda() for h in (8, 2, 3))
