@@ -341,7 +341,7 @@ __global__ __launch_bounds__(kNT) void kv_evict_kernel(PageArgs a, CacheArgs c, 
 
 // The pages behind the budget go back, in the order of the requests and of the rows' pages.
 __global__ __launch_bounds__(kThreads) void kv_evict_pages_kernel(PageArgs a, int budget, const int32_t* rows, int n, const int32_t* status) {
-    __shared__ int s_row[kThreads], s_need[kThreads];
+    __shared__ int s_row[kThreads];
     __shared__ int64_t s_upto[kThreads], s_wave[kThreads / 64];
     const int i = threadIdx.x;
     int row = -1, give = 0;
