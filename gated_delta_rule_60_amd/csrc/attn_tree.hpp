@@ -719,7 +719,10 @@ template <bool BF16, int DV, int CG, TreeMode M>
 hipError_t launch_join(TreeArgs a, const TreePlan& p) {
     constexpr int rows = 256 / (DV / 4) / CG;  // of a workgroup
     const int sets = (p.rows + rows - 1) / rows;
-    // at least so many workgroups a compute unit: a window's sequences hardly ever have chunks to join
+    // at least so many workgroups a compute unit: a window's sequences hardly ever have chunks to join (256 sequences,
+    // 32/8 heads, window 1024: 183.7 us, with eight 188.3, with one head a workgroup 195; 512 of 400 positions 221, 227,
+    // 265), the others' do (weighed, 256 sequences of 300 to 4000: 379.8, with two 383.8, with one head 385.5; 512 of 400:
+    // 318, 314, 340)
     const int least = M == TreeMode::kWindow ? 2 : 8;
     if (M != TreeMode::kTree && CG == 1)
         while (a.Hkv % (2 * a.join_heads) == 0 && p.tiles * sets * a.Hkv / (2 * a.join_heads) >= least * p.cus) a.join_heads *= 2;

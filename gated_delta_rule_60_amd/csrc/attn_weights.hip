@@ -19,11 +19,12 @@
 // prompts, 32/8 heads of 128, every row: 1156 us in one part, 915 in six, 936 and
 // 941 in three and twelve; with a sequence's blocks following one another 850 in
 // six; with the statistics of rows without a score seen to 880, and 852 where the
-// parts look their blocks of keys up, in turn).  Bound by nothing alone there: 840 TFLOP/s, the matrix
-// cores busy 40 % and the vector units 53 %, two waves a SIMD that wait for their
-// products, exponentials and loads in turn.  Taking turns by hand (products of the next
-// rows between the exponentials) took 877 to 928 us beside 846 to 870,
-// workgroups that stay 943 to 996 beside 849 to 856.
+// parts look their blocks of keys up, in turn; 811 to 850 among calls, 880 to 920
+// TFLOP/s).  What bounds it there is open: the matrix cores are busy 43 % and the
+// vector units 57 % of the time, which add up to all of it, with 2.4 waves a SIMD
+// of the three that fit.  Taking turns by hand (products of the next rows between
+// the exponentials) took 877 to 928 us beside 846 to 870, workgroups that stay 943
+// to 996 beside 849 to 856.
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -245,7 +246,11 @@ hipError_t launch_dk(const WeightsArgs& w) {
 
 // Parts that the rows of a block of keys go to.  The first keys of a long sequence have all its rows: one
 // workgroup's chain of them is longer than the whole launch should take, and few blocks leave compute
-// units idle.
+// units idle.  24 workgroups a unit, whose chains differ (32/8 heads of 128, 32k tokens in 8 prompts: 825 us, 889
+// with 12, 836 with 48; one of 4000: 99.6, 95.9, 99.2; 4 of 4096, 16/16 heads of 64: 130, 125, 153), in parts of
+// eight tiles at least (32k tokens, the last 256 rows: 111 us, 119 with two, 123 with 16; one of 4000: 99.5, 108,
+// 96; one of 2000, 4/4 heads: 17, 14, 25), and 64 parts at most (8000 tokens, 8/1 heads: 121 us, 131 with 32 and
+// with 128, 124 with 16).
 int32_t attn_weights_parts(int32_t N, int64_t T_tot, int32_t Hq, int32_t Hkv, int32_t rows, int cus) {
     const int64_t blocks = (T_tot / kBK + N) * Hkv;
     const int64_t steps = (Hq / Hkv) * (((rows < T_tot ? rows : T_tot) + 63) / 64);  // of the longest chain, at most

@@ -17,9 +17,9 @@
 // pieces give the sinks to what their window gave.
 //
 // Bound by what feeds the matrix cores (16k tokens in 4 sequences, 32/8 heads
-// of 128, bf16, window 1024: forward and backward 1.32 to 1.37 ms; one by one under
-// the profiler forward 0.36, dq 0.47, 44 % busy, dk/dv 0.61, 41 % busy, its waves waiting half of their time, the sinks' pieces 0.07, the join
-// 0.005).
+// of 128, bf16, window 1024: forward and backward 1.30 to 1.35 ms; one by one
+// under the profiler forward 0.31, dq 0.40, 44 % busy, dk/dv 0.52, 41 % busy,
+// its waves waiting half of their time, the sinks' pieces 0.06, the join 0.006).
 #include <hip/hip_runtime.h>
 
 #include "attn_window.hpp"

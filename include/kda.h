@@ -505,7 +505,8 @@ kda_status attn_window_prefill(const void* q, const void* k, const void* v, cons
  * attn_prefill_backward's formulas over the pairs that are seen, from the
  * forward's o and lse of the same window and sinks.  Sums and roundings as
  * there; N * ceil(sinks / 32) * H_kv and the device's compute units must
- * together number less than 2^24.
+ * together number less than 2^24.  The rows behind the sinks' windows are
+ * summed in pieces whose length goes by T_tot, H_kv and sinks.
  *   workspace  at least attn_window_prefill_backward_workspace_size bytes,
  *   256-byte aligned, used until the queued work ends.
  */
@@ -520,7 +521,8 @@ kda_status attn_window_prefill_backward(const void* q, const void* k, const void
 /* Workspace bytes attn_window_prefill_backward needs on the current device (0
  * for unsupported sizes): two floats per row and query head, for small batches
  * the parts of d_k and d_v that different query heads give, and what pieces of
- * the rows past the window give the sinks. */
+ * the rows past the window give the sinks (of the sequences that can have such
+ * rows, at most T_tot / (window + 1)). */
 size_t attn_window_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int32_t H_q, int32_t H_kv,
                                                    int32_t d_k, int32_t d_v, int32_t window,
                                                    int32_t sinks, kda_dtype dtype);
@@ -543,7 +545,9 @@ size_t attn_window_prefill_backward_workspace_size(int32_t N, int64_t T_tot, int
  *   width      in [1, 2^30], with ceil(width / 256) * N * H_kv < 2^24
  *   workspace  at least attn_prefill_weights_workspace_size bytes (NULL if 0),
  *              256-byte aligned, used until the queued work ends
- * Sums are fp32, in one order: the same inputs give the same bits.
+ * Sums are fp32, in one order: the same inputs give the same bits.  A row whose
+ * lse is -infinity weighs nothing; one whose lse is NaN gives NaN to every
+ * position it sees.
  */
 kda_status attn_prefill_weights(const void* q, const void* k, const float* lse,
                                 const int32_t* cu_seqlens, int32_t N, int64_t T_tot, int32_t H_q,
@@ -656,7 +660,8 @@ size_t attn_window_decode_workspace_size(int32_t N, int64_t T_q, int32_t H_q, in
  *   weights    device [N, H_kv, max_pages * page_size] float32, read and
  *              written up to the token's own position (later ones stay); zero
  *              for positions that have not been weighed yet.  The weight of a
- *              position without a page is zero.
+ *              position without a page is zero.  An lse of -infinity or NaN: as
+ *              for attn_prefill_weights.
  *   lse        may be NULL
  *   workspace  at least attn_weighed_decode_workspace_size bytes, 256-byte
  *              aligned, used until the queued work ends
