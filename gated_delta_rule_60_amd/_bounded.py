@@ -14,15 +14,14 @@ from ._attn import (KVPages, _cache_shape, _gpu, _layers, _need, _on_stream, _pa
 from ._lib import _check, _dtype_code, load
 
 
-def _fits(*values) -> bool:
-    """Whether these are what an int32 argument of the C ABI can take (ctypes would cut them to 32 bits)."""
-    return all(-(1 << 31) <= x < (1 << 31) for x in values)
+# What an int32 argument of the C ABI can take: ctypes would cut a larger number to its lowest 32 bits.  Compared in
+# place (a call is some 10 us in all).
+_LEAST, _MOST = -(1 << 31), (1 << 31) - 1
 
 
-def _int32(**values) -> None:
-    for name, x in values.items():
-        if not _fits(x):
-            raise ValueError(f"{name} does not fit in 32 bits: {x}")
+def _too_large(**values):
+    name, x = next((n, x) for n, x in values.items() if not _LEAST <= x <= _MOST)
+    raise ValueError(f"{name} does not fit in 32 bits: {x}")
 
 
 # ---------------------------------------------------------------------------
@@ -30,7 +29,8 @@ def _int32(**values) -> None:
 # ---------------------------------------------------------------------------
 def attn_window_prefill(q, k, v, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_stride, k_stride, v_stride, window, sinks,
                         scale, dtype, o, lse, stream) -> int:
-    _int32(window=window, sinks=sinks)
+    if not (_LEAST <= window <= _MOST and _LEAST <= sinks <= _MOST):
+        _too_large(window=window, sinks=sinks)
     return load().attn_window_prefill(q, k, v, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_stride, k_stride, v_stride,
                                       window, sinks, scale, dtype, o, lse, stream)
 
@@ -38,28 +38,30 @@ def attn_window_prefill(q, k, v, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_st
 def attn_window_prefill_backward(q, k, v, o, lse, d_o, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_stride, k_stride,
                                  v_stride, window, sinks, scale, dtype, d_q, d_k_out, d_v_out, workspace,
                                  workspace_bytes, stream) -> int:
-    _int32(window=window, sinks=sinks)
+    if not (_LEAST <= window <= _MOST and _LEAST <= sinks <= _MOST):
+        _too_large(window=window, sinks=sinks)
     return load().attn_window_prefill_backward(q, k, v, o, lse, d_o, cu_seqlens, N, T_tot, H_q, H_kv, d_k, d_v, q_stride,
                                                k_stride, v_stride, window, sinks, scale, dtype, d_q, d_k_out, d_v_out,
                                                workspace, workspace_bytes, stream)
 
 
 def attn_window_prefill_backward_workspace_size(N, T_tot, H_q, H_kv, d_k, d_v, window, sinks, dtype) -> int:
-    if not _fits(window, sinks):
+    if not (_LEAST <= window <= _MOST and _LEAST <= sinks <= _MOST):
         return 0
     return int(load().attn_window_prefill_backward_workspace_size(N, T_tot, H_q, H_kv, d_k, d_v, window, sinks, dtype))
 
 
 def attn_window_decode(q, k_cache, v_cache, block_table, ctx_lens, cu_q, N, T_q, H_q, H_kv, d_k, d_v, n_pages, page_size,
                        max_pages, q_stride, window, sinks, scale, dtype, o, lse, workspace, workspace_bytes, stream) -> int:
-    _int32(window=window, sinks=sinks)
+    if not (_LEAST <= window <= _MOST and _LEAST <= sinks <= _MOST):
+        _too_large(window=window, sinks=sinks)
     return load().attn_window_decode(q, k_cache, v_cache, block_table, ctx_lens, cu_q, N, T_q, H_q, H_kv, d_k, d_v, n_pages,
                                      page_size, max_pages, q_stride, window, sinks, scale, dtype, o, lse, workspace,
                                      workspace_bytes, stream)
 
 
 def attn_window_decode_workspace_size(N, T_q, H_q, H_kv, d_v, page_size, max_pages, window, sinks) -> int:
-    if not _fits(window, sinks):
+    if not (_LEAST <= window <= _MOST and _LEAST <= sinks <= _MOST):
         return 0
     return int(load().attn_window_decode_workspace_size(N, T_q, H_q, H_kv, d_v, page_size, max_pages, window, sinks))
 
@@ -76,20 +78,22 @@ def attn_weighed_decode_workspace_size(N, H_q, H_kv, d_v, page_size, max_pages) 
 
 def attn_prefill_weights(q, k, lse, cu_seqlens, N, T_tot, H_q, H_kv, d_k, q_stride, k_stride, rows, scale, dtype, weights,
                          width, workspace, workspace_bytes, stream) -> int:
-    _int32(rows=rows, width=width)
+    if not (_LEAST <= rows <= _MOST and _LEAST <= width <= _MOST):
+        _too_large(rows=rows, width=width)
     return load().attn_prefill_weights(q, k, lse, cu_seqlens, N, T_tot, H_q, H_kv, d_k, q_stride, k_stride, rows, scale,
                                        dtype, weights, width, workspace, workspace_bytes, stream)
 
 
 def attn_prefill_weights_workspace_size(N, T_tot, H_q, H_kv, rows) -> int:
-    if not _fits(rows):
+    if not _LEAST <= rows <= _MOST:
         return 0
     return int(load().attn_prefill_weights_workspace_size(N, T_tot, H_q, H_kv, rows))
 
 
 def kv_evict(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages, rows, n, k_cache,
              v_cache, n_layers, H_kv, d_k, d_v, dtype, weights, budget, recent, sinks, status, stream) -> int:
-    _int32(budget=budget, recent=recent, sinks=sinks)
+    if not (_LEAST <= budget <= _MOST and _LEAST <= recent <= _MOST and _LEAST <= sinks <= _MOST):
+        _too_large(budget=budget, recent=recent, sinks=sinks)
     return load().kv_evict(block_table, lens, held, refs, free_list, n_free, n_rows, n_pages, page_size, max_pages, rows, n,
                            k_cache, v_cache, n_layers, H_kv, d_k, d_v, dtype, weights, budget, recent, sinks, status, stream)
 
