@@ -39,11 +39,22 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kKeys = 64;             // of a wave
 constexpr int kBK = kKeys * kWaves;   // of a workgroup
+constexpr int kStrip = 4096;          // positions that a workgroup clears
+
+// The blocks of keys that workgroups are launched for.
+enum class KeyBlocks {
+    kWidth,         // of the width, in one part or several
+    kThere,         // those that there are, looked up, in one part; a second row of the grid clears what lies behind
+    kThereInParts,  // the same in several parts (the join writes what lies behind)
+};
 
 }  // namespace
 
-template <bool BF16, int DK>
-__global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, float c /* scale log2(e) */) {
+// In parts and looked up, the compiler is held to the registers of three waves a SIMD, which it takes by itself by
+// the width (32k tokens, every row: 847 us, 882 with two waves).  Not in one part, where a chain is short and its
+// first loads count (the last 64 rows of 4000: 22 us, 25 with three).
+template <bool BF16, int DK, KeyBlocks B>
+__global__ __launch_bounds__(256, B == KeyBlocks::kThereInParts && DK * (BF16 ? 2 : 4) <= 256 ? 3 : 2) void attn_weights_kernel(WeightsArgs wa, float c /* scale log2(e) */) {
     using Op = AttnOp<BF16>;
     using QT = AttnTile<BF16, DK>;
     using G = typename Op::G;
@@ -56,11 +67,20 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = a.Hq / a.Hkv;
-    // A sequence's blocks of keys follow one another, the key heads of a block side by side: in several parts the
-    // blocks that there are, found among the sequences; in one all blocks of the width, whose zeros are written here.
     const int g = blockIdx.x % a.Hkv;
+    if (B == KeyBlocks::kThere && blockIdx.y == 1) {  // the zeros behind a sequence's last block of keys
+        const int strips = (wa.width + kStrip - 1) / kStrip, n = blockIdx.x / a.Hkv / strips;
+        if (n >= a.N) return;
+        const int len = seq_bounds(a.cu_seqlens, n, a.T_tot).y, there = (len + kBK - 1) / kBK * kBK;
+        float* w = wa.weights + (static_cast<size_t>(n) * a.Hkv + g) * wa.width;
+        const int j0 = static_cast<int>(blockIdx.x / a.Hkv % strips) * kStrip;
+#pragma unroll 1
+        for (int j = (j0 > there ? j0 : there) + threadIdx.x; j < wa.width && j < j0 + kStrip; j += 64 * kWaves) w[j] = 0.f;
+        return;
+    }
+    // a sequence's blocks of keys follow one another, the key heads of a block side by side
     SeqTile st;
-    if (wa.parts > 1) {
+    if constexpr (B != KeyBlocks::kWidth) {
         if (!find_window_tile(a.cu_seqlens, a.N, a.T_tot, kBK, blockIdx.x / a.Hkv, st) || st.tile * kBK >= wa.width) return;
     } else {
         const int KBn = (wa.width + kBK - 1) / kBK;
@@ -72,11 +92,13 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
     }
     const int key0 = st.tile * kBK, wkey = key0 + kKeys * wave;
     const int n = st.n, beg = st.beg, len = st.len;
+    const int parts = B == KeyBlocks::kThere ? 1 : wa.parts, part = B == KeyBlocks::kThere ? 0 : blockIdx.y;
+    if (B == KeyBlocks::kWidth && parts > 1 && key0 >= len) return;
 
     // A tile's weights are summed by themselves and added with what the sum before has lost to rounding
     // (compensated): one number takes thousands of rows of every head.
     float sum[NK] = {}, lost[NK] = {};
-    if (key0 < len) {
+    if (B != KeyBlocks::kWidth || key0 < len) {
         typename Op::Row k[NK][QT::NF];
 #pragma unroll
         for (int x = 0; x < NK; ++x) {
@@ -110,7 +132,7 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
         };
         // this workgroup's part of them
         const int64_t all = static_cast<int64_t>(group) * (t1 - t0);
-        const int begin = static_cast<int>(all * blockIdx.y / wa.parts), end = static_cast<int>(all * (blockIdx.y + 1) / wa.parts);
+        const int begin = static_cast<int>(all * part / parts), end = static_cast<int>(all * (part + 1) / parts);
         int hh = begin / (t1 - t0), t = t0 + begin % (t1 - t0), slot = 0;
         if (begin < end) {
             if (wave == 0) keep_statistic(0, statistic(hh, t));
@@ -190,8 +212,8 @@ __global__ __launch_bounds__(256, 2) void attn_weights_kernel(WeightsArgs wa, fl
         const int kj = wkey + 32 * x + (lane & 31);
         const float y = half_sum(sum[x]);
         if (half != 0) continue;
-        if (wa.parts > 1) {
-            if (kj < len) wa.part[(static_cast<size_t>(blockIdx.y) * a.Hkv + g) * a.T_tot + beg + kj] = y;
+        if (parts > 1) {
+            if (kj < len) wa.part[(static_cast<size_t>(part) * a.Hkv + g) * a.T_tot + beg + kj] = y;
         } else if (kj < wa.width) {
             wa.weights[(static_cast<size_t>(n) * a.Hkv + g) * wa.width + kj] = kj < len ? y : 0.f;
         }
@@ -220,13 +242,28 @@ namespace {
 template <bool BF16, int DK>
 hipError_t launch(const WeightsArgs& w) {
     const AttnArgs& a = w.f;
-    const unsigned blocks = static_cast<unsigned>((w.width + kBK - 1) / kBK) * a.N * a.Hkv;
     const hipStream_t st = static_cast<hipStream_t>(a.stream);
-    // blocks of 256 keys that there can be (4000 tokens, 32/8 heads of 128, a table of 131072 positions: 122 us, 174
-    // with the blocks of the width for every part; 16 prompts of 500 in one of 32768: 81 and 251)
+    const unsigned blocks = static_cast<unsigned>((w.width + kBK - 1) / kBK) * a.N * a.Hkv;
     const int64_t there = (static_cast<int64_t>(a.T_tot) / kBK + a.N) * a.Hkv;
-    hipLaunchKernelGGL((attn_weights_kernel<BF16, DK>), dim3(w.parts > 1 ? static_cast<unsigned>(there) : blocks, w.parts), dim3(64 * kWaves), 0,
-                       st, w, a.scale * kLog2e);
+    const int64_t strips = (static_cast<int64_t>(w.width) + kStrip - 1) / kStrip * a.N * a.Hkv;
+    // A workgroup for every block of keys that there can be, or for every block of the width, most of them empty where
+    // a table has room to grow (and the full ones then on few of the XCDs).  A look-up costs a round of loads for 64
+    // sequences, which many short ones pay, and in one part a kernel of more registers.  Parts, looked up and by the
+    // width, us: 32k tokens in 8 prompts, 32/8 heads of 128, in a table of 8192 positions 816 and 849, of 131072 826
+    // and 920; 4000 tokens in one of 4096 108 and 106, of 65536 103 and 125; 16 prompts of 500 in one of 32768 72 and
+    // 244; 1000 of 100, 8/1 heads, in one of 256 105 and 71, of 1024 106 and 249.  One part: the last 64 rows of the
+    // 32k tokens in a table of 16384 72 and 66, of 131072 75 and 97; of 128 prompts of 500 in one of 1536 116 and 108,
+    // of 32768 150 and 341; 4096 of 64, 8/2 heads, in one of 512 292 and 228, of 16384 777 and 2319.
+    const bool look_up = static_cast<int64_t>(blocks) * 2048 > (w.parts > 1 ? 1 : 4) * there * (2048 + a.N);
+    const float c = a.scale * kLog2e;
+    if (!look_up)
+        hipLaunchKernelGGL((attn_weights_kernel<BF16, DK, KeyBlocks::kWidth>), dim3(blocks, w.parts), dim3(64 * kWaves), 0, st, w, c);
+    else if (w.parts > 1)
+        hipLaunchKernelGGL((attn_weights_kernel<BF16, DK, KeyBlocks::kThereInParts>), dim3(static_cast<unsigned>(there), w.parts),
+                           dim3(64 * kWaves), 0, st, w, c);
+    else
+        hipLaunchKernelGGL((attn_weights_kernel<BF16, DK, KeyBlocks::kThere>), dim3(static_cast<unsigned>(there > strips ? there : strips), 2),
+                           dim3(64 * kWaves), 0, st, w, c);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || w.parts == 1) return e;
     hipLaunchKernelGGL(attn_weights_join_kernel, dim3(blocks), dim3(256), 0, st, w);

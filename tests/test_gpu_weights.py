@@ -464,12 +464,33 @@ def test_keys_of_minus_infinity_weigh_nothing(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("width", [700, 2100, 70000])
-def test_prompt_parts_of_many_sequences(dtype, width):
-    """Rows in parts, more sequences than a look-up's round, and a table narrower and much wider than they are."""
+@pytest.mark.parametrize("width", [200, 700, 2100, 70001])
+@pytest.mark.parametrize("rows", [17, None])
+def test_prompt_tables_of_many_sequences(dtype, width, rows):
+    """All rows (in parts) and few, more sequences than a look-up's round, and a table narrower and much wider than they
+    are."""
     lens = [40] * 70 + [0, 1, 2100, 300]
-    assert kda.attn_prefill_weights_workspace_size(len(lens), sum(lens), 8, 2, sum(lens)) > 0
-    _check_prompt(lens, 8, 2, 64, dtype, width=width, seed=3)
+    assert (kda.attn_prefill_weights_workspace_size(len(lens), sum(lens), 8, 2, rows or sum(lens)) > 0) == (rows is None)
+    _check_prompt(lens, 8, 2, 64, dtype, rows=rows, width=width, seed=3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", [1, 255, 4095, 4096, 4097, 8193, 12289])
+@pytest.mark.parametrize("before", [0, 30])
+def test_prompt_a_wide_table_is_zero_behind_its_sequences(dtype, width, before):
+    """Written in full, whatever stood there; rows before the first sequence do not count."""
+    lens = [256, 257, 0, 40, 511]
+    q, k, lse, _ = _prompt([before] + lens, 4, 2, 32, dtype, width)
+    cu = torch.tensor([before, *(before + torch.tensor(lens).cumsum(0)).tolist()], dtype=torch.int32).cuda()
+    guard = torch.full((5 * 2 * width + 2 * 64,), 7.0, device="cuda")
+    w = guard[64:-64].view(5, 2, width)
+    w.fill_(float("nan"))
+    kda.attn_prefill_weights_t(q, k, lse, cu, weights=w, rows=9)
+    torch.cuda.synchronize()
+    assert (guard[:64] == 7).all() and (guard[-64:] == 7).all()
+    for n, length in enumerate(lens):
+        m = min(length, width)
+        assert (w[n, :, m:] == 0).all() and (w[n, :, :m] > 0).all()
 
 
 def test_prompt_more_rows_than_there_are():
