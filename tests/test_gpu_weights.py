@@ -94,6 +94,16 @@ def test_decode_long_contexts_and_many_sequences(dtype):
         c.check_weights(before)
 
 
+def test_decode_more_positions_than_workgroups_take_at_once():
+    """Many sequences in a wide table: a row's positions go to its workgroups in turns."""
+    c = Case([random.Random(2).randrange(60) for _ in range(600)] + [6000, 4095, 4096], 8, 8, 32, 32, 64, "bf16", seed=1)
+    before = c.weights.clone()
+    c.check()
+    c.check_weights(before)
+    for n, x in enumerate(c.ctx):
+        assert torch.equal(c.weights[n, :, x + 1:], before[n, :, x + 1:])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("scale", [1.0, 1e-3])
 def test_decode_scales(dtype, scale):
