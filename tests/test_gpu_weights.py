@@ -358,6 +358,14 @@ def test_prompt_no_tokens():
     assert (w == 0).all()
 
 
+def test_prompt_no_tokens_in_a_wide_table():
+    q, k = (torch.empty(0, h, 64, device="cuda") for h in (4, 2))
+    w = kda.attn_prefill_weights_t(q, k, torch.empty(0, 4, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda"),
+                                   weights=torch.full((2, 2, 50000), 7.0, device="cuda"))
+    torch.cuda.synchronize()
+    assert (w == 0).all()
+
+
 def test_prompt_offsets_past_32_bits():
     stride, t = 1 << 16, 33000
     fused = torch.zeros(t, stride, dtype=torch.bfloat16, device="cuda")
