@@ -20,8 +20,8 @@
 // 941 in three and twelve; with a sequence's blocks following one another 850 in
 // six; with the statistics of rows without a score seen to 880, and 852 where the
 // parts look their blocks of keys up, in turn; 811 to 850 among calls, 880 to 920
-// TFLOP/s).  What bounds it there is open: the matrix cores are busy 43 % and the
-// vector units 57 % of the time, which add up to all of it, with 2.4 waves a SIMD
+// TFLOP/s).  What bounds it there is open: the matrix cores are busy 41 % and the
+// vector units 55 % of the time, which hardly overlap, with 2.4 waves a SIMD
 // of the three that fit.  Taking turns by hand (products of the next rows between
 // the exponentials) took 877 to 928 us beside 846 to 870, workgroups that stay 943
 // to 996 beside 849 to 856.
