@@ -506,7 +506,7 @@ kda_status attn_window_prefill(const void* q, const void* k, const void* v, cons
  * forward's o and lse of the same window and sinks.  Sums and roundings as
  * there; N * ceil(sinks / 32) * H_kv and the device's compute units must
  * together number less than 2^24.  The rows behind the sinks' windows are
- * summed in pieces whose length goes by T_tot, H_kv and sinks.
+ * summed in pieces whose length goes by T_tot, window, sinks and H_kv.
  *   workspace  at least attn_window_prefill_backward_workspace_size bytes,
  *   256-byte aligned, used until the queued work ends.
  */
